@@ -12,6 +12,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsa.so")
 
 SELECT_TOKEN_MAX = 1   # bsa_select_params.flags: per-token query aggregation
+ROPE_PAIRS = 1         # bsa_rope_shape.flags: rotate adjacent dimensions
+ROPE_NO_NORM = 2       # bsa_rope_shape.flags: rotation only
+CACHE_BF16, CACHE_E4M3, CACHE_E2M1 = 0, 1, 2   # bsa_cache_shape.format
 
 STATUS = {
     0: "BSA_OK", 1: "BSA_ERR_INVALID_ARG", 2: "BSA_ERR_SHAPE", 3: "BSA_ERR_UNSUPPORTED",
@@ -39,7 +42,26 @@ class VarlenShape(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("block", ctypes.c_int32)]
 
 
+class RopeShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_int32)]
+
+
+class CacheShape(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class TreeShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_draft", ctypes.c_int32), ("max_draft", ctypes.c_int32),
+                ("max_cached", ctypes.c_int32), ("hq", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
 _SP = ctypes.POINTER(Shape)
+_RP = ctypes.POINTER(RopeShape)
+_CP = ctypes.POINTER(CacheShape)
+_TP = ctypes.POINTER(TreeShape)
 _VP = ctypes.POINTER(VarlenShape)
 _PP = ctypes.POINTER(SelectParams)
 
@@ -84,6 +106,17 @@ SIGNATURES = {
                                       ctypes.c_size_t, _P, _P]),
     "bsa_decode_step": (ctypes.c_int, [_VP, _PP, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P,
                                        _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "bsa_qk_norm_rope": (ctypes.c_int, [_RP, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, _P, _P,
+                                        ctypes.c_int64, _P, ctypes.c_int64, _P]),
+    "bsa_cache_code_bytes": (ctypes.c_size_t, [_CP]),
+    "bsa_cache_scale_bytes": (ctypes.c_size_t, [_CP]),
+    "bsa_cache_write": (ctypes.c_int, [_CP, ctypes.c_int32, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P,
+                                       _P, _P, _P, _P]),
+    "bsa_cache_read": (ctypes.c_int, [_CP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                      ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "bsa_tree_workspace_bytes": (ctypes.c_size_t, [_TP, _CP]),
+    "bsa_tree_fwd": (ctypes.c_int, [_TP, _CP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                    ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "bsa_selftest_wait_timeout": (ctypes.c_int, [_P, ctypes.c_uint64, ctypes.c_int32, _P]),
     "bsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "bsa_version": (ctypes.c_int32, []),

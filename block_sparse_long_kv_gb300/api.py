@@ -25,12 +25,21 @@ __all__ = [
     "decode_workspace_bytes", "decode_select", "decode_fwd", "decode_step",
     "block_meta_fp8", "select_mask_fp8", "prefill_fwd_fp8", "prefill_dense_fwd_fp8",
     "prefill_fp8_workspace_bytes",
+    "RopeShape", "make_rope_shape", "ROPE_PAIRS", "ROPE_NO_NORM", "qk_norm_rope",
+    "CacheShape", "make_cache_shape", "CACHE_BF16", "CACHE_E4M3", "CACHE_E2M1", "cache_code_bytes",
+    "cache_scale_bytes", "alloc_cache", "cache_write", "cache_read",
+    "TreeShape", "make_tree_shape", "tree_workspace_bytes", "tree_fwd",
 ]
 
 Shape = _lib.Shape
 SelectParams = _lib.SelectParams
 SELECT_TOKEN_MAX = _lib.SELECT_TOKEN_MAX
 VarlenShape = _lib.VarlenShape
+RopeShape = _lib.RopeShape
+ROPE_PAIRS, ROPE_NO_NORM = _lib.ROPE_PAIRS, _lib.ROPE_NO_NORM
+CacheShape = _lib.CacheShape
+CACHE_BF16, CACHE_E4M3, CACHE_E2M1 = _lib.CACHE_BF16, _lib.CACHE_E4M3, _lib.CACHE_E2M1
+TreeShape = _lib.TreeShape
 
 
 def make_shape(batch: int, seq: int, hq: int, hkv: int, head_dim: int, block: int) -> Shape:
@@ -446,6 +455,163 @@ def decode_step(shape: VarlenShape, params: SelectParams, cu_seqlens, q_new, k, 
         _ptr(o, "o", torch.bfloat16, b * hq * d), _ptr(lse, "lse", torch.float32, b * hq),
         _ptr(workspace, "workspace", torch.uint8), ctypes.c_size_t(workspace.numel()),
         _ptr(dev_status, "dev_status", torch.int32), _stream(stream)))
+
+
+# ---------------------------------------------------------------- norm, rotation, paged cache, drafted tokens
+
+def _here(*named):
+    """Tensors of these entry points live on the current device: the kernels are launched there."""
+    dev = torch.cuda.current_device()
+    for t, name in named:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(t, name, tokens, heads, d):
+    """(pointer, elements between tokens) of bf16 rows [tokens, heads, d]; the tokens may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {(tokens, heads, d)}")
+    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), ctypes.c_int64(t.stride(0) if tokens > 1 else heads * d)
+
+
+def make_rope_shape(tokens: int, hq: int, hkv: int, head_dim: int, rotary_dim: int, eps: float = 1e-6,
+                    flags: int = 0) -> RopeShape:
+    return RopeShape(tokens, hq, hkv, head_dim, rotary_dim, eps, flags)
+
+
+def qk_norm_rope(shape: RopeShape, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, stream=None):
+    """bsa_qk_norm_rope: per-head norm and rotation of q [tokens, hq, d] and k [tokens, hkv, d] (bf16, any
+    stride between tokens) into q_out and k_out, which may be q and k themselves."""
+    t, d = shape.tokens, shape.head_dim
+    lib = _lib.load()
+    _here((q, "q"), (k, "k"), (q_weight, "q_weight"), (k_weight, "k_weight"), (positions, "positions"),
+          (inv_freq, "inv_freq"), (q_out, "q_out"), (k_out, "k_out"))
+    _lib.check("bsa_qk_norm_rope", lib.bsa_qk_norm_rope(
+        ctypes.byref(shape), *_rows(q, "q", t, shape.hq, d), *_rows(k, "k", t, shape.hkv, d),
+        _ptr(q_weight, "q_weight", torch.bfloat16, d), _ptr(k_weight, "k_weight", torch.bfloat16, d),
+        _ptr(positions, "positions", torch.int32, t),
+        _ptr(inv_freq, "inv_freq", torch.float32, shape.rotary_dim // 2),
+        *_rows(q_out, "q_out", t, shape.hq, d), *_rows(k_out, "k_out", t, shape.hkv, d), _stream(stream)))
+
+
+def make_cache_shape(pages: int, page: int, hkv: int, head_dim: int, format: int) -> CacheShape:
+    return CacheShape(pages, page, hkv, head_dim, format)
+
+
+def cache_code_bytes(shape: CacheShape) -> int:
+    return int(_lib.load().bsa_cache_code_bytes(ctypes.byref(shape)))
+
+
+def cache_scale_bytes(shape: CacheShape) -> int:
+    return int(_lib.load().bsa_cache_scale_bytes(ctypes.byref(shape)))
+
+
+def alloc_cache(shape: CacheShape, device="cuda") -> dict:
+    """The cache's arrays as uint8 tensors: codes "k", "v" and scales "k_scale", "v_scale" (None for bf16)."""
+    codes = cache_code_bytes(shape)
+    if codes == 0:
+        raise _lib.BsaError("bsa_cache_code_bytes", 2)
+    scales = cache_scale_bytes(shape)
+    u8 = dict(dtype=torch.uint8, device=device)
+    dims = (shape.pages, shape.hkv)
+    out = {}
+    for name in ("k", "v"):
+        out[name] = torch.empty(codes, **u8).view(*dims, shape.page, -1)
+        out[name + "_scale"] = torch.empty(scales, **u8).view(*dims, -1) if scales else None
+    return out
+
+
+def _cache(shape, cache):
+    codes, scales = cache_code_bytes(shape), cache_scale_bytes(shape)
+    if codes == 0:
+        raise _lib.BsaError("bsa_cache_code_bytes", 2)
+    _here(*((cache[n], n) for n in ("k", "k_scale", "v", "v_scale")))
+    args = []
+    for n in ("k", "v"):
+        if cache[n] is None or (scales and cache[n + "_scale"] is None):
+            raise TypeError(f"the cache lacks {n} or its scales")
+        args += [_ptr(cache[n], n, torch.uint8, codes),
+                 _ptr(cache[n + "_scale"], n + "_scale", torch.uint8, scales) if scales else None]
+    return args
+
+
+def cache_write(shape: CacheShape, k, v, slots, cache: dict, dev_status=None, stream=None):
+    """bsa_cache_write: rows k, v [tokens, hkv, d] (bf16, any stride between tokens) into their slots of the
+    cache of alloc_cache (int32 [tokens], page index * page + row; negative: left out)."""
+    t = slots.numel()
+    lib = _lib.load()
+    _here((k, "k"), (v, "v"), (slots, "slots"), (dev_status, "dev_status"))
+    _lib.check("bsa_cache_write", lib.bsa_cache_write(
+        ctypes.byref(shape), ctypes.c_int32(t), *_rows(k, "k", t, shape.hkv, shape.head_dim),
+        *_rows(v, "v", t, shape.hkv, shape.head_dim), _ptr(slots, "slots", torch.int32), *_cache(shape, cache),
+        _ptr(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+
+
+def _table(block_table, batch):
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, needs [{batch}, pages]")
+    return _ptr(block_table, "block_table", torch.int32), ctypes.c_int32(block_table.shape[1])
+
+
+def cache_read(shape: CacheShape, cu_seqlens, block_table, max_seqlen: int, cache: dict, k_out, v_out,
+               dev_status=None, stream=None):
+    """bsa_cache_read: every sequence's cached tokens, in order, as packed bf16 rows k_out, v_out
+    [total_tokens, hkv, d]."""
+    batch, total = cu_seqlens.numel() - 1, k_out.shape[0]
+    n = total * shape.hkv * shape.head_dim
+    lib = _lib.load()
+    _here((cu_seqlens, "cu_seqlens"), (block_table, "block_table"), (k_out, "k_out"), (v_out, "v_out"),
+          (dev_status, "dev_status"))
+    _lib.check("bsa_cache_read", lib.bsa_cache_read(
+        ctypes.byref(shape), ctypes.c_int32(batch), ctypes.c_int32(total), ctypes.c_int32(max_seqlen),
+        _cu(cu_seqlens, batch), *_table(block_table, batch), *_cache(shape, cache),
+        _ptr(k_out, "k_out", torch.bfloat16, n), _ptr(v_out, "v_out", torch.bfloat16, n),
+        _ptr(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+
+
+def make_tree_shape(batch: int, total_draft: int, max_draft: int, max_cached: int, hq: int,
+                    table_stride: int) -> TreeShape:
+    return TreeShape(batch, total_draft, max_draft, max_cached, hq, table_stride)
+
+
+def tree_workspace_bytes(shape: TreeShape, cache_shape: CacheShape) -> int:
+    return int(_lib.load().bsa_tree_workspace_bytes(ctypes.byref(shape), ctypes.byref(cache_shape)))
+
+
+def tree_fwd(shape: TreeShape, cache_shape: CacheShape, cu_draft, cached, block_table, parents, q, k_new, v_new,
+             cache: dict, kv_idx, kv_cnt, softmax_scale, o, lse=None, workspace=None, dev_status=None, stream=None):
+    """bsa_tree_fwd: drafted tokens q [total_draft, hq, d] over the cached tokens (of the listed pages, or of
+    all when kv_idx and kv_cnt are None) and over their own path of the draft tree (parents None: a chain).
+    ``workspace``: uint8 tensor of tree_workspace_bytes bytes (allocated here if None)."""
+    b, t, hkv, d = shape.batch, shape.total_draft, cache_shape.hkv, cache_shape.head_dim
+    lib = _lib.load()
+    if workspace is None:   # allocated on the call's stream, so that the allocator's order is that stream's
+        with torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream)
+                               else torch.cuda.ExternalStream(int(stream))):
+            workspace = torch.empty(tree_workspace_bytes(shape, cache_shape), dtype=torch.uint8, device=q.device)
+    _here(*((x, n) for x, n in ((cu_draft, "cu_draft"), (cached, "cached"), (block_table, "block_table"),
+                                (parents, "parents"), (q, "q"), (k_new, "k_new"), (v_new, "v_new"),
+                                (kv_idx, "kv_idx"), (kv_cnt, "kv_cnt"), (o, "o"), (lse, "lse"),
+                                (workspace, "workspace"), (dev_status, "dev_status"))))
+    table, stride = _table(block_table, b)
+    if stride.value != shape.table_stride:
+        raise ValueError(f"block_table has {stride.value} pages a sequence, the shape says {shape.table_stride}")
+    _lib.check("bsa_tree_fwd", lib.bsa_tree_fwd(
+        ctypes.byref(shape), ctypes.byref(cache_shape), _ptr(cu_draft, "cu_draft", torch.int32, b + 1),
+        _ptr(cached, "cached", torch.int32, b), table, _ptr(parents, "parents", torch.int32, t),
+        _ptr(q, "q", torch.bfloat16, t * shape.hq * d), _ptr(k_new, "k_new", torch.bfloat16, t * hkv * d),
+        _ptr(v_new, "v_new", torch.bfloat16, t * hkv * d), *_cache(cache_shape, cache),
+        _ptr(kv_idx, "kv_idx", torch.int32, b * hkv * shape.table_stride),
+        _ptr(kv_cnt, "kv_cnt", torch.int32, b * hkv), ctypes.c_float(softmax_scale),
+        _ptr(o, "o", torch.bfloat16, t * shape.hq * d), _ptr(lse, "lse", torch.float32, t * shape.hq),
+        _ptr(workspace, "workspace", torch.uint8), ctypes.c_size_t(workspace.numel()),
+        _ptr(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
 
 
 def selftest_wait_timeout(dev_status, limit_ns: int, ctas: int = 1, stream=None):

@@ -1,0 +1,209 @@
+// Per-head norm of queries and keys with the position rotation in the same pass.
+//
+//   y = x * w / sqrt(mean(x^2) + eps),  then pairs of y turn by p * f_i
+//
+// Every value is read once and written once, about ten operations each, so the
+// kernel is bound by HBM.  A row (one head of one token) belongs to D / 8
+// lanes, eight dimensions and one 16-byte access each; the sum of squares is a
+// butterfly over those lanes.  A warp takes whole tokens, one after another, and
+// walks the heads of a token, all of which turn by the same angles: a lane
+// computes the cosines and sines of its own dimensions once per token.  With
+// few tokens the heads of a token are spread over warps instead, so that the
+// step is one round of loads.
+//
+// The angle p * f is taken modulo one turn before any rounding: f / 2 pi as a
+// 64-bit fraction of a turn times the integer p wraps modulo 2^64, which is
+// exact, and its top 32 bits give the angle to 2^-32 of a turn at any
+// position.  The product p * f in fp32 would be off by 2^-24 p radians.
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "bsa_cache.h"
+#include "sm103_ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+__device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = lo_bf16(w[e]);
+    f[2 * e + 1] = hi_bf16(w[e]);
+  }
+}
+
+// f / 2 pi modulo one turn, in units of 2^-64 turns.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+  const double t = static_cast<double>(f) * 0.15915494309189535;
+  const double fr = t - floor(t);  // in [0, 1); exact for the |f| < 2 pi of every rotary table
+  return static_cast<uint64_t>(fr * 18446744073709551616.0);
+}
+
+// cos and sin of p times the fraction.  The reduced angle lies in [-pi, pi), where the fast sine
+// and cosine are within 2^-20; the bf16 result holds 2^-9.
+__device__ __forceinline__ void rotation(int p, uint64_t frac, float &c, float &s) {
+  const uint64_t turns = static_cast<uint64_t>(p) * frac;
+  const float a = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  c = __cosf(a);
+  s = __sinf(a);
+}
+
+// One warp: the heads [h0, h1) of a token, R = 32 / (D / 8) at a time; head h < hq is q's, the
+// others are k's.
+template <int D, bool PAIRS, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int heads_per_warp, int warps_per_token) {
+  constexpr int LPR = D / 8;      // lanes per row
+  constexpr int R = 32 / LPR;     // rows per warp step
+  constexpr int NA = PAIRS ? 4 : 8;
+  constexpr int U = 3;            // warp steps whose loads are in flight together
+  const int lane = threadIdx.x & 31;
+  const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
+  int64_t w = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const int64_t items = static_cast<int64_t>(a.tokens) * warps_per_token;
+  if (w >= items) return;
+  const int heads = a.hq + a.hkv;
+  const int sub = lane / LPR, c = lane % LPR;  // row of the step, 8-dimension chunk of the row
+  const int d0 = 8 * c;
+  const bool rot = d0 < a.rotary;
+  // half-split pairs: the partner dimensions lie rotary / 2 further on or back, whole chunks away
+  const int hc = a.rotary / 16;
+  const bool first = c < hc;
+  const int partner = !PAIRS && rot ? sub * LPR + (first ? c + hc : c - hc) : lane;
+  uint64_t frac[NA];
+#pragma unroll
+  for (int e = 0; e < NA; ++e) frac[e] = 0;
+  if (rot) {
+    const float *f = a.inv_freq + (PAIRS ? d0 / 2 : (first ? d0 : d0 - a.rotary / 2));
+#pragma unroll
+    for (int e = 0; e < NA; ++e) frac[e] = turn_fraction(__ldg(f + e));
+  }
+  // the weights of the lane's own dimensions, and of its partner's
+  const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  uint4 wq = ones, wk = ones, wqp = ones, wkp = ones;
+  if constexpr (NORM) {
+    const int dp = 8 * (partner % LPR);
+    if (a.q_weight != nullptr) {
+      wq = *reinterpret_cast<const uint4 *>(a.q_weight + d0);
+      wqp = *reinterpret_cast<const uint4 *>(a.q_weight + dp);
+    }
+    if (a.k_weight != nullptr) {
+      wk = *reinterpret_cast<const uint4 *>(a.k_weight + d0);
+      wkp = *reinterpret_cast<const uint4 *>(a.k_weight + dp);
+    }
+  }
+  for (; w < items; w += n_warps) {
+  const int64_t t = w / warps_per_token;
+  const int pos = __ldg(a.positions + t);
+  if (pos < 0) continue;
+  const int h0 = static_cast<int>(w - t * warps_per_token) * heads_per_warp;
+  const int h1 = min(heads, h0 + heads_per_warp);
+  float cs[NA], sn[NA];
+#pragma unroll
+  for (int e = 0; e < NA; ++e) rotation(pos, frac[e], cs[e], sn[e]);
+  const uint16_t *qrow = a.q + t * a.q_stride + d0, *krow = a.k + t * a.k_stride + d0;
+  uint16_t *qo = a.q_out + t * a.q_out_stride + d0, *ko = a.k_out + t * a.k_out_stride + d0;
+  for (int hb = h0; hb < h1; hb += R * U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = hb + u * R + sub;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < h1)
+        raw[u] = __ldcs(reinterpret_cast<const uint4 *>(h < a.hq ? qrow + static_cast<int64_t>(h) * D
+                                                                 : krow + static_cast<int64_t>(h - a.hq) * D));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = hb + u * R + sub;
+      if (hb + u * R >= h1) break;  // warp-uniform
+      const bool is_q = h < a.hq;
+      float x[8];
+      unpack8(raw[u], x);
+      float inv = 1.f;
+      if constexpr (NORM) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        float wf[8];
+        unpack8(is_q ? wq : wk, wf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wf[e];
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = x[e];
+      if constexpr (PAIRS) {
+        if (rot) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] = x[2 * e] * cs[e] - x[2 * e + 1] * sn[e];
+            y[2 * e + 1] = x[2 * e + 1] * cs[e] + x[2 * e] * sn[e];
+          }
+        }
+      } else {
+        // the partner's raw values cross lanes (four words instead of eight) and are normed here
+        uint4 pr;
+        pr.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
+        pr.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
+        pr.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
+        pr.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
+        if (rot) {
+          float z[8];
+          unpack8(pr, z);
+          if constexpr (NORM) {
+            float wf[8];
+            unpack8(is_q ? wqp : wkp, wf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = z[e] * inv * wf[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = first ? x[e] * cs[e] - z[e] * sn[e] : x[e] * cs[e] + z[e] * sn[e];
+        }
+      }
+      if (h < h1) {
+        const uint4 out = make_uint4(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]),
+                                     ptx::pack_bf16x2(y[4], y[5]), ptx::pack_bf16x2(y[6], y[7]));
+        __stcs(reinterpret_cast<uint4 *>(is_q ? qo + static_cast<int64_t>(h) * D
+                                              : ko + static_cast<int64_t>(h - a.hq) * D), out);
+      }
+    }
+  }
+  }
+}
+
+template <int D, bool PAIRS>
+cudaError_t launch_norm(const RopeArgs &a, bool norm, cudaStream_t stream) {
+  constexpr int R = 32 / (D / 8);
+  const int heads = a.hq + a.hkv;
+  // A warp that keeps a token computes its angles once for all heads.  Below about two warps per
+  // scheduler that leaves the GPU idle, so each warp takes one step of R heads.
+  const bool spread = static_cast<int64_t>(a.tokens) < 152 * 8;
+  const int per = spread ? R : heads;
+  const int wpt = (heads + per - 1) / per;
+  const int64_t warps = static_cast<int64_t>(a.tokens) * wpt;
+  const int64_t most = 152 * 8;  // resident CTAs: 256 threads of at most 32 registers' worth of each eighth of an SM
+  const int64_t ctas = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  const int64_t grid = ctas < most ? ctas : most;
+  if (norm) rope_kernel<D, PAIRS, true><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a, per, wpt);
+  else rope_kernel<D, PAIRS, false><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a, per, wpt);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs &a, int head_dim, bool pairs, bool norm, cudaStream_t stream) {
+  if (head_dim == 64) return pairs ? launch_norm<64, true>(a, norm, stream) : launch_norm<64, false>(a, norm, stream);
+  return pairs ? launch_norm<128, true>(a, norm, stream) : launch_norm<128, false>(a, norm, stream);
+}
+
+}  // namespace bsa

@@ -433,6 +433,151 @@ bsa_status bsa_decode_step(const bsa_varlen_shape *shape, const bsa_select_param
                            bsa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Norm and rotation of queries and keys, the step before every attention here.
+ *
+ * For each token t and each head of q [tokens, hq, d] and k [tokens, hkv, d]
+ * (bf16), with w the tensor's weight (bf16 [d], null = ones):
+ *   y = x * w / sqrt(mean(x^2) + eps)         (y = x with BSA_ROPE_NO_NORM)
+ * and then the first rotary_dim dimensions are rotated in pairs by the angle
+ * positions[t] * inv_freq[i], i < rotary_dim / 2, the product of the two given
+ * numbers without rounding (positions up to 2^31 - 1 keep their angle).  Pair i
+ * is (i, i + rotary_dim / 2), or (2i, 2i + 1) with BSA_ROPE_PAIRS.  Arithmetic
+ * in fp32, one rounding to bf16.  A token whose position is negative is left
+ * out: its rows of q_out and k_out stay as they were.
+ *
+ * Strides are elements between tokens (multiples of 8, at least heads * d; the
+ * heads of a token are contiguous), so q and k may be columns of a fused
+ * projection's rows.  q_out may be q with the same stride, and k_out k; other
+ * overlaps of an output with an input or the other output are refused
+ * (BSA_ERR_INVALID_ARG).  Supported: head_dim in {64, 128}; rotary_dim a
+ * multiple of 16 in [0, head_dim] (with 0, inv_freq may be null and positions
+ * only say which tokens count); tokens >= 0 (0 launches nothing).  inv_freq:
+ * fp32 [rotary_dim / 2], finite.  positions: int32 [tokens].  eps finite, >= 0.
+ * q, k, outputs, weights 16-byte aligned; positions, inv_freq 4-byte aligned.
+ * ------------------------------------------------------------------------ */
+#define BSA_ROPE_PAIRS 1
+#define BSA_ROPE_NO_NORM 2
+
+typedef struct {
+  int32_t tokens, hq, hkv, head_dim, rotary_dim;
+  float eps;
+  int32_t flags;
+} bsa_rope_shape;
+
+bsa_status bsa_qk_norm_rope(const bsa_rope_shape *shape, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *q_weight, const void *k_weight,
+                            const int32_t *positions, const float *inv_freq, void *q_out,
+                            int64_t q_out_stride, void *k_out, int64_t k_out_stride, bsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache of keys and values in 16, 8 or 4 bits.
+ *
+ * The cache holds `pages` pages of `page` tokens, a page being a key block of
+ * the selection, K and V in two arrays each:
+ *   codes  [pages, hkv, page, row]   row = 2 d (BF16), d (E4M3), d / 2 (E2M1) bytes
+ *   scales [pages, hkv, page * s]    s = 0, 1, 1 + d / 16 bytes: of every page and
+ *                                    head the `page` row exponents, then (E2M1) the
+ *                                    group scales [page, d / 16]
+ * A token's row of one head is stored as follows (reading 17 with scales of
+ * its own for every token, so a row is final the moment it is written):
+ *   BSA_CACHE_BF16  the bf16 values
+ *   BSA_CACHE_E4M3  value = e4m3(code) * 2^(e - 127): e - 127 is the least
+ *                   integer >= -126 with max|x| <= 448 * 2^(e - 127).  A power of
+ *                   two shifts e4m3's exponent and costs no fraction bit
+ *   BSA_CACHE_E2M1  value = e2m1(code) * e4m3(group scale) * 2^(e - 127): e - 127
+ *                   the least integer >= -126 with max|x| <= 2688 * 2^(e - 127);
+ *                   a group is 16 dimensions, its scale RN(max of the group
+ *                   * 2^(127 - e) / 6), a code RN(x * 2^(127 - e) / scale)
+ *                   saturated at 6 (0 where the scale is 0); even dimensions in
+ *                   the low four bits of a byte
+ * Roundings are to nearest, ties to even.  Every held value is a bf16 value
+ * (E4M3 and E2M1 down to bf16's smallest normal times the code's own range).
+ * Supported: head_dim in {64, 128}; page in {64, 128, 256}; pages * page <
+ * 2^31.  Code and scale arrays 16-byte aligned; scale pointers are ignored (may
+ * be null) for BF16.  bsa_cache_code_bytes / bsa_cache_scale_bytes: bytes of
+ * one codes and one scales array (0 for an invalid shape).
+ *
+ * bsa_cache_write: token t's rows k[t], v[t] (bf16 [tokens, hkv, d], strides as
+ * above) into slot slots[t] = page index * page + row; a negative slot leaves
+ * the token out, one past the cache sets BSA_ERR_INVALID_ARG in *dev_status and
+ * leaves it out.  Everything else in the cache stays as it was.  The slots of
+ * one call must be distinct (two tokens in one slot leave a mix of the two).
+ *
+ * bsa_cache_read: tokens 0 .. len_b - 1 of every sequence, gathered through
+ * block_table (int32 [batch, table_stride]: entry j of sequence b is the page
+ * of its tokens j * page ..), as bf16 values into the packed k_out, v_out
+ * [total_tokens, hkv, d] at rows cu_seqlens[b] ..; what the varlen entry points
+ * take.  cu_seqlens is checked as in a packed batch (at most max_seqlen tokens
+ * a sequence, which table_stride must cover); a table entry outside the cache
+ * sets BSA_ERR_INVALID_ARG in *dev_status and leaves its rows, like those past
+ * the last sequence, as they were.
+ * ------------------------------------------------------------------------ */
+#define BSA_CACHE_BF16 0
+#define BSA_CACHE_E4M3 1
+#define BSA_CACHE_E2M1 2
+
+typedef struct {
+  int32_t pages, page, hkv, head_dim, format;
+} bsa_cache_shape;
+
+size_t bsa_cache_code_bytes(const bsa_cache_shape *shape);
+size_t bsa_cache_scale_bytes(const bsa_cache_shape *shape);
+bsa_status bsa_cache_write(const bsa_cache_shape *shape, int32_t tokens, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, const int32_t *slots, void *k_codes,
+                           void *k_scales, void *v_codes, void *v_scales, int32_t *dev_status,
+                           bsa_stream_t stream);
+bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t total_tokens,
+                          int32_t max_seqlen, const int32_t *cu_seqlens, const int32_t *block_table,
+                          int32_t table_stride, const void *k_codes, const void *k_scales,
+                          const void *v_codes, const void *v_scales, void *k_out, void *v_out,
+                          int32_t *dev_status, bsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsa_tree_fwd - attention of drafted tokens over the paged cache.
+ *
+ * Sequence b holds cached[b] tokens in the cache (pages through block_table,
+ * as above) and drafts the tokens cu_draft[b] .. cu_draft[b+1]-1 of q
+ * [total_draft, hq, d], k_new and v_new [total_draft, hkv, d] (bf16), which are
+ * not in the cache.  parents [total_draft] gives each drafted token's parent as
+ * an index within its sequence's drafts, smaller than its own, or -1 for a
+ * root; null means a chain (token i's parent is i - 1, token 0 a root).  Token
+ * t, head h attends to
+ *   - the cached tokens of the pages kv_idx[b][g][0 .. kv_cnt[b][g]-1] (int32
+ *     [batch, hkv, table_stride] and [batch, hkv], strictly ascending: the list
+ *     bsa_decode_select writes), or of all pages when both are null;
+ *   - itself and its ancestors among the drafts:
+ *   O[t][h] = sum_s softmax_s(scale * q . k_s) v_s;  lse[t][h] (fp32
+ *   [total_draft, hq], nullable) the natural log of the normaliser.
+ * The dot products use the held values exactly; softmax statistics and sums
+ * are fp32.  One drafted token is a decode step.  Rows past cu_draft[batch] are
+ * left as they were.
+ *
+ * Limits: hq % hkv == 0 with G in {1, 2, 4, 8, 16}; max_draft <= 256 drafted
+ * tokens a sequence; max_cached tokens <= 4096 pages and <= table_stride pages;
+ * batch * hkv <= 4096.  max_draft and max_cached are upper bounds that the
+ * device checks: an inconsistent cu_draft entry or cached[b] sets
+ * BSA_ERR_INVALID_ARG in *dev_status and reads as no drafts / an empty cache, a
+ * table entry outside the cache sets it and is left out, a parent that is not
+ * smaller than its token sets it and reads as -1; list entries that name no
+ * page of the sequence are left out.  workspace: bsa_tree_workspace_bytes bytes, 16-byte
+ * aligned, the caller's alone while the call runs; its contents need no
+ * initialisation and are dead afterwards.  cu_draft, cached, block_table and
+ * parents 4-byte aligned, the rest 16-byte.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch, total_draft, max_draft, max_cached, hq, table_stride;
+} bsa_tree_shape;
+
+size_t bsa_tree_workspace_bytes(const bsa_tree_shape *shape, const bsa_cache_shape *cache);
+bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cache, const int32_t *cu_draft,
+                        const int32_t *cached, const int32_t *block_table, const int32_t *parents,
+                        const void *q, const void *k_new, const void *v_new, const void *k_codes,
+                        const void *k_scales, const void *v_codes, const void *v_scales,
+                        const int32_t *kv_idx, const int32_t *kv_cnt, float softmax_scale, void *o,
+                        float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                        bsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Self-test of the device wait limits (no compute).  Launches `ctas` CTAs
  * (1..8) whose first thread waits, through the bounded wait the attention
  * kernel uses, on an mbarrier that nothing completes.  CTA 0 gives up after
