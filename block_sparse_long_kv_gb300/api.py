@@ -458,26 +458,56 @@ def decode_step(shape: VarlenShape, params: SelectParams, cu_seqlens, q_new, k, 
 
 
 # ---------------------------------------------------------------- norm, rotation, paged cache, drafted tokens
+#
+# A step's kernels take a few microseconds each, so these bindings are kept lean: every tensor is
+# checked by a handful of attribute reads and goes to ctypes as a plain address.
 
-def _here(*named):
-    """Tensors of these entry points live on the current device: the kernels are launched there."""
-    dev = torch.cuda.current_device()
-    for t, name in named:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t, name, tokens, heads, d):
-    """(pointer, elements between tokens) of bf16 rows [tokens, heads, d]; the tokens may be strided."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _stream_of(stream, dev):
+    """Address of the given stream, or of the current stream of device `dev`."""
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(t, name, dev):
+    """Refuses what is no tensor of device `dev` (the current one: the kernels are launched there)."""
+    at = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if at < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
+
+
+def _addr(t, name, dtype, numel, dev):
+    """Address of a contiguous tensor of at least numel elements; None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, name, dev)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
+    return t.data_ptr()
+
+
+def _rows(t, name, tokens, heads, d, dev):
+    """(address, elements between tokens) of bf16 rows [tokens, heads, d]; the tokens may be strided."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, name, dev)
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (tokens, heads, d):
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {(tokens, heads, d)}")
-    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    st, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), ctypes.c_int64(t.stride(0) if tokens > 1 else heads * d)
+    return t.data_ptr(), st if tokens > 1 else heads * d
 
 
 def make_rope_shape(tokens: int, hq: int, hkv: int, head_dim: int, rotary_dim: int, eps: float = 1e-6,
@@ -488,16 +518,15 @@ def make_rope_shape(tokens: int, hq: int, hkv: int, head_dim: int, rotary_dim: i
 def qk_norm_rope(shape: RopeShape, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, stream=None):
     """bsa_qk_norm_rope: per-head norm and rotation of q [tokens, hq, d] and k [tokens, hkv, d] (bf16, any
     stride between tokens) into q_out and k_out, which may be q and k themselves."""
-    t, d = shape.tokens, shape.head_dim
-    lib = _lib.load()
-    _here((q, "q"), (k, "k"), (q_weight, "q_weight"), (k_weight, "k_weight"), (positions, "positions"),
-          (inv_freq, "inv_freq"), (q_out, "q_out"), (k_out, "k_out"))
-    _lib.check("bsa_qk_norm_rope", lib.bsa_qk_norm_rope(
-        ctypes.byref(shape), *_rows(q, "q", t, shape.hq, d), *_rows(k, "k", t, shape.hkv, d),
-        _ptr(q_weight, "q_weight", torch.bfloat16, d), _ptr(k_weight, "k_weight", torch.bfloat16, d),
-        _ptr(positions, "positions", torch.int32, t),
-        _ptr(inv_freq, "inv_freq", torch.float32, shape.rotary_dim // 2),
-        *_rows(q_out, "q_out", t, shape.hq, d), *_rows(k_out, "k_out", t, shape.hkv, d), _stream(stream)))
+    t, hq, hkv, d = shape.tokens, shape.hq, shape.hkv, shape.head_dim
+    dev = torch.cuda.current_device()
+    code = _lib.load().bsa_qk_norm_rope(
+        ctypes.byref(shape), *_rows(q, "q", t, hq, d, dev), *_rows(k, "k", t, hkv, d, dev),
+        _addr(q_weight, "q_weight", torch.bfloat16, d, dev), _addr(k_weight, "k_weight", torch.bfloat16, d, dev),
+        _addr(positions, "positions", torch.int32, t, dev),
+        _addr(inv_freq, "inv_freq", torch.float32, shape.rotary_dim // 2, dev),
+        *_rows(q_out, "q_out", t, hq, d, dev), *_rows(k_out, "k_out", t, hkv, d, dev), _stream_of(stream, dev))
+    _lib.check("bsa_qk_norm_rope", code)
 
 
 def make_cache_shape(pages: int, page: int, hkv: int, head_dim: int, format: int) -> CacheShape:
@@ -513,11 +542,11 @@ def cache_scale_bytes(shape: CacheShape) -> int:
 
 
 def alloc_cache(shape: CacheShape, device="cuda") -> dict:
-    """The cache's arrays as uint8 tensors: codes "k", "v" and scales "k_scale", "v_scale" (None for bf16)."""
-    codes = cache_code_bytes(shape)
+    """The cache's arrays as uint8 tensors: codes "k", "v" [pages, hkv, page, row bytes] and scales "k_scale",
+    "v_scale" [pages, hkv, scale bytes] (None for bf16)."""
+    codes, scales = cache_code_bytes(shape), cache_scale_bytes(shape)
     if codes == 0:
         raise _lib.BsaError("bsa_cache_code_bytes", 2)
-    scales = cache_scale_bytes(shape)
     u8 = dict(dtype=torch.uint8, device=device)
     dims = (shape.pages, shape.hkv)
     out = {}
@@ -527,52 +556,56 @@ def alloc_cache(shape: CacheShape, device="cuda") -> dict:
     return out
 
 
-def _cache(shape, cache):
-    codes, scales = cache_code_bytes(shape), cache_scale_bytes(shape)
-    if codes == 0:
-        raise _lib.BsaError("bsa_cache_code_bytes", 2)
-    _here(*((cache[n], n) for n in ("k", "k_scale", "v", "v_scale")))
-    args = []
-    for n in ("k", "v"):
-        if cache[n] is None or (scales and cache[n + "_scale"] is None):
-            raise TypeError(f"the cache lacks {n} or its scales")
-        args += [_ptr(cache[n], n, torch.uint8, codes),
-                 _ptr(cache[n + "_scale"], n + "_scale", torch.uint8, scales) if scales else None]
-    return args
+def _cache(shape, cache, dev):
+    """Addresses of the cache's four arrays (no scales for bf16)."""
+    d, fmt = shape.head_dim, shape.format
+    rows = shape.pages * shape.hkv * shape.page
+    codes, scales = ((2 * d, 0), (d, 1), (d // 2, 1 + d // 16))[fmt] if 0 <= fmt <= 2 else (0, 0)
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    if k is None or v is None or (scales and (ks is None or vs is None)):
+        raise TypeError("the cache lacks codes or scales")
+    u8 = torch.uint8
+    if not scales:
+        return _addr(k, "k", u8, rows * codes, dev), None, _addr(v, "v", u8, rows * codes, dev), None
+    return (_addr(k, "k", u8, rows * codes, dev), _addr(ks, "k_scale", u8, rows * scales, dev),
+            _addr(v, "v", u8, rows * codes, dev), _addr(vs, "v_scale", u8, rows * scales, dev))
 
 
 def cache_write(shape: CacheShape, k, v, slots, cache: dict, dev_status=None, stream=None):
     """bsa_cache_write: rows k, v [tokens, hkv, d] (bf16, any stride between tokens) into their slots of the
     cache of alloc_cache (int32 [tokens], page index * page + row; negative: left out)."""
-    t = slots.numel()
-    lib = _lib.load()
-    _here((k, "k"), (v, "v"), (slots, "slots"), (dev_status, "dev_status"))
-    _lib.check("bsa_cache_write", lib.bsa_cache_write(
-        ctypes.byref(shape), ctypes.c_int32(t), *_rows(k, "k", t, shape.hkv, shape.head_dim),
-        *_rows(v, "v", t, shape.hkv, shape.head_dim), _ptr(slots, "slots", torch.int32), *_cache(shape, cache),
-        _ptr(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+    dev = torch.cuda.current_device()
+    at = _addr(slots, "slots", torch.int32, 0, dev)
+    t, hkv, d = slots.numel(), shape.hkv, shape.head_dim
+    code = _lib.load().bsa_cache_write(
+        ctypes.byref(shape), t, *_rows(k, "k", t, hkv, d, dev), *_rows(v, "v", t, hkv, d, dev), at,
+        *_cache(shape, cache, dev), _addr(dev_status, "dev_status", torch.int32, 1, dev), _stream_of(stream, dev))
+    _lib.check("bsa_cache_write", code)
 
 
-def _table(block_table, batch):
+def _table(block_table, batch, dev):
+    """(address, pages a sequence) of an int32 [batch, pages] table."""
+    at = _addr(block_table, "block_table", torch.int32, 0, dev)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table has shape {tuple(block_table.shape)}, needs [{batch}, pages]")
-    return _ptr(block_table, "block_table", torch.int32), ctypes.c_int32(block_table.shape[1])
+    return at, block_table.shape[1]
 
 
 def cache_read(shape: CacheShape, cu_seqlens, block_table, max_seqlen: int, cache: dict, k_out, v_out,
                dev_status=None, stream=None):
     """bsa_cache_read: every sequence's cached tokens, in order, as packed bf16 rows k_out, v_out
     [total_tokens, hkv, d]."""
+    dev = torch.cuda.current_device()
+    cu = _addr(cu_seqlens, "cu_seqlens", torch.int32, 2, dev)
+    _on(k_out, "k_out", dev)
     batch, total = cu_seqlens.numel() - 1, k_out.shape[0]
     n = total * shape.hkv * shape.head_dim
-    lib = _lib.load()
-    _here((cu_seqlens, "cu_seqlens"), (block_table, "block_table"), (k_out, "k_out"), (v_out, "v_out"),
-          (dev_status, "dev_status"))
-    _lib.check("bsa_cache_read", lib.bsa_cache_read(
-        ctypes.byref(shape), ctypes.c_int32(batch), ctypes.c_int32(total), ctypes.c_int32(max_seqlen),
-        _cu(cu_seqlens, batch), *_table(block_table, batch), *_cache(shape, cache),
-        _ptr(k_out, "k_out", torch.bfloat16, n), _ptr(v_out, "v_out", torch.bfloat16, n),
-        _ptr(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+    table, stride = _table(block_table, batch, dev)
+    code = _lib.load().bsa_cache_read(
+        ctypes.byref(shape), batch, total, max_seqlen, cu, table, stride, *_cache(shape, cache, dev),
+        _addr(k_out, "k_out", torch.bfloat16, n, dev), _addr(v_out, "v_out", torch.bfloat16, n, dev),
+        _addr(dev_status, "dev_status", torch.int32, 1, dev), _stream_of(stream, dev))
+    _lib.check("bsa_cache_read", code)
 
 
 def make_tree_shape(batch: int, total_draft: int, max_draft: int, max_cached: int, hq: int,
@@ -589,29 +622,27 @@ def tree_fwd(shape: TreeShape, cache_shape: CacheShape, cu_draft, cached, block_
     """bsa_tree_fwd: drafted tokens q [total_draft, hq, d] over the cached tokens (of the listed pages, or of
     all when kv_idx and kv_cnt are None) and over their own path of the draft tree (parents None: a chain).
     ``workspace``: uint8 tensor of tree_workspace_bytes bytes (allocated here if None)."""
-    b, t, hkv, d = shape.batch, shape.total_draft, cache_shape.hkv, cache_shape.head_dim
-    lib = _lib.load()
+    b, t, hq, hkv, d = shape.batch, shape.total_draft, shape.hq, cache_shape.hkv, cache_shape.head_dim
+    dev = torch.cuda.current_device()
+    i32, bf16 = torch.int32, torch.bfloat16
+    table, stride = _table(block_table, b, dev)
+    if stride != shape.table_stride:
+        raise ValueError(f"block_table has {stride} pages a sequence, the shape says {shape.table_stride}")
+    args = (_addr(cu_draft, "cu_draft", i32, b + 1, dev), _addr(cached, "cached", i32, b, dev), table,
+            _addr(parents, "parents", i32, t, dev), _addr(q, "q", bf16, t * hq * d, dev),
+            _addr(k_new, "k_new", bf16, t * hkv * d, dev), _addr(v_new, "v_new", bf16, t * hkv * d, dev),
+            *_cache(cache_shape, cache, dev), _addr(kv_idx, "kv_idx", i32, b * hkv * stride, dev),
+            _addr(kv_cnt, "kv_cnt", i32, b * hkv, dev), softmax_scale, _addr(o, "o", bf16, t * hq * d, dev),
+            _addr(lse, "lse", torch.float32, t * hq, dev))
+    status = _addr(dev_status, "dev_status", i32, 1, dev)
     if workspace is None:   # allocated on the call's stream, so that the allocator's order is that stream's
         with torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream)
                                else torch.cuda.ExternalStream(int(stream))):
             workspace = torch.empty(tree_workspace_bytes(shape, cache_shape), dtype=torch.uint8, device=q.device)
-    _here(*((x, n) for x, n in ((cu_draft, "cu_draft"), (cached, "cached"), (block_table, "block_table"),
-                                (parents, "parents"), (q, "q"), (k_new, "k_new"), (v_new, "v_new"),
-                                (kv_idx, "kv_idx"), (kv_cnt, "kv_cnt"), (o, "o"), (lse, "lse"),
-                                (workspace, "workspace"), (dev_status, "dev_status"))))
-    table, stride = _table(block_table, b)
-    if stride.value != shape.table_stride:
-        raise ValueError(f"block_table has {stride.value} pages a sequence, the shape says {shape.table_stride}")
-    _lib.check("bsa_tree_fwd", lib.bsa_tree_fwd(
-        ctypes.byref(shape), ctypes.byref(cache_shape), _ptr(cu_draft, "cu_draft", torch.int32, b + 1),
-        _ptr(cached, "cached", torch.int32, b), table, _ptr(parents, "parents", torch.int32, t),
-        _ptr(q, "q", torch.bfloat16, t * shape.hq * d), _ptr(k_new, "k_new", torch.bfloat16, t * hkv * d),
-        _ptr(v_new, "v_new", torch.bfloat16, t * hkv * d), *_cache(cache_shape, cache),
-        _ptr(kv_idx, "kv_idx", torch.int32, b * hkv * shape.table_stride),
-        _ptr(kv_cnt, "kv_cnt", torch.int32, b * hkv), ctypes.c_float(softmax_scale),
-        _ptr(o, "o", torch.bfloat16, t * shape.hq * d), _ptr(lse, "lse", torch.float32, t * shape.hq),
-        _ptr(workspace, "workspace", torch.uint8), ctypes.c_size_t(workspace.numel()),
-        _ptr(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+    code = _lib.load().bsa_tree_fwd(
+        ctypes.byref(shape), ctypes.byref(cache_shape), *args, _addr(workspace, "workspace", torch.uint8, 0, dev),
+        workspace.numel(), status, _stream_of(stream, dev))
+    _lib.check("bsa_tree_fwd", code)
 
 
 def selftest_wait_timeout(dev_status, limit_ns: int, ctas: int = 1, stream=None):

@@ -83,27 +83,19 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
                                                                     int warps_per_token) {
   constexpr int LPR = D / 8;
   constexpr int R = 32 / LPR;
-  constexpr int U = 2;  // warp steps whose loads are in flight together
+  constexpr int U = 4;  // warp steps whose loads are in flight together: a token's eight rows
   constexpr int RB = FMT == BSA_CACHE_BF16 ? 2 * D : FMT == BSA_CACHE_E4M3 ? D : D / 2;
   constexpr int PER = FMT == BSA_CACHE_BF16 ? 0 : FMT == BSA_CACHE_E4M3 ? 1 : 1 + D / 16;
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / warps_per_token;
   if (t >= a.tokens) return;
-  const int slot = __ldg(a.slots + t);
-  if (slot < 0) return;
-  const int page = slot >> a.c.page_shift, off = slot & (a.c.page - 1);
-  if (page >= a.c.pages) {
-    if (a.status != nullptr && lane == 0) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-    return;
-  }
+  const int slot = __ldg(a.slots + t);  // needed only when the first rows have arrived
   const int sub = lane / LPR, c = lane % LPR;
   const int hkv = a.c.hkv, rows = 2 * hkv;
   const int r0 = static_cast<int>(w - t * warps_per_token) * rows_per_warp;
   const int r1 = min(rows, r0 + rows_per_warp);
   const uint16_t *ks = a.k + t * a.k_stride + 8 * c, *vs = a.v + t * a.v_stride + 8 * c;
-  const size_t tile0 = static_cast<size_t>(page) * hkv;
-
   for (int rb = r0; rb < r1; rb += R * U) {
     uint4 raw[U];
 #pragma unroll
@@ -114,6 +106,13 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
         raw[u] = __ldcs(reinterpret_cast<const uint4 *>(r < hkv ? ks + static_cast<int64_t>(r) * D
                                                                 : vs + static_cast<int64_t>(r - hkv) * D));
     }
+    if (slot < 0) return;
+    const int page = slot >> a.c.page_shift, off = slot & (a.c.page - 1);
+    if (page >= a.c.pages) {
+      if (a.status != nullptr && lane == 0) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
+      return;
+    }
+    const size_t tile0 = static_cast<size_t>(page) * hkv;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = rb + u * R + sub;

@@ -26,6 +26,7 @@ namespace bsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 4;  // resident per SM
 
 __device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
@@ -56,128 +57,103 @@ __device__ __forceinline__ void rotation(int p, uint64_t frac, float &c, float &
 }
 
 // One warp: the heads [h0, h1) of a token, R = 32 / (D / 8) at a time; head h < hq is q's, the
-// others are k's.
+// others are k's.  A lane's eight dimensions are two groups of four that turn with each other:
+// half-split pairs (i, i + rotary / 2) put both in one lane, so nothing crosses lanes but the sum of
+// squares, and a lane needs four angles.  Lane c of a row holds dimensions 4c .. and rotary / 2 + 4c ..
+// while 8c < rotary, and its own eight past them; adjacent pairs are eight dimensions in a row anyway.
 template <int D, bool PAIRS, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int heads_per_warp, int warps_per_token) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeArgs a, int heads_per_warp,
+                                                                       int warps_per_token) {
   constexpr int LPR = D / 8;      // lanes per row
   constexpr int R = 32 / LPR;     // rows per warp step
-  constexpr int NA = PAIRS ? 4 : 8;
-  constexpr int U = 3;            // warp steps whose loads are in flight together
+  constexpr int U = 4;            // warp steps whose loads are in flight together
   const int lane = threadIdx.x & 31;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
   int64_t w = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
   const int64_t items = static_cast<int64_t>(a.tokens) * warps_per_token;
   if (w >= items) return;
   const int heads = a.hq + a.hkv;
-  const int sub = lane / LPR, c = lane % LPR;  // row of the step, 8-dimension chunk of the row
-  const int d0 = 8 * c;
-  const bool rot = d0 < a.rotary;
-  // half-split pairs: the partner dimensions lie rotary / 2 further on or back, whole chunks away
-  const int hc = a.rotary / 16;
-  const bool first = c < hc;
-  const int partner = !PAIRS && rot ? sub * LPR + (first ? c + hc : c - hc) : lane;
-  uint64_t frac[NA];
+  const int sub = lane / LPR, c = lane % LPR;  // row of the step, lane of the row
+  const bool rot = 8 * c < a.rotary;
+  const int da = !PAIRS && rot ? 4 * c : 8 * c;
+  const int db = !PAIRS && rot ? 4 * c + a.rotary / 2 : 8 * c + 4;
+  auto load = [&](const uint16_t *p) -> uint4 {
+    if constexpr (PAIRS) return __ldcs(reinterpret_cast<const uint4 *>(p + da));
+    const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(p + da));
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + db));
+    return make_uint4(u.x, u.y, v.x, v.y);
+  };
+  uint64_t frac[4];
 #pragma unroll
-  for (int e = 0; e < NA; ++e) frac[e] = 0;
-  if (rot) {
-    const float *f = a.inv_freq + (PAIRS ? d0 / 2 : (first ? d0 : d0 - a.rotary / 2));
-#pragma unroll
-    for (int e = 0; e < NA; ++e) frac[e] = turn_fraction(__ldg(f + e));
-  }
-  // the weights of the lane's own dimensions, and of its partner's
+  for (int e = 0; e < 4; ++e) frac[e] = rot ? turn_fraction(__ldg(a.inv_freq + 4 * c + e)) : 0;
   const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-  uint4 wq = ones, wk = ones, wqp = ones, wkp = ones;
+  uint4 wq = ones, wk = ones;
   if constexpr (NORM) {
-    const int dp = 8 * (partner % LPR);
-    if (a.q_weight != nullptr) {
-      wq = *reinterpret_cast<const uint4 *>(a.q_weight + d0);
-      wqp = *reinterpret_cast<const uint4 *>(a.q_weight + dp);
-    }
-    if (a.k_weight != nullptr) {
-      wk = *reinterpret_cast<const uint4 *>(a.k_weight + d0);
-      wkp = *reinterpret_cast<const uint4 *>(a.k_weight + dp);
-    }
+    if (a.q_weight != nullptr) wq = load(a.q_weight);
+    if (a.k_weight != nullptr) wk = load(a.k_weight);
   }
+
   for (; w < items; w += n_warps) {
-  const int64_t t = w / warps_per_token;
-  const int pos = __ldg(a.positions + t);
-  if (pos < 0) continue;
-  const int h0 = static_cast<int>(w - t * warps_per_token) * heads_per_warp;
-  const int h1 = min(heads, h0 + heads_per_warp);
-  float cs[NA], sn[NA];
+    const int64_t t = w / warps_per_token;
+    const int h0 = static_cast<int>(w - t * warps_per_token) * heads_per_warp;
+    const int h1 = min(heads, h0 + heads_per_warp);
+    const uint16_t *qrow = a.q + t * a.q_stride, *krow = a.k + t * a.k_stride;
+    uint16_t *qo = a.q_out + t * a.q_out_stride, *ko = a.k_out + t * a.k_out_stride;
+    const int pos = __ldg(a.positions + t);
+    if (pos < 0) continue;
+    float cs[4], sn[4];
 #pragma unroll
-  for (int e = 0; e < NA; ++e) rotation(pos, frac[e], cs[e], sn[e]);
-  const uint16_t *qrow = a.q + t * a.q_stride + d0, *krow = a.k + t * a.k_stride + d0;
-  uint16_t *qo = a.q_out + t * a.q_out_stride + d0, *ko = a.k_out + t * a.k_out_stride + d0;
-  for (int hb = h0; hb < h1; hb += R * U) {
-    uint4 raw[U];
+    for (int e = 0; e < 4; ++e) rotation(pos, frac[e], cs[e], sn[e]);
+    for (int hb = h0; hb < h1; hb += R * U) {
+      uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * R + sub;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < h1)
-        raw[u] = __ldcs(reinterpret_cast<const uint4 *>(h < a.hq ? qrow + static_cast<int64_t>(h) * D
-                                                                 : krow + static_cast<int64_t>(h - a.hq) * D));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * R + sub;
-      if (hb + u * R >= h1) break;  // warp-uniform
-      const bool is_q = h < a.hq;
-      float x[8];
-      unpack8(raw[u], x);
-      float inv = 1.f;
-      if constexpr (NORM) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        float wf[8];
-        unpack8(is_q ? wq : wk, wf);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wf[e];
+      for (int u = 0; u < U; ++u) {
+        const int h = hb + u * R + sub;
+        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < h1)
+          raw[u] = load(h < a.hq ? qrow + static_cast<int64_t>(h) * D : krow + static_cast<int64_t>(h - a.hq) * D);
       }
-      float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[e];
-      if constexpr (PAIRS) {
+      for (int u = 0; u < U; ++u) {
+        const int h = hb + u * R + sub;
+        if (hb + u * R >= h1) break;  // warp-uniform
+        const bool is_q = h < a.hq;
+        float x[8];
+        unpack8(raw[u], x);
+        if constexpr (NORM) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+          for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+          float wf[8];
+          unpack8(is_q ? wq : wk, wf);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wf[e];
+        }
         if (rot) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            y[2 * e] = x[2 * e] * cs[e] - x[2 * e + 1] * sn[e];
-            y[2 * e + 1] = x[2 * e + 1] * cs[e] + x[2 * e] * sn[e];
+            const int i = PAIRS ? 2 * e : e, j = PAIRS ? 2 * e + 1 : e + 4;
+            const float xi = x[i], xj = x[j];
+            x[i] = xi * cs[e] - xj * sn[e];
+            x[j] = xj * cs[e] + xi * sn[e];
           }
         }
-      } else {
-        // the partner's raw values cross lanes (four words instead of eight) and are normed here
-        uint4 pr;
-        pr.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
-        pr.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
-        pr.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
-        pr.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
-        if (rot) {
-          float z[8];
-          unpack8(pr, z);
-          if constexpr (NORM) {
-            float wf[8];
-            unpack8(is_q ? wqp : wkp, wf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = z[e] * inv * wf[e];
+        if (h < h1) {
+          uint16_t *out = is_q ? qo + static_cast<int64_t>(h) * D : ko + static_cast<int64_t>(h - a.hq) * D;
+          const uint2 u0 = make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
+          const uint2 u1 = make_uint2(ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
+          if constexpr (PAIRS) {
+            __stcs(reinterpret_cast<uint4 *>(out + da), make_uint4(u0.x, u0.y, u1.x, u1.y));
+          } else {
+            __stcs(reinterpret_cast<uint2 *>(out + da), u0);
+            __stcs(reinterpret_cast<uint2 *>(out + db), u1);
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = first ? x[e] * cs[e] - z[e] * sn[e] : x[e] * cs[e] + z[e] * sn[e];
         }
-      }
-      if (h < h1) {
-        const uint4 out = make_uint4(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]),
-                                     ptx::pack_bf16x2(y[4], y[5]), ptx::pack_bf16x2(y[6], y[7]));
-        __stcs(reinterpret_cast<uint4 *>(is_q ? qo + static_cast<int64_t>(h) * D
-                                              : ko + static_cast<int64_t>(h - a.hq) * D), out);
       }
     }
-  }
   }
 }
 
@@ -191,7 +167,7 @@ cudaError_t launch_norm(const RopeArgs &a, bool norm, cudaStream_t stream) {
   const int per = spread ? R : heads;
   const int wpt = (heads + per - 1) / per;
   const int64_t warps = static_cast<int64_t>(a.tokens) * wpt;
-  const int64_t most = 152 * 8;  // resident CTAs: 256 threads of at most 32 registers' worth of each eighth of an SM
+  const int64_t most = 152 * kRopeCtas;
   const int64_t ctas = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   const int64_t grid = ctas < most ? ctas : most;
   if (norm) rope_kernel<D, PAIRS, true><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a, per, wpt);
