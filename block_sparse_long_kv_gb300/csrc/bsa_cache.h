@@ -59,6 +59,9 @@ struct TreeArgs {
   float scale_log2;
   int32_t *status;
 };
+// Few query rows per KV head (bsa_tree.cu), and many (bsa_tree_mma.cu).
+size_t tree_mma_workspace_bytes(const CacheDims &c);
+bsa_status launch_tree_mma(const TreeArgs &a, void *workspace, cudaStream_t stream);
 size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft);
 bsa_status launch_tree(const TreeArgs &a, void *workspace, cudaStream_t stream);
 

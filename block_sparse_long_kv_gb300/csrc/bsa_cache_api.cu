@@ -39,6 +39,7 @@ bsa_status check_cache(const bsa_cache_shape *s, bsa::CacheDims *c) {
   if (s->format != BSA_CACHE_BF16 && s->format != BSA_CACHE_E4M3 && s->format != BSA_CACHE_E2M1)
     return BSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(s->pages) * s->page > INT32_MAX || s->hkv > 4096) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(s->pages) * s->hkv > INT32_MAX) return BSA_ERR_UNSUPPORTED;
   c->pages = s->pages;
   c->page = s->page;
   c->page_shift = s->page == 64 ? 6 : s->page == 128 ? 7 : 8;

@@ -849,9 +849,12 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
 
 }  // namespace
 
-size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft) { return workspace_layout(c.d).total; }
+size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft) {
+  return max_draft * (hq / c.hkv) > kRows ? tree_mma_workspace_bytes(c) : workspace_layout(c.d).total;
+}
 
 bsa_status launch_tree(const TreeArgs &a, void *workspace, cudaStream_t stream) {
+  if (a.max_draft * a.group > kRows) return launch_tree_mma(a, workspace, stream);
   cudaError_t e;
   const bool wide = a.c.d == 128;
   switch (a.c.format) {

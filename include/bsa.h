@@ -492,8 +492,8 @@ bsa_status bsa_qk_norm_rope(const bsa_rope_shape *shape, const void *q, int64_t 
  *                   the low four bits of a byte
  * Roundings are to nearest, ties to even.  Every held value is a bf16 value
  * (E4M3 and E2M1 down to bf16's smallest normal times the code's own range).
- * Supported: head_dim in {64, 128}; page in {64, 128, 256}; pages * page <
- * 2^31.  Code and scale arrays 16-byte aligned; scale pointers are ignored (may
+ * Supported: head_dim in {64, 128}; page in {64, 128, 256}; pages * page and
+ * pages * hkv < 2^31.  Code and scale arrays 16-byte aligned; scale pointers are ignored (may
  * be null) for BF16.  bsa_cache_code_bytes / bsa_cache_scale_bytes: bytes of
  * one codes and one scales array (0 for an invalid shape).
  *
