@@ -48,7 +48,6 @@ namespace {
 
 using wait::Ctl;
 using wait::drain_bar;
-using wait::wait_bar;
 
 constexpr int kSms = 152;
 constexpr int kThreads = 512;
@@ -102,7 +101,7 @@ struct Cfg {
   static constexpr uint32_t IDESC_O = Q16 ? ptx::idesc_bf16_f32(128, D, true) & ~((1u << 7) | (1u << 10))
                                           : ptx::idesc_bf16_f32(128, D, true);
   static constexpr int TM_O = 256;                 // S_0, S_1, O_0, O_1
-  static_assert(PER >= 0 && B_FIN < 64, "");
+  static_assert(PER >= 0 && NCH >= 1 && B_FIN < 64, "");
 };
 
 // 2^(e - 127); 0 for e <= 0.
@@ -134,6 +133,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // 3-D tiled load global -> shared, completion counted in bytes on `bar`.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, uint32_t bar, int c0, int c1, int c2) {
@@ -175,6 +177,32 @@ template <int N>
 struct Int {
   static constexpr int value = N;
 };
+
+// wait::wait_bar with a time for which the hardware may park the warp: twenty warps that poll would take
+// issue slots from the ones that compute.
+__device__ __forceinline__ bool try_wait_parked(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_parked(uint32_t bar, uint32_t parity, const Ctl &c) {
+  if (try_wait_parked(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (;;) {
+    if (try_wait_parked(bar, parity)) return true;
+    if (*c.abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > wait::kWaitTimeoutNs) {
+      wait::report(c, BSA_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 struct Span {
   int start, len;
@@ -269,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Ctl ctl{abort_flag, nullptr};
   auto put16 = [&](uint32_t at, uint4 v) { *reinterpret_cast<uint4 *>(sb + at) = v; };
   // a whole warp waits, and goes on or gives up together
-  auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar(i), parity, ctl)) != 0; };
+  auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait_parked(bar(i), parity, ctl)) != 0; };
   auto arrive_warp = [&](int i) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar(i));
@@ -381,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t parity = pv_count[t] & 1;
         auto chunk = [&](auto at, uint32_t acc) -> bool {  // 32 keys: two MMAs of 16
           constexpr int c = decltype(at)::value;
-          if (!wait_bar(bar(C::B_PR + t * C::NPC + c), parity, ctl)) return false;
+          if (!wait_parked(bar(C::B_PR + t * C::NPC + c), parity, ctl)) return false;
           ptx::tc_fence_after();
           mma_ts_at<16 * c, 256 * c>(dst, src, dv, C::IDESC_O, acc);
           mma_ts_at<16 * c + 8, 256 * c + 128>(dst, src, dv, C::IDESC_O, 1u);
@@ -398,17 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the lane's first P V of a segment overwrites O: the last segment's must have been read
       auto o_free = [&](int t) -> bool {
         const uint32_t k = lane_segs[t]++;
-        return k == 0 || wait_bar(bar(C::B_OE + t), (k - 1) & 1, ctl);
+        return k == 0 || wait_parked(bar(C::B_OE + t), (k - 1) & 1, ctl);
       };
       for (int x = x0; ok && x < x1;) {
         const Segment s = segment_at<C::NTQ>(a, pre, groups, x, x1);
         x += s.units;
-        if (!(ok = wait_bar(bar(C::B_QF), n_seg & 1, ctl))) break;
+        if (!(ok = wait_parked(bar(C::B_QF), n_seg & 1, ctl))) break;
         ++n_seg;
         for (int i = 0; i < s.units; ++i, ++n) {
           const uint32_t ks = n % C::KS, vs = n % C::VS;
           const bool last = i == s.units - 1;
-          if (!(ok = wait_bar(bar(C::B_KF + ks), (n / C::KS) & 1, ctl))) break;
+          if (!(ok = wait_parked(bar(C::B_KF + ks), (n / C::KS) & 1, ctl))) break;
           ptx::tc_fence_after();
           if constexpr (PAIR) {
             issue_s(0, ks);
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mma_commit(bar(C::B_KE + ks));
             if (last) ptx::mma_commit(bar(C::B_QE));
             // V(n) has two stages only and is refilled late: it is waited for as late as possible
-            if (!(ok = wait_bar(bar(C::B_VF + vs), (n / C::VS) & 1, ctl))) break;
+            if (!(ok = wait_parked(bar(C::B_VF + vs), (n / C::VS) & 1, ctl))) break;
             if (i == 0 && !(ok = o_free(0))) break;
             if (!(ok = issue_pv(0, vs, i > 0))) break;
             if (last) {
@@ -440,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j == i && !last) break;
               const uint32_t nj = n - static_cast<uint32_t>(i - j), pvs = nj % C::VS;
               const int t = j & 1;
-              if (!(ok = wait_bar(bar(C::B_VF + pvs), (nj / C::VS) & 1, ctl))) break;
+              if (!(ok = wait_parked(bar(C::B_VF + pvs), (nj / C::VS) & 1, ctl))) break;
               ptx::tc_fence_after();
               if (j == t && !(ok = o_free(t))) break;
               if (!(ok = issue_pv(t, pvs, j >= 2))) break;
@@ -571,25 +599,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("cp.async.commit_group;" ::: "memory");
       }
     };
-    uint32_t ew = 0u, ew_next = 0u;  // exponents of the rows 4 lane .. + 3 of this unit and the next
+    // exponents of the rows 4 lane .. + 3 of this unit and the next; of the next also which bytes are there
+    // (applied only when they are used: it would wait for the load)
+    uint32_t ew = 0u, ew_next = 0u, ew_mask = 0u;
     uint16_t gw[FMT == BSA_CACHE_E2M1 ? NP : 1], gw_next[FMT == BSA_CACHE_E2M1 ? NP : 1];  // group scales of the pieces
     auto fetch_scales = [&](int u) {
       if constexpr (Q16) {
         const int4 d0 = unit[2 * (u % (2 * kBatch))], d1 = unit[2 * (u % (2 * kBatch)) + 1];
-        ew_next = 0u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int pg = h == 0 ? d1.x : d1.z, w = h == 0 ? d1.y : d1.w;
-          const int row = (w >> 16) * kChunk, n = d0.z ? 0 : w & 0xFFFF;
+        {
+          const int pg = lane < 16 ? d1.x : d1.z, w = lane < 16 ? d1.y : d1.w;
+          const int rr = 4 * (lane & 15), live = (d0.z ? 0 : w & 0xFFFF) - rr;
           const uint8_t *sc = scales + (static_cast<size_t>(pg) * a.c.hkv + d0.w) * a.c.page * C::PER;
-          if ((lane >> 4) == h) {
-            const int rr = 4 * (lane & 15), live = n - rr;
-            if (live > 0) {
-              ew_next = __ldg(reinterpret_cast<const uint32_t *>(sc + row + rr));
-              if (live < 4) ew_next &= (1u << (8 * live)) - 1u;  // bytes past the last key are nobody's
-            }
-          }
-          if constexpr (FMT == BSA_CACHE_E2M1) {
+          ew_mask = live >= 4 ? 0xffffffffu : live <= 0 ? 0u : (1u << (8 * live)) - 1u;
+          ew_next = 0u;
+          if (live > 0) ew_next = __ldg(reinterpret_cast<const uint32_t *>(sc + (w >> 16) * kChunk + rr));
+        }
+        if constexpr (FMT == BSA_CACHE_E2M1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int pg = h == 0 ? d1.x : d1.z, w = h == 0 ? d1.y : d1.w;
+            const int row = (w >> 16) * kChunk, n = d0.z ? 0 : w & 0xFFFF;
+            const uint8_t *sc = scales + (static_cast<size_t>(pg) * a.c.hkv + d0.w) * a.c.page * C::PER;
 #pragma unroll
             for (int i = 0; i < NP / 2; ++i) {
               const int rr = r0 + STEP * i;
@@ -776,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (d0.z) drafted += ((static_cast<size_t>(drafts_of(a, d0.x / a.c.hkv).start) + (d1.y >> 16) * kUnit) * a.c.hkv + g) * D;
       int ref = 0;
       if constexpr (Q16) {
-        ew = ew_next;
+        ew = ew_next & ew_mask;
         if constexpr (FMT == BSA_CACHE_E2M1) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) gw[i] = gw_next[i];
@@ -803,7 +833,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int full = (kv == 0 ? C::B_KF : C::B_VF) + st, empty = (kv == 0 ? C::B_KE : C::B_VE) + st;
       const uint32_t tile = (kv == 0 ? C::OFF_K : C::OFF_V) + st * C::TILE;
       if (round > 0 && !(ok = wait_warp(empty, (round - 1) & 1))) break;
-      uint32_t tx = 0;
+      // bf16: whole chunks by TMA, at once (one box of 128 rows where a page holds both chunks); a chunk with
+      // absent rows by hand below, with zeros for them
+      uint32_t by_tma = 0;  // bit h: chunk h
+      if constexpr (!Q16) {
+        if (!d0.z) by_tma = (n0 == kChunk ? 1u : 0u) | (n1 == kChunk ? 2u : 0u);
+        if (a.c.page >= kUnit && by_tma != 3) by_tma = 0;
+        if ((lw & 1) == 0 && by_tma != 0) {
+          // (announced without arriving: this warp may still have rows of the other chunk to write)
+          if (lane == 0) mbar_expect_tx(bar(full), (by_tma == 3 ? 2u : 1u) * (C::TILE / 2));
+          __syncwarp();
+          const int c = lane >> 1, h = lane & 1;  // a lane for every copy
+          const bool mine = c < C::NCH && (by_tma >> h & 1) && (h == 0 || a.c.page < kUnit);
+          if (mine)
+            tma_load_3d(base + tile + c * C::CHUNK + h * (kChunk * 128), kv == 0 ? &tm_k : &tm_v, bar(full), c * 64,
+                        ((h == 0 ? d1.y : d1.w) >> 16) * kChunk, (h == 0 ? d1.x : d1.z) * a.c.hkv + g);
+          __syncwarp();
+          copies = n + 1;
+        }
+      }
       if (d0.z) {
         const float f = Q16 ? pow2_biased(254 + C::SHV - ref) : 1.f;
         store_rows(tile, 0, drafted, dstride, n0, f);
@@ -815,33 +863,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if constexpr (Q16) {
         convert(tile, ref);
       } else {
-        // whole chunks by TMA; a chunk with absent rows by hand, with zeros for them
-        tx = (n0 == kChunk ? 1u : 0u) + (n1 == kChunk ? 1u : 0u);
+        if (by_tma != 3) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int nh = h == 0 ? n0 : n1, pg = h == 0 ? d1.x : d1.z, sub = (h == 0 ? d1.y : d1.w) >> 16;
-          if (nh == kChunk) continue;
-          const size_t row = (static_cast<size_t>(pg) * a.c.hkv + g) * a.c.page + sub * kChunk;
-          store_rows(tile, h, reinterpret_cast<const uint16_t *>(codes) + row * D, D, nh, 1.f);
+          for (int h = 0; h < 2; ++h) {
+            if (by_tma >> h & 1) continue;
+            const int nh = h == 0 ? n0 : n1, pg = h == 0 ? d1.x : d1.z, sub = (h == 0 ? d1.y : d1.w) >> 16;
+            const size_t row = (static_cast<size_t>(pg) * a.c.hkv + g) * a.c.page + sub * kChunk;
+            store_rows(tile, h, reinterpret_cast<const uint16_t *>(codes) + row * D, D, nh, 1.f);
+          }
         }
       }
-      if (tx < 2) ptx::fence_proxy_async_smem();  // what was written by hand
-      __syncwarp();
-      if (lane == 0) {
-        if (!Q16 && (lw & 1) == 0 && tx > 0) ptx::mbar_arrive_expect_tx(bar(full), tx * (C::TILE / 2));
-        else ptx::mbar_arrive(bar(full));
-      }
-      if (!Q16 && (lw & 1) == 0 && tx > 0) {
-        __syncwarp();
-        const int h = lane & 1, c = lane >> 1;  // a copy per chunk and swizzle column, each from its own lane
-        if (c < C::NCH && (h == 0 ? n0 : n1) == kChunk) {
-          const int pg = h == 0 ? d1.x : d1.z, sub = (h == 0 ? d1.y : d1.w) >> 16;
-          tma_load_3d(base + tile + c * C::CHUNK + h * (kChunk * 128), kv == 0 ? &tm_k : &tm_v, bar(full), c * 64,
-                      sub * kChunk, pg * a.c.hkv + g);
-        }
-        __syncwarp();
-        copies = n + 1;
-      }
+      if (by_tma != 3) ptx::fence_proxy_async_smem();  // what was written by hand
+      arrive_warp(full);
     }
     if (Q16) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!Q16 && *abort_flag && (lw & 1) == 0 && lane == 0) {
@@ -1150,12 +1183,13 @@ Workspace workspace_layout(int d) {
   return w;
 }
 
-// One page chunk of a bf16 cache: [pages * hkv, page, d], box {64, 64, 1}, 128-byte swizzle.
+// Rows of a bf16 cache [pages * hkv, page, d]: box of 64 dimensions and 128 rows, or 64 where a page has no
+// more; 128-byte swizzle.
 bool chunk_map(EncodeTiledFn fn, CUtensorMap *map, const void *codes, const CacheDims &c) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page),
                               static_cast<cuuint64_t>(c.pages) * c.hkv};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d) * 2, static_cast<cuuint64_t>(c.page) * c.d * 2};
-  const cuuint32_t box[3] = {64u, 64u, 1u}, estr[3] = {1u, 1u, 1u};
+  const cuuint32_t box[3] = {64u, c.page >= kUnit ? 128u : 64u, 1u}, estr[3] = {1u, 1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(codes), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
