@@ -40,11 +40,21 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
   }
 }
 
-// f / 2 pi modulo one turn, in units of 2^-64 turns.
+// f / 2 pi modulo one turn, in units of 2^-64 turns: f = m * 2^e with an integer m of 24 bits, times
+// 2^64 / 2 pi as an integer of 62 bits, shifted.  Integer arithmetic: the double-precision pipe of this part
+// is slow enough to show in a step.  For |f| < 2^16 the result is within |f| units.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
-  const double t = static_cast<double>(f) * 0.15915494309189535;
-  const double fr = t - floor(t);  // in [0, 1); exact for the |f| < 2 pi of every rotary table
-  return static_cast<uint64_t>(fr * 18446744073709551616.0);
+  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+  const uint32_t u = __float_as_uint(f);
+  const int ex = static_cast<int>((u >> 23) & 0xFFu);
+  const uint64_t m = (u & 0x7FFFFFu) | (ex != 0 ? 0x800000u : 0u);
+  const int right = 150 - (ex != 0 ? ex : 1);  // f = m * 2^-right
+  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  uint64_t r;
+  if (right <= 0) r = right > -64 ? lo << -right : 0;
+  else if (right < 64) r = (lo >> right) | (hi << (64 - right));
+  else r = right < 128 ? hi >> (right - 64) : 0;
+  return (u >> 31) ? 0 - r : r;
 }
 
 // cos and sin of p times the fraction.  The reduced angle lies in [-pi, pi), where the fast sine

@@ -38,6 +38,7 @@
 
 #include "bsa_cache.h"
 #include "bsa_internal.h"
+#include "bsa_tree.cuh"
 #include "sm103_ptx.cuh"
 
 namespace bsa {
@@ -50,7 +51,7 @@ constexpr int kKeys = 64;        // keys of a unit
 constexpr int kBatch = kThreads; // units resolved at a time
 constexpr int kSms = 152;
 constexpr int kMaxCtas = 3 * kSms;
-constexpr int kSeg = 8;          // ints of a CTA's record for the combine
+constexpr int kSeg = kTreeSeg;   // ints of a CTA's record for the combine
 
 template <int D, int FMT>
 struct Cfg {
@@ -220,10 +221,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     int local = 0;
     for (int x = g0; x < g1; ++x) {
       const int b = x / a.c.hkv;
-      const Drafts dr = drafts_of(a, b);
+      const int listed = a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + x);  // (the loads in one round)
       const int n = cached_of(a, b);
+      const Drafts dr = drafts_of(a, b);
       const int pages = (n + a.c.page - 1) >> a.c.page_shift;
-      const int kept = a.kv_cnt == nullptr ? pages : max(0, min(__ldg(a.kv_cnt + x), pages));
+      const int kept = max(0, min(listed, pages));
       // without a list the chunks past the last token are not units at all
       const int ku = a.kv_cnt == nullptr ? (n + kKeys - 1) / kKeys : kept * cpp;
       per[x] = ku + (dr.len + kKeys - 1) / kKeys;
@@ -739,14 +741,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   for (int x = 0; x < C::STAGES - 1; ++x) issue(x);
   for (int u = 0; u < nu; ++u) {
     if ((u + C::STAGES - 1) % kBatch == 0) resolve(u + C::STAGES - 1);  // its buffer's units are all behind u
-    cp_wait<C::STAGES - 2>();  // unit u has landed
-    __syncthreads();           // for every thread; and unit u - 1's stage and a resolved batch are free to use
-    issue(u + C::STAGES - 1);
     const int4 d = unit[u % (2 * kBatch)];
-    if (d.x != arow_g || d.y != arow_t) {
+    if (d.x != arow_g || d.y != arow_t) {  // (Q's loads beside the unit's)
       if (arow_g >= 0) flush();
       start_tile(d.x, d.y);
     }
+    cp_wait<C::STAGES - 2>();  // unit u has landed
+    __syncthreads();           // for every thread; and unit u - 1's stage and a resolved batch are free to use
+    issue(u + C::STAGES - 1);
     const int n = d.w & 0xFFFF;
     if (n > 0) {
       if (d.z >= 0) cached_chunk(smem + (u % C::STAGES) * C::STAGE, n);
@@ -757,29 +759,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   flush();
 }
 
-// Row r of the tile that begins in CTA c - 1's run and goes on in CTA c's: O = sum w_p O_p / sum w_p l_p over
-// its parts p = c - 1 .., w_p = 2^(m_p - max m).  Warp w sums the parts w, w + 8, ..; the eight sums are added
-// in order.
+// The row tiles that several CTAs share.  CTA x takes the x-th of them in the order of their first CTA: it
+// begins in the run of CTA c - 1 and goes on in CTA c's, which has recorded it.  Row r:
+// O = sum w_p O_p / sum w_p l_p over its parts p = c - 1 .., w_p = 2^(m_p - max m).  Warp w sums the parts
+// w, w + 8, .. and the eight sums are added in order.
 constexpr int kCombineWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const TreeArgs a, const float *part_o,
-                                                                         const float *part_ml, const int *seg) {
+                                                                         const float *part_ml, const int *seg, int ctas) {
   constexpr int VL = D / 32;
+  constexpr int U = 4;  // parts of a warp in flight
   __shared__ float red_o[kCombineWarps][D];
   __shared__ float red_l[kCombineWarps];
-  const int c = blockIdx.x + 1, r = blockIdx.y;
-  const int grp = seg[c * kSeg];
-  if (grp < 0) return;
-  const int rt = seg[c * kSeg + 1], rs = seg[c * kSeg + 2], re = seg[c * kSeg + 3], W = seg[c * kSeg + 4];
-  if (rs >= c * W || rs < (c - 1) * W) return;  // the tile begins here, or further back
+  const int r = blockIdx.y;
+  const int c = shared_tile(seg, ctas, blockIdx.x);
+  if (c < 0) return;
+  const int *rec = seg + c * kSeg;
+  const int grp = rec[0], rt = rec[1], rs = rec[2], re = rec[3], W = rec[4];
   const int row = rt * kRows + r, t = row / a.group;
   const Drafts dr = drafts_of(a, grp / a.c.hkv);
   if (t >= dr.len) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int p0 = c - 1, np = (re - 1) / W - p0 + 1;
+  // every part after the first begins its CTA's run; the first may be that CTA's last tile
   auto at = [&](int p) {
-    return (2 * static_cast<size_t>(p0 + p) + (rs <= (p0 + p) * W ? 0 : 1)) * kRows + r;
+    return (2 * static_cast<size_t>(p0 + p) + (p > 0 || rs == p0 * W ? 0 : 1)) * kRows + r;
   };
   float m = -INFINITY;
   for (int p = lane; p < np; p += 32) m = fmaxf(m, part_ml[at(p) * 2]);
@@ -788,14 +793,35 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   float acc[VL], l = 0.f;
 #pragma unroll
   for (int x = 0; x < VL; ++x) acc[x] = 0.f;
-  for (int p = warp; p < np; p += kCombineWarps) {
-    const float2 ml = *reinterpret_cast<const float2 *>(part_ml + at(p) * 2);
-    if (ml.x == -INFINITY) continue;
-    const float wgt = exp2f(ml.x - m);
-    l = fmaf(ml.y, wgt, l);
-    const float *src = part_o + at(p) * D + lane * VL;
+  for (int pb = warp; pb < np; pb += U * kCombineWarps) {
+    float2 ml[U];
+    float v[U][VL];
 #pragma unroll
-    for (int x = 0; x < VL; ++x) acc[x] = fmaf(src[x], wgt, acc[x]);
+    for (int u = 0; u < U; ++u) {
+      const int p = pb + u * kCombineWarps;
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < VL; ++x) v[u][x] = 0.f;
+      if (p < np) {
+        ml[u] = *reinterpret_cast<const float2 *>(part_ml + at(p) * 2);
+        const float *src = part_o + at(p) * D + lane * VL;
+        if constexpr (VL == 4) {
+          const float4 q = *reinterpret_cast<const float4 *>(src);
+          v[u][0] = q.x; v[u][1] = q.y; v[u][2] = q.z; v[u][3] = q.w;
+        } else {
+          const float2 q = *reinterpret_cast<const float2 *>(src);
+          v[u][0] = q.x; v[u][1] = q.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].x == -INFINITY) continue;
+      const float wgt = exp2f(ml[u].x - m);
+      l = fmaf(ml[u].y, wgt, l);
+#pragma unroll
+      for (int x = 0; x < VL; ++x) acc[x] = fmaf(v[u][x], wgt, acc[x]);
+    }
   }
 #pragma unroll
   for (int x = 0; x < VL; ++x) red_o[warp][lane * VL + x] = acc[x];
@@ -842,8 +868,10 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, seg);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int rows = a.max_draft * a.group < kRows ? a.max_draft * a.group : kRows;
-  tree_combine_kernel<D><<<dim3(kSms * C::CTAS - 1, rows), kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, seg);
+  const int ctas = kSms * C::CTAS, rows = a.max_draft * a.group < kRows ? a.max_draft * a.group : kRows;
+  const long long tiles = static_cast<long long>(a.batch) * a.c.hkv * ((a.max_draft * a.group + kRows - 1) / kRows);
+  const int shared = static_cast<int>(tiles < ctas - 1 ? tiles : ctas - 1);  // at most: a run boundary each
+  tree_combine_kernel<D><<<dim3(shared, rows), kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, seg, ctas);
   return cudaGetLastError();
 }
 

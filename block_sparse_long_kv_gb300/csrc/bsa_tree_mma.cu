@@ -40,6 +40,7 @@
 
 #include "bsa_cache.h"
 #include "bsa_internal.h"
+#include "bsa_tree.cuh"
 #include "bsa_wait.cuh"
 #include "sm103_ptx.cuh"
 
@@ -56,7 +57,7 @@ constexpr int kUnit = 128;     // keys of a unit
 constexpr int kChunk = 64;     // keys of a page chunk
 constexpr int kBatch = 32;     // units resolved at a time, one chunk per thread of the K loaders
 constexpr int kInfo = 8;       // units whose scales are kept
-constexpr int kSeg = 8;        // ints of a CTA's record for the combine
+constexpr int kSeg = kTreeSeg; // ints of a CTA's record for the combine
 constexpr int kRegMma = 40, kRegLoad = 88, kRegSoft = 192;
 static_assert(128 * (kRegMma + kRegLoad + 2 * kRegSoft) <= kThreads * 128, "register split exceeds the launch");
 
@@ -232,14 +233,15 @@ struct GroupPlan {
 template <int NTQ>
 __device__ __forceinline__ GroupPlan plan_of(const TreeArgs &a, int x) {
   const int b = x / a.c.hkv;
-  const Span dr = drafts_of(a, b);
+  const int listed = a.kv_cnt == nullptr ? 0 : __ldg(a.kv_cnt + x);  // (the loads in one round)
   const int n = cached_of(a, b);
+  const Span dr = drafts_of(a, b);
   GroupPlan p;
   if (a.kv_cnt == nullptr) {
     p.chunks = (n + kChunk - 1) / kChunk;
   } else {
     const int pages = (n + a.c.page - 1) >> a.c.page_shift;
-    p.chunks = max(0, min(__ldg(a.kv_cnt + x), pages)) * (a.c.page / kChunk);
+    p.chunks = max(0, min(listed, pages)) * (a.c.page / kChunk);
   }
   p.per = (p.chunks + 1) / 2 + (dr.len + kUnit - 1) / kUnit;
   p.tiles = (dr.len * a.group + kRows * NTQ - 1) / (kRows * NTQ);
@@ -1127,46 +1129,93 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The row tile that begins in CTA c - 1's run and goes on in CTA c's: thread (row, 4 dimensions) sums
-// w_p O_p and w_p l_p over its parts p = c - 1 .. in order, w_p = 2^(m_p - max m).
-constexpr int kCombineDims = 8;   // dimensions per CTA
+// The row tiles that several CTAs share; CTA x takes the x-th of them (shared_tile), kCombineRows of its
+// rows and kCombineDims dimensions.  Parts p = c - 1 .. are spread over the warps (warp w takes w, w + 8, ..),
+// a lane is a row; O = sum w_p O_p / sum w_p l_p, w_p = 2^(m_p - max m), the eight sums added in order.
+constexpr int kCombineRows = 32, kCombineDims = 16, kCombineWarps = 8;
 
 template <int D, bool PAIR>
-__global__ void __launch_bounds__(kRows * kCombineDims / 4) tree_mma_combine_kernel(const TreeArgs a, const float *part_o,
-                                                                                   const float *part_ml, const int *seg) {
-  constexpr int NTQ = PAIR ? 2 : 1;
-  const int c = blockIdx.x + 1, t = blockIdx.z;
-  const int grp = seg[c * kSeg];
-  if (grp < 0) return;
-  const int rt = seg[c * kSeg + 1], rs = seg[c * kSeg + 2], re = seg[c * kSeg + 3], W = seg[c * kSeg + 4];
-  if (rs >= c * W || rs < (c - 1) * W) return;  // the tile begins here, or further back
-  const int r = threadIdx.x % kRows, d4 = blockIdx.y * (kCombineDims / 4) + threadIdx.x / kRows;
-  const int row = (rt * NTQ + t) * kRows + r, tok = row / a.group;
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(const TreeArgs a, const float *part_o,
+                                                                             const float *part_ml, const int *seg) {
+  constexpr int NTQ = PAIR ? 2 : 1, NQ = kCombineDims / 4, U = 2;
+  __shared__ float red_m[kCombineWarps][32], red_l[kCombineWarps][32];
+  __shared__ float4 red_o[kCombineWarps][NQ][32];
+  const int c = shared_tile(seg, kSms, blockIdx.x);
+  if (c < 0) return;
+  const int *rec = seg + c * kSeg;
+  const int grp = rec[0], rt = rec[1], rs = rec[2], re = rec[3], W = rec[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int BLOCKS = kRows / kCombineRows;
+  const int t = blockIdx.z / BLOCKS, r = (blockIdx.z % BLOCKS) * kCombineRows + lane, q0 = blockIdx.y * NQ;
   const Span dr = drafts_of(a, grp / a.c.hkv);
-  if (tok >= dr.len) return;
+  if (((rt * NTQ + t) * kRows + r - lane) / a.group >= dr.len) return;  // no row of the block is there
+  const int row = (rt * NTQ + t) * kRows + r, tok = row / a.group;
   const int p0 = c - 1, np = (re - 1) / W - p0 + 1;
-  auto slot = [&](int p) { return (2 * static_cast<size_t>(p0 + p) + (rs <= (p0 + p) * W ? 0 : 1)) * NTQ + t; };
-  float m = -INFINITY;
-  for (int p = 0; p < np; ++p) m = fmaxf(m, part_ml[(slot(p) * kRows + r) * 2]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < np; ++p) {
-    const float2 ml = *reinterpret_cast<const float2 *>(part_ml + (slot(p) * kRows + r) * 2);
-    const float4 v = reinterpret_cast<const float4 *>(part_o)[(slot(p) * (D / 4) + d4) * kRows + r];
-    if (ml.x == -INFINITY) continue;
-    const float w = exp2f(ml.x - m);
-    l = fmaf(ml.y, w, l);
-    acc.x = fmaf(v.x, w, acc.x);
-    acc.y = fmaf(v.y, w, acc.y);
-    acc.z = fmaf(v.z, w, acc.z);
-    acc.w = fmaf(v.w, w, acc.w);
+  // every part after the first begins its CTA's run; the first may be that CTA's last tile
+  auto slot = [&](int p) { return (2 * static_cast<size_t>(p0 + p) + (p > 0 || rs == p0 * W ? 0 : 1)) * NTQ + t; };
+  // each warp with its own running maximum
+  float m = -INFINITY, l = 0.f;
+  float4 acc[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int pb = warp; pb < np; pb += U * kCombineWarps) {
+    float2 ml[U];
+    float4 v[U][NQ];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = pb + u * kCombineWarps;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (p < np) {
+        ml[u] = *reinterpret_cast<const float2 *>(part_ml + (slot(p) * kRows + r) * 2);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          v[u][q] = reinterpret_cast<const float4 *>(part_o)[(slot(p) * (D / 4) + q0 + q) * kRows + r];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].x == -INFINITY) continue;
+      const float mn = fmaxf(m, ml[u].x);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(ml[u].x - mn);
+      m = mn;
+      l = fmaf(ml[u].y, w, l * f);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        acc[q].x = fmaf(v[u][q].x, w, acc[q].x * f);
+        acc[q].y = fmaf(v[u][q].y, w, acc[q].y * f);
+        acc[q].z = fmaf(v[u][q].z, w, acc[q].z * f);
+        acc[q].w = fmaf(v[u][q].w, w, acc[q].w * f);
+      }
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  red_m[warp][lane] = m;
+  red_l[warp][lane] = l;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) red_o[warp][q][lane] = acc[q];
+  __syncthreads();
+  if (warp >= NQ) return;  // warp q finishes dimensions 4 (q0 + q) ..
+  float mm = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) mm = fmaxf(mm, red_m[w][lane]);
+  float ls = 0.f;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) {
+    if (red_m[w][lane] == -INFINITY) continue;
+    const float f = exp2f(red_m[w][lane] - mm);
+    ls = fmaf(red_l[w][lane], f, ls);
+    const float4 v = red_o[w][warp][lane];
+    s.x = fmaf(v.x, f, s.x);
+    s.y = fmaf(v.y, f, s.y);
+    s.z = fmaf(v.z, f, s.z);
+    s.w = fmaf(v.w, f, s.w);
+  }
+  if (tok >= dr.len) return;
+  const float inv = ls > 0.f ? 1.f / ls : 0.f;
   const size_t out = static_cast<size_t>(dr.start + tok) * a.hq + (grp % a.c.hkv) * a.group + row % a.group;
-  *reinterpret_cast<uint2 *>(a.o + out * D + 4 * d4) =
-      make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (a.lse != nullptr && d4 == 0) a.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  *reinterpret_cast<uint2 *>(a.o + out * D + 4 * (q0 + warp)) =
+      make_uint2(ptx::pack_bf16x2(s.x * inv, s.y * inv), ptx::pack_bf16x2(s.z * inv, s.w * inv));
+  if (a.lse != nullptr && q0 + warp == 0) a.lse[out] = ls > 0.f ? (mm + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
 struct Workspace {
@@ -1221,8 +1270,12 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
     return BSA_ERR_CUDA;
   kern<<<kSms, kThreads, smem, stream>>>(mk, mv, a, part_o, part_ml, lane_o, seg);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  tree_mma_combine_kernel<D, PAIR><<<dim3(kSms - 1, D / kCombineDims, C::NTQ), kRows * kCombineDims / 4, 0, stream>>>(
-      a, part_o, part_ml, seg);
+  const int rows = a.max_draft * a.group;
+  const long long tiles = static_cast<long long>(a.batch) * a.c.hkv * ((rows + kRows * C::NTQ - 1) / (kRows * C::NTQ));
+  const int shared = static_cast<int>(tiles < kSms - 1 ? tiles : kSms - 1);  // at most: a run boundary each
+  const int most = rows < kRows * C::NTQ ? rows : kRows * C::NTQ;
+  const dim3 grid(shared, D / kCombineDims, (most + kCombineRows - 1) / kCombineRows);
+  tree_mma_combine_kernel<D, PAIR><<<grid, kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, seg);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

@@ -452,7 +452,7 @@ bsa_status bsa_decode_step(const bsa_varlen_shape *shape, const bsa_select_param
  * (BSA_ERR_INVALID_ARG).  Supported: head_dim in {64, 128}; rotary_dim a
  * multiple of 16 in [0, head_dim] (with 0, inv_freq may be null and positions
  * only say which tokens count); tokens >= 0 (0 launches nothing).  inv_freq:
- * fp32 [rotary_dim / 2], finite.  positions: int32 [tokens].  eps finite, >= 0.
+ * fp32 [rotary_dim / 2], below 2^16 in size.  positions: int32 [tokens].  eps finite, >= 0.
  * q, k, outputs, weights 16-byte aligned; positions, inv_freq 4-byte aligned.
  * ------------------------------------------------------------------------ */
 #define BSA_ROPE_PAIRS 1
