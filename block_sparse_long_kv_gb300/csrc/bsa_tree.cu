@@ -22,11 +22,14 @@
 // brings its largest element to [2^14, 2^15): bf16's eight bits fit f16's eleven
 // and what lies 2^28 below the largest element loses bits.
 //
-// P of an 8- or 4-bit cache is P' = p * 2^(e - eref + 15) in f16, e the exponent
-// of the key's V row and eref the largest seen, O held in units of 2^(eref - 15):
-// p <= 1 keeps P' within f16, and the shift by 15 leaves 29 powers of two below
-// the largest product at f16's full 2^-11, 10 more with fewer bits.  P of a bf16 cache is
-// bf16, 2^-8 relative at any size.  Sums and statistics are fp32 from unrounded p.
+// The softmax reference m of a row moves only when its maximum has grown by more
+// than 2^TH, so that O is rarely rescaled; p <= 2^TH.
+//
+// P of an 8- or 4-bit cache is P' = p * 2^(e - eref + SHIFT) in f16, e the exponent
+// of the key's V row and eref the largest seen, O held in units of 2^(eref - SHIFT):
+// SHIFT = 15 - TH keeps P' within f16 and leaves 25 powers of two below the largest
+// product at f16's full 2^-11, 10 more with fewer bits.  P of a bf16 cache is bf16, 2^-8
+// relative at any size.  Sums and statistics are fp32 from unrounded p.
 //
 // Tiles that one CTA holds whole are written by it; of the others every CTA
 // leaves an unnormalised part (O, max, sum), which tree_combine_kernel merges in
@@ -51,7 +54,6 @@ constexpr int kKeys = 64;        // keys of a unit
 constexpr int kBatch = kThreads; // units resolved at a time
 constexpr int kSms = 152;
 constexpr int kMaxCtas = 3 * kSms;
-constexpr int kSeg = kTreeSeg;   // ints of a CTA's record for the combine
 
 template <int D, int FMT>
 struct Cfg {
@@ -63,6 +65,9 @@ struct Cfg {
   // resident CTAs per SM (the register limit allows three) and ring stages that fill the 227 KB
   static constexpr int CTAS = FMT == BSA_CACHE_BF16 && D == 128 ? 2 : 3;
   static constexpr int STAGES = STAGE > 12000 ? 3 : 4;
+  static constexpr int TH = FMT == BSA_CACHE_BF16 ? 8 : 4;
+  static constexpr int SHIFT = FMT == BSA_CACHE_BF16 ? 0 : 15 - TH;
+  static constexpr int UNIT1 = 127 + SHIFT;  // the exponent reference at which O's unit is 1
   static constexpr int NKS = D / 16;  // k-steps of S
   static constexpr int NNT = D / 8;   // n-tiles of O
   static constexpr int TB = RB / 4;   // bytes of a key row per thread
@@ -88,9 +93,12 @@ __device__ __forceinline__ int v_swizzle(int row) {
   return RB == 256 ? ((row >> 1) & 1) | (row & 4) : RB == 128 ? row & 7 : RB == 64 ? row & 2 : 0;
 }
 
-__device__ __forceinline__ void cp16(void *dst, const void *src, bool live) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool live) {
   const int n = live ? 16 : 0;  // 0: zeros, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(dst)), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -190,11 +198,11 @@ __device__ __forceinline__ int cta_scan(int c, int *total, int *wsum) {
   return off + inc - c;
 }
 
-// A unit: .x the group (b * hkv + g), .y the tile, .z the page (-1: drafted tokens), .w keys in the
-// low half and first key (chunk of the page, or of the drafts) in units of 64 in the high half.
+// A unit: .x the group (b * hkv + g), .y the row tile, .z the cache tile (page * hkv + g; -1: drafted
+// tokens), .w keys in the low half and first key (chunk of the page, or of the drafts) in units of 64 in the high half.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(const TreeArgs a, float *part_o, float *part_ml,
-                                                                        int *seg) {
+                                                                        TreeRun *runs) {
   using C = Cfg<D, FMT>;
   constexpr bool Q16 = FMT != BSA_CACHE_BF16;  // f16 fragments
   extern __shared__ __align__(16) unsigned char smem[];
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   const int W = (n_all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int x0 = min(n_all, cta * W), x1 = min(n_all, x0 + W);
   if (x0 >= x1) {  // CTA-uniform
-    if (tid == 0) seg[cta * kSeg] = -1;
+    if (tid == 0) runs[cta].group = -1;
     return;
   }
   const int nu = x1 - x0;
@@ -262,21 +270,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       else hi = mid - 1;
     }
     const int local = x - pre[lo], b = lo / a.c.hkv;
-    const int rt = local / per[lo], k = local - rt * per[lo];
+    const int n = cached_of(a, b);
     const Drafts dr = drafts_of(a, b);
+    const int rt = local / per[lo], k = local - rt * per[lo];
     const int ku = per[lo] - (dr.len + kKeys - 1) / kKeys;
     int4 d = make_int4(lo, rt, -1, 0);
     if (k >= ku) {
       const int c = k - ku;
       d.w = min(kKeys, dr.len - c * kKeys) | c << 16;
     } else {
-      const int n = cached_of(a, b);
-      const int e = k / cpp, sub = k - e * cpp;
+      const int e = k >> (a.c.page_shift - 6), sub = k & (cpp - 1);
       const int j = a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
       if (j >= 0 && j < (n + a.c.page - 1) >> a.c.page_shift) {
         const int pg = __ldg(a.table + static_cast<size_t>(b) * a.table_stride + j);
         if (pg >= 0 && pg < a.c.pages) {
-          d.z = pg;
+          d.z = pg * a.c.hkv + (lo - b * a.c.hkv);
           d.w = max(0, min(kKeys, n - j * a.c.page - sub * kKeys)) | sub << 16;
         } else if (a.status != nullptr) {
           atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
@@ -286,33 +294,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     unit[u % (2 * kBatch)] = d;
   };
 
+  // A thread copies the same 16-byte column of rows a fixed step apart (a multiple of eight, or of the
+  // swizzles' period), so every address is one of a few bases plus a constant.
+  constexpr int PR = C::RB / 16, STEP = kThreads / PR, COPIES = kKeys / STEP;
+  const int crow = tid / PR, ccol = tid % PR;
+  const uint32_t k_dst = ptx::smem_addr(smem) + crow * C::RB + (ccol ^ k_swizzle<C::RB>(crow)) * 16;
+  const uint32_t v_dst = ptx::smem_addr(smem) + C::CODE + crow * C::RB + (ccol ^ v_swizzle<C::RB>(crow)) * 16;
   auto issue = [&](int u) {
     if (u < nu) {
       const int4 d = unit[u % (2 * kBatch)];
       const int n = d.w & 0xFFFF;
       if (d.z >= 0 && n > 0) {
-        unsigned char *st = smem + (u % C::STAGES) * C::STAGE;
-        const size_t tile = static_cast<size_t>(d.z) * a.c.hkv + d.x % a.c.hkv;
+        const uint32_t st = static_cast<uint32_t>(u % C::STAGES) * C::STAGE;
         const int sub = d.w >> 16;
-        const size_t at = (tile * a.c.page + sub * kKeys) * C::RB;
-        constexpr int PR = C::RB / 16;
-        for (int x = tid; x < kKeys * PR; x += kThreads) {
-          const int r = x / PR, pc = x % PR;
-          const bool live = r < n;
-          cp16(st + r * C::RB + (pc ^ k_swizzle<C::RB>(r)) * 16, a.k_codes + at + x * 16, live);
-          cp16(st + C::CODE + r * C::RB + (pc ^ v_swizzle<C::RB>(r)) * 16, a.v_codes + at + x * 16, live);
+        const size_t at = (static_cast<size_t>(d.z) * a.c.page + sub * kKeys) * C::RB + tid * 16;
+        const uint8_t *ks = a.k_codes + at, *vs = a.v_codes + at;
+        if (n == kKeys) {
+#pragma unroll
+          for (int i = 0; i < COPIES; ++i) {
+            cp16(k_dst + st + i * STEP * C::RB, ks + i * kThreads * 16);
+            cp16(v_dst + st + i * STEP * C::RB, vs + i * kThreads * 16);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < COPIES; ++i) {
+            const bool live = crow + i * STEP < n;
+            cp16_or_zero(k_dst + st + i * STEP * C::RB, ks + i * kThreads * 16, live);
+            cp16_or_zero(v_dst + st + i * STEP * C::RB, vs + i * kThreads * 16, live);
+          }
         }
         if constexpr (C::PER > 0) {
           // the exponents of the chunk's 64 rows, then their group scales
-          const size_t sc = tile * a.c.page * C::PER;
-          unsigned char *ss = st + 2 * C::CODE;
+          const size_t sc = static_cast<size_t>(d.z) * a.c.page * C::PER;
           constexpr int PS = kKeys * C::PER / 16;
-          for (int x = tid; x < PS; x += kThreads) {
-            const size_t from = x < kKeys / 16
-                                    ? sc + sub * kKeys + x * 16
-                                    : sc + a.c.page + static_cast<size_t>(sub) * kKeys * (C::PER - 1) + (x - kKeys / 16) * 16;
-            cp16(ss + x * 16, a.k_scales + from, true);
-            cp16(ss + C::SCALE + x * 16, a.v_scales + from, true);
+          if (tid < PS) {
+            const size_t from = tid < kKeys / 16 ? sc + sub * kKeys + tid * 16
+                                                 : sc + a.c.page + static_cast<size_t>(sub) * kKeys * (C::PER - 1) +
+                                                       (tid - kKeys / 16) * 16;
+            const uint32_t to = ptx::smem_addr(smem) + st + 2 * C::CODE + tid * 16;
+            cp16(to, a.k_scales + from);
+            cp16(to + C::SCALE, a.v_scales + from);
           }
         }
       }
@@ -324,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   float o[C::NNT][4];
   float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
   float sc_lo = a.scale_log2, sc_hi = a.scale_log2;  // logit scales of the rows gq and gq + 8
-  int eref = 0;  // O is in units of 2^(eref - 142); 0: nothing yet
+  int eref = 0;  // O is in units of 2^(eref - UNIT1); 0: nothing yet
   int arow_g = -1, arow_t = -1;
   Drafts adr{0, 0};
 
@@ -404,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       mlo = fmaxf(mlo, wm[x][gq]);
       mhi = fmaxf(mhi, wm[x][gq + 8]);
     }
-    const float unit_f = Q16 && eref != 0 ? exp2f(static_cast<float>(eref - 142)) : 1.f;
-    const float slo = m_lo == -INFINITY ? 0.f : exp2f(m_lo - mlo) * unit_f;
-    const float shi = m_hi == -INFINITY ? 0.f : exp2f(m_hi - mhi) * unit_f;
+    const float unit_f = Q16 && eref != 0 ? exp2f(static_cast<float>(eref - C::UNIT1)) : 1.f;
+    const float slo = m_lo == -INFINITY ? 0.f : ptx::ex2_approx(m_lo - mlo) * unit_f;
+    const float shi = m_hi == -INFINITY ? 0.f : ptx::ex2_approx(m_hi - mhi) * unit_f;
     for (int x = 0; x < kWarps; ++x) {  // one warp after another: a fixed order of the sums
       if (warp == x) {
         float *rlo = obuf + gq * C::LDO + 2 * tq * (D / 8), *rhi = rlo + 8 * C::LDO;
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       for (int x = 0; x < kWarps; ++x) m = fmaxf(m, wm[x][r]);
 #pragma unroll
       for (int x = 0; x < kWarps; ++x)
-        if (wm[x][r] != -INFINITY) l = fmaf(exp2f(wm[x][r] - m), wl[x][r], l);
+        if (wm[x][r] != -INFINITY) l = fmaf(ptx::ex2_approx(wm[x][r] - m), wl[x][r], l);
       const float4 v = *reinterpret_cast<const float4 *>(obuf + r * C::LDO + d4);
       if (whole) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -450,54 +471,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   };
 
   // The softmax step of a 16-key slice: x holds the logits (log2 units, -inf where masked), and on
-  // return p; the running statistics and O move to the new maximum.  `fo` further scales O.
+  // return p; the row references, sums and O move on where they have to.  `fo` further scales O.
   auto softmax = [&](float (&x)[2][4], float fo) {
-    float mx_lo = -INFINITY, mx_hi = -INFINITY;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      mx_lo = fmaxf(mx_lo, fmaxf(x[nt][0], x[nt][1]));
-      mx_hi = fmaxf(mx_hi, fmaxf(x[nt][2], x[nt][3]));
-    }
+    float mx_lo = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+    float mx_hi = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
 #pragma unroll
     for (int off = 1; off <= 2; off <<= 1) {
       mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, off));
       mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, off));
     }
-    const float mn_lo = fmaxf(m_lo, mx_lo), mn_hi = fmaxf(m_hi, mx_hi);
-    const float f_lo = m_lo == -INFINITY ? 0.f : exp2f(m_lo - mn_lo);
-    const float f_hi = m_hi == -INFINITY ? 0.f : exp2f(m_hi - mn_hi);
-    m_lo = mn_lo;
-    m_hi = mn_hi;
-    float ps_lo = 0.f, ps_hi = 0.f;
+    const bool up_lo = mx_lo > m_lo + static_cast<float>(C::TH), up_hi = mx_hi > m_hi + static_cast<float>(C::TH);
+    if (__any_sync(0xffffffffu, up_lo || up_hi || fo != 1.f)) {
+      float f_lo = 1.f, f_hi = 1.f;
+      if (up_lo) {
+        f_lo = m_lo == -INFINITY ? 0.f : ptx::ex2_approx(m_lo - mx_lo);
+        m_lo = mx_lo;
+      }
+      if (up_hi) {
+        f_hi = m_hi == -INFINITY ? 0.f : ptx::ex2_approx(m_hi - mx_hi);
+        m_hi = mx_hi;
+      }
+      l_lo *= f_lo;
+      l_hi *= f_hi;
+      f_lo *= fo;
+      f_hi *= fo;
+#pragma unroll
+      for (int nt = 0; nt < C::NNT; ++nt) {
+        o[nt][0] *= f_lo;
+        o[nt][1] *= f_lo;
+        o[nt][2] *= f_hi;
+        o[nt][3] *= f_hi;
+      }
+    }
+    // (a row without any key so far has only -inf here, and p = 0)
+    const float r_lo = m_lo == -INFINITY ? 0.f : m_lo, r_hi = m_hi == -INFINITY ? 0.f : m_hi;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[nt][e] = x[nt][e] == -INFINITY ? 0.f : exp2f(x[nt][e] - (e < 2 ? mn_lo : mn_hi));
-        if (e < 2) ps_lo += x[nt][e];
-        else ps_hi += x[nt][e];
-      }
-    l_lo = fmaf(l_lo, f_lo, ps_lo);
-    l_hi = fmaf(l_hi, f_hi, ps_hi);
-    const float g_lo = f_lo * fo, g_hi = f_hi * fo;
-    if (g_lo != 1.f || g_hi != 1.f) {
-#pragma unroll
-      for (int nt = 0; nt < C::NNT; ++nt) {
-        o[nt][0] *= g_lo;
-        o[nt][1] *= g_lo;
-        o[nt][2] *= g_hi;
-        o[nt][3] *= g_hi;
-      }
-    }
+      for (int e = 0; e < 4; ++e) x[nt][e] = ptx::ex2_approx(x[nt][e] - (e < 2 ? r_lo : r_hi));
+    l_lo += (x[0][0] + x[0][1]) + (x[1][0] + x[1][1]);
+    l_hi += (x[0][2] + x[0][3]) + (x[1][2] + x[1][3]);
   };
 
   // One 64-key chunk of the cache; n keys of it are there.
   auto cached_chunk = [&](const unsigned char *st, int n) {
     const int k0 = warp * 16;
     if (k0 >= n) return;  // warp-uniform
-    float s[2][4];
+    float s[2][4], s2[2][4];  // even and odd k-steps: two chains of MMAs per n-tile
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
     const unsigned char *ksc = st + 2 * C::CODE, *vsc = ksc + C::SCALE;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
@@ -522,10 +546,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       }
       if constexpr (FMT == BSA_CACHE_BF16) {
 #pragma unroll
-        for (int ks = 0; ks < C::NKS; ++ks) mma<true>(s[nt], qa[ks], w[2 * ks], w[2 * ks + 1]);
+        for (int ks = 0; ks < C::NKS; ++ks) mma<true>(ks & 1 ? s2[nt] : s[nt], qa[ks], w[2 * ks], w[2 * ks + 1]);
       } else if constexpr (FMT == BSA_CACHE_E4M3) {
 #pragma unroll
-        for (int ks = 0; ks < C::NKS; ++ks) mma<false>(s[nt], qa[ks], e4m3x2_f16(w[ks]), e4m3x2_f16(w[ks] >> 16));
+        for (int ks = 0; ks < C::NKS; ++ks)
+          mma<false>(ks & 1 ? s2[nt] : s[nt], qa[ks], e4m3x2_f16(w[ks]), e4m3x2_f16(w[ks] >> 16));
       } else {
         // the thread's quarter is whole groups of 16 dimensions: four k-steps each
         constexpr int NG = D / 64;
@@ -542,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 #pragma unroll
         for (int ks = 0; ks < C::NKS; ++ks) {
           const uint32_t h = w[ks / 2] >> (16 * (ks & 1));
-          mma<false>(s[nt], qa[ks], mul_f16x2(e2m1x2_f16(h), g2[ks / 4]), mul_f16x2(e2m1x2_f16(h >> 8), g2[ks / 4]));
+          mma<false>(ks & 1 ? s2[nt] : s[nt], qa[ks], mul_f16x2(e2m1x2_f16(h), g2[ks / 4]),
+                     mul_f16x2(e2m1x2_f16(h >> 8), g2[ks / 4]));
         }
       }
     }
@@ -565,7 +591,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f = Q16 ? (e < 2 ? sc_lo : sc_hi) * kf[e & 1] : a.scale_log2;
-        s[nt][e] = key + (e & 1) < n ? s[nt][e] * f : -INFINITY;
+        s[nt][e] = (s[nt][e] + s2[nt][e]) * f;
+      }
+      if (n < k0 + 16) {  // warp-uniform: the slice is not whole
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (key + (e & 1) >= n) s[nt][e] = -INFINITY;
       }
     }
     if constexpr (Q16) {
@@ -578,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       }
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        vs[nt][0] = pow2_biased(ev[nt][0] - eref + 142);
-        vs[nt][1] = pow2_biased(ev[nt][1] - eref + 142);
+        vs[nt][0] = pow2_biased(ev[nt][0] - eref + C::UNIT1);
+        vs[nt][1] = pow2_biased(ev[nt][1] - eref + C::UNIT1);
       }
     }
     softmax(s, fo);
@@ -705,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
         }
       float fo = 1.f;
       if constexpr (Q16) {  // O to units of 1
-        if (eref != 0) fo = exp2f(static_cast<float>(eref - 142));
-        eref = 142;
+        if (eref != 0) fo = exp2f(static_cast<float>(eref - C::UNIT1));
+        eref = C::UNIT1;
       }
       softmax(s, fo);
       const uint32_t pa[4] = {ptx::pack_bf16x2(s[0][0], s[0][1]), ptx::pack_bf16x2(s[0][2], s[0][3]),
@@ -730,12 +761,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   if (tid == 0) {  // the run's first tile, for the combine
     const int4 d = unit[0];
     const int rs = pre[d.x] + d.y * per[d.x];
-    int *rec = seg + cta * kSeg;
-    rec[0] = d.x;
-    rec[1] = d.y;
-    rec[2] = rs;
-    rec[3] = rs + per[d.x];
-    rec[4] = W;
+    const Drafts dr = drafts_of(a, d.x / a.c.hkv);
+    runs[cta] = TreeRun{d.x, d.y, rs, rs + per[d.x], W, dr.start, dr.len, 0};
   }
 #pragma unroll
   for (int x = 0; x < C::STAGES - 1; ++x) issue(x);
@@ -762,35 +789,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 // The row tiles that several CTAs share.  CTA x takes the x-th of them in the order of their first CTA: it
 // begins in the run of CTA c - 1 and goes on in CTA c's, which has recorded it.  Row r:
 // O = sum w_p O_p / sum w_p l_p over its parts p = c - 1 .., w_p = 2^(m_p - max m).  Warp w sums the parts
-// w, w + 8, .. and the eight sums are added in order.
+// w, w + 8, .. against its own maximum, and the eight sums are added in order.
 constexpr int kCombineWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const TreeArgs a, const float *part_o,
-                                                                         const float *part_ml, const int *seg, int ctas) {
+                                                                         const float *part_ml, const TreeRun *runs,
+                                                                         int ctas) {
   constexpr int VL = D / 32;
   constexpr int U = 4;  // parts of a warp in flight
   __shared__ float red_o[kCombineWarps][D];
-  __shared__ float red_l[kCombineWarps];
+  __shared__ float red_m[kCombineWarps], red_l[kCombineWarps];
   const int r = blockIdx.y;
-  const int c = shared_tile(seg, ctas, blockIdx.x);
+  TreeRun run;
+  const int c = shared_tile(runs, ctas, blockIdx.x, &run);
   if (c < 0) return;
-  const int *rec = seg + c * kSeg;
-  const int grp = rec[0], rt = rec[1], rs = rec[2], re = rec[3], W = rec[4];
-  const int row = rt * kRows + r, t = row / a.group;
-  const Drafts dr = drafts_of(a, grp / a.c.hkv);
-  if (t >= dr.len) return;
+  const int row = run.tile * kRows + r, t = row / a.group;
+  if (t >= run.drafts) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int p0 = c - 1, np = (re - 1) / W - p0 + 1;
+  const int p0 = c - 1, np = (run.last - 1) / run.run - p0 + 1;
   // every part after the first begins its CTA's run; the first may be that CTA's last tile
   auto at = [&](int p) {
-    return (2 * static_cast<size_t>(p0 + p) + (p > 0 || rs == p0 * W ? 0 : 1)) * kRows + r;
+    return (2 * static_cast<size_t>(p0 + p) + (p > 0 || run.first == p0 * run.run ? 0 : 1)) * kRows + r;
   };
-  float m = -INFINITY;
-  for (int p = lane; p < np; p += 32) m = fmaxf(m, part_ml[at(p) * 2]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  float acc[VL], l = 0.f;
+  // each warp with its own running maximum
+  float m = -INFINITY, l = 0.f, acc[VL];
 #pragma unroll
   for (int x = 0; x < VL; ++x) acc[x] = 0.f;
   for (int pb = warp; pb < np; pb += U * kCombineWarps) {
@@ -817,40 +840,50 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (ml[u].x == -INFINITY) continue;
-      const float wgt = exp2f(ml[u].x - m);
-      l = fmaf(ml[u].y, wgt, l);
+      const float mn = fmaxf(m, ml[u].x);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), wgt = exp2f(ml[u].x - mn);
+      m = mn;
+      l = fmaf(ml[u].y, wgt, l * f);
 #pragma unroll
-      for (int x = 0; x < VL; ++x) acc[x] = fmaf(v[u][x], wgt, acc[x]);
+      for (int x = 0; x < VL; ++x) acc[x] = fmaf(v[u][x], wgt, acc[x] * f);
     }
   }
 #pragma unroll
   for (int x = 0; x < VL; ++x) red_o[warp][lane * VL + x] = acc[x];
-  if (lane == 0) red_l[warp] = l;
+  if (lane == 0) {
+    red_m[warp] = m;
+    red_l[warp] = l;
+  }
   __syncthreads();
-  const size_t out = static_cast<size_t>(dr.start + t) * a.hq + (grp % a.c.hkv) * a.group + row % a.group;
+  float mm = -INFINITY, fw[kCombineWarps];
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) mm = fmaxf(mm, red_m[w]);
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) fw[w] = red_m[w] == -INFINITY ? 0.f : exp2f(red_m[w] - mm);
+  const size_t out = static_cast<size_t>(run.draft0 + t) * a.hq + (run.group % a.c.hkv) * a.group + row % a.group;
   for (int d = threadIdx.x; d < D; d += kCombineWarps * 32) {
     float s = 0.f, ls = 0.f;
 #pragma unroll
     for (int w = 0; w < kCombineWarps; ++w) {
-      s += red_o[w][d];
-      ls += red_l[w];
+      s = fmaf(red_o[w][d], fw[w], s);
+      ls = fmaf(red_l[w], fw[w], ls);
     }
     const __nv_bfloat16 v = __float2bfloat16_rn(ls > 0.f ? s / ls : 0.f);
     a.o[out * D + d] = *reinterpret_cast<const uint16_t *>(&v);
-    if (a.lse != nullptr && d == 0) a.lse[out] = ls > 0.f ? (m + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+    if (a.lse != nullptr && d == 0) a.lse[out] = ls > 0.f ? (mm + log2f(ls)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
 struct Workspace {
-  size_t part_o, part_ml, seg, total;
+  size_t part_o, part_ml, runs, total;
 };
 Workspace workspace_layout(int d) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Workspace w;
   w.part_o = 0;
   w.part_ml = up(2ull * kMaxCtas * kRows * d * 4);
-  w.seg = w.part_ml + up(2ull * kMaxCtas * kRows * 2 * 4);
-  w.total = w.seg + up(static_cast<size_t>(kMaxCtas) * kSeg * 4);
+  w.runs = w.part_ml + up(2ull * kMaxCtas * kRows * 2 * 4);
+  w.total = w.runs + up(kMaxCtas * sizeof(TreeRun));
   return w;
 }
 
@@ -860,18 +893,18 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const Workspace ws = workspace_layout(D);
   char *base = static_cast<char *>(workspace);
   float *part_o = reinterpret_cast<float *>(base + ws.part_o), *part_ml = reinterpret_cast<float *>(base + ws.part_ml);
-  int *seg = reinterpret_cast<int *>(base + ws.seg);
+  TreeRun *runs = reinterpret_cast<TreeRun *>(base + ws.runs);
   auto kern = tree_attn_kernel<D, FMT>;
   const size_t smem = C::smem(a.batch * a.c.hkv);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, seg);
+  kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, runs);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int ctas = kSms * C::CTAS, rows = a.max_draft * a.group < kRows ? a.max_draft * a.group : kRows;
   const long long tiles = static_cast<long long>(a.batch) * a.c.hkv * ((a.max_draft * a.group + kRows - 1) / kRows);
   const int shared = static_cast<int>(tiles < ctas - 1 ? tiles : ctas - 1);  // at most: a run boundary each
-  tree_combine_kernel<D><<<dim3(shared, rows), kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, seg, ctas);
+  tree_combine_kernel<D><<<dim3(shared, rows), kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, runs, ctas);
   return cudaGetLastError();
 }
 

@@ -5,25 +5,31 @@
 
 namespace bsa {
 
-// What CTA c of an attention launch records of its run of units, kTreeSeg ints:
-//   [0] the group (sequence * hkv + KV head) of its first row tile, -1 without units
-//   [1] that tile, [2] [3] the tile's first unit and the one past its last, [4] units per run
-constexpr int kTreeSeg = 8;
+// What CTA c of an attention launch records of its run of units: the group (sequence * hkv + KV head) of its
+// first row tile (-1 without units), that tile, the tile's first unit and the one past its last, the units of
+// a run, and the sequence's first drafted token and their number.
+struct alignas(16) TreeRun {
+  int group, tile, first, last, run, draft0, drafts, pad;
+};
 
-// The CTA c >= 1 whose first row tile is the x-th of those that begin in run c - 1 and go on in run c; -1
-// when there are fewer.  Every thread of the block takes part.
-__device__ __forceinline__ int shared_tile(const int *seg, int ctas, int x) {
+// The run c >= 1 whose first row tile is the x-th of those that begin in run c - 1 and go on in run c; its
+// number, or -1 when there are fewer.  Every thread of the block takes part, and finds the record in *out.
+__device__ __forceinline__ int shared_tile(const TreeRun *runs, int ctas, int x, TreeRun *out) {
   __shared__ int warp_count[32];
-  __shared__ int found;
+  __shared__ TreeRun found;
+  __shared__ int found_at;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
-  if (threadIdx.x == 0) found = -1;
+  if (threadIdx.x == 0) found_at = -1;
   int seen = 0;
   for (int base = 1; base < ctas; base += blockDim.x) {
     const int c = base + static_cast<int>(threadIdx.x);
+    TreeRun r;
     bool mine = false;
-    if (c < ctas && seg[c * kTreeSeg] >= 0) {
-      const int rs = seg[c * kTreeSeg + 2], W = seg[c * kTreeSeg + 4];
-      mine = rs < c * W && rs >= (c - 1) * W;
+    if (c < ctas) {
+      const int4 *p = reinterpret_cast<const int4 *>(runs + c);
+      const int4 a = p[0], b = p[1];
+      r = TreeRun{a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
+      mine = r.group >= 0 && r.first < c * r.run && r.first >= (c - 1) * r.run;
     }
     const unsigned vote = __ballot_sync(0xffffffffu, mine);
     if (lane == 0) warp_count[warp] = __popc(vote);
@@ -33,12 +39,16 @@ __device__ __forceinline__ int shared_tile(const int *seg, int ctas, int x) {
       if (w < warp) before += warp_count[w];
       total += warp_count[w];
     }
-    if (mine && before + __popc(vote & ((1u << lane) - 1u)) == x) found = c;
+    if (mine && before + __popc(vote & ((1u << lane) - 1u)) == x) {
+      found = r;
+      found_at = c;
+    }
     __syncthreads();
     seen = total;
     if (seen > x) break;
   }
-  return found;
+  *out = found;
+  return found_at;
 }
 
 }  // namespace bsa

@@ -57,7 +57,6 @@ constexpr int kUnit = 128;     // keys of a unit
 constexpr int kChunk = 64;     // keys of a page chunk
 constexpr int kBatch = 32;     // units resolved at a time, one chunk per thread of the K loaders
 constexpr int kInfo = 8;       // units whose scales are kept
-constexpr int kSeg = kTreeSeg; // ints of a CTA's record for the combine
 constexpr int kRegMma = 40, kRegLoad = 88, kRegSoft = 192;
 static_assert(128 * (kRegMma + kRegLoad + 2 * kRegSoft) <= kThreads * 128, "register split exceeds the launch");
 
@@ -277,7 +276,7 @@ __device__ __forceinline__ Segment segment_at(const TreeArgs &a, const int *pre,
 template <int D, int FMT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const TreeArgs a, float *part_o, float *part_ml, float *lane_o, int *seg) {
+                    const TreeArgs a, float *part_o, float *part_ml, float *lane_o, TreeRun *runs) {
   using C = Cfg<D, FMT, PAIR>;
   constexpr bool Q16 = C::Q16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -367,16 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int W = (n_all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int x0 = min(n_all, cta * W), x1 = min(n_all, x0 + W);
   if (tid == 0) {  // the run's first row tile, for the combine
-    int *rec = seg + cta * kSeg;
     if (x0 < x1) {
       const Segment s = segment_at<C::NTQ>(a, pre, groups, x0, x1);
-      rec[1] = s.rt;
-      rec[2] = s.rs;
-      rec[3] = s.re;
-      rec[4] = W;
-      rec[0] = s.grp;
+      const Span dr = drafts_of(a, s.grp / a.c.hkv);
+      runs[cta] = TreeRun{s.grp, s.rt, s.rs, s.re, W, dr.start, dr.len, 0};
     } else {
-      rec[0] = -1;
+      runs[cta].group = -1;
     }
   }
 
@@ -1136,23 +1131,21 @@ constexpr int kCombineRows = 32, kCombineDims = 16, kCombineWarps = 8;
 
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(const TreeArgs a, const float *part_o,
-                                                                             const float *part_ml, const int *seg) {
+                                                                             const float *part_ml, const TreeRun *runs) {
   constexpr int NTQ = PAIR ? 2 : 1, NQ = kCombineDims / 4, U = 2;
   __shared__ float red_m[kCombineWarps][32], red_l[kCombineWarps][32];
   __shared__ float4 red_o[kCombineWarps][NQ][32];
-  const int c = shared_tile(seg, kSms, blockIdx.x);
+  TreeRun run;
+  const int c = shared_tile(runs, kSms, blockIdx.x, &run);
   if (c < 0) return;
-  const int *rec = seg + c * kSeg;
-  const int grp = rec[0], rt = rec[1], rs = rec[2], re = rec[3], W = rec[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int BLOCKS = kRows / kCombineRows;
   const int t = blockIdx.z / BLOCKS, r = (blockIdx.z % BLOCKS) * kCombineRows + lane, q0 = blockIdx.y * NQ;
-  const Span dr = drafts_of(a, grp / a.c.hkv);
-  if (((rt * NTQ + t) * kRows + r - lane) / a.group >= dr.len) return;  // no row of the block is there
-  const int row = (rt * NTQ + t) * kRows + r, tok = row / a.group;
-  const int p0 = c - 1, np = (re - 1) / W - p0 + 1;
+  const int row = (run.tile * NTQ + t) * kRows + r, tok = row / a.group;
+  if ((row - lane) / a.group >= run.drafts) return;  // no row of the block is there
+  const int p0 = c - 1, np = (run.last - 1) / run.run - p0 + 1;
   // every part after the first begins its CTA's run; the first may be that CTA's last tile
-  auto slot = [&](int p) { return (2 * static_cast<size_t>(p0 + p) + (p > 0 || rs == p0 * W ? 0 : 1)) * NTQ + t; };
+  auto slot = [&](int p) { return (2 * static_cast<size_t>(p0 + p) + (p > 0 || run.first == p0 * run.run ? 0 : 1)) * NTQ + t; };
   // each warp with its own running maximum
   float m = -INFINITY, l = 0.f;
   float4 acc[NQ];
@@ -1210,16 +1203,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(co
     s.z = fmaf(v.z, f, s.z);
     s.w = fmaf(v.w, f, s.w);
   }
-  if (tok >= dr.len) return;
+  if (tok >= run.drafts) return;
   const float inv = ls > 0.f ? 1.f / ls : 0.f;
-  const size_t out = static_cast<size_t>(dr.start + tok) * a.hq + (grp % a.c.hkv) * a.group + row % a.group;
+  const size_t out = static_cast<size_t>(run.draft0 + tok) * a.hq + (run.group % a.c.hkv) * a.group + row % a.group;
   *reinterpret_cast<uint2 *>(a.o + out * D + 4 * (q0 + warp)) =
       make_uint2(ptx::pack_bf16x2(s.x * inv, s.y * inv), ptx::pack_bf16x2(s.z * inv, s.w * inv));
   if (a.lse != nullptr && q0 + warp == 0) a.lse[out] = ls > 0.f ? (mm + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
 struct Workspace {
-  size_t part_o, part_ml, lane_o, seg, total;
+  size_t part_o, part_ml, lane_o, runs, total;
 };
 Workspace workspace_layout(int d) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -1227,8 +1220,8 @@ Workspace workspace_layout(int d) {
   w.part_o = 0;  // two parts per CTA, up to two row tiles each
   w.part_ml = up(4ull * kSms * kRows * d * 4);
   w.lane_o = w.part_ml + up(4ull * kSms * kRows * 2 * 4);
-  w.seg = w.lane_o + up(static_cast<size_t>(kSms) * kRows * (d + 4) * 4);
-  w.total = w.seg + up(static_cast<size_t>(kSms) * kSeg * 4);
+  w.runs = w.lane_o + up(static_cast<size_t>(kSms) * kRows * (d + 4) * 4);
+  w.total = w.runs + up(kSms * sizeof(TreeRun));
   return w;
 }
 
@@ -1258,7 +1251,7 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   char *base = static_cast<char *>(workspace);
   float *part_o = reinterpret_cast<float *>(base + ws.part_o), *part_ml = reinterpret_cast<float *>(base + ws.part_ml);
   float *lane_o = reinterpret_cast<float *>(base + ws.lane_o);
-  int *seg = reinterpret_cast<int *>(base + ws.seg);
+  TreeRun *runs = reinterpret_cast<TreeRun *>(base + ws.runs);
   auto kern = tree_mma_kernel<D, FMT, PAIR>;
   // setmaxnreg.inc waits until the registers it asks for are free: the split is only safe if the
   // kernel really launches with 128 registers per thread
@@ -1268,14 +1261,14 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const size_t smem = C::smem(a.batch * a.c.hkv);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return BSA_ERR_CUDA;
-  kern<<<kSms, kThreads, smem, stream>>>(mk, mv, a, part_o, part_ml, lane_o, seg);
+  kern<<<kSms, kThreads, smem, stream>>>(mk, mv, a, part_o, part_ml, lane_o, runs);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   const int rows = a.max_draft * a.group;
   const long long tiles = static_cast<long long>(a.batch) * a.c.hkv * ((rows + kRows * C::NTQ - 1) / (kRows * C::NTQ));
   const int shared = static_cast<int>(tiles < kSms - 1 ? tiles : kSms - 1);  // at most: a run boundary each
   const int most = rows < kRows * C::NTQ ? rows : kRows * C::NTQ;
   const dim3 grid(shared, D / kCombineDims, (most + kCombineRows - 1) / kCombineRows);
-  tree_mma_combine_kernel<D, PAIR><<<grid, kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, seg);
+  tree_mma_combine_kernel<D, PAIR><<<grid, kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, runs);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

@@ -7,9 +7,9 @@ much again for an f16 query element that lies 2^28 below its row's largest.  P i
 A = sum p |v| / sum p,  |O - ref| <= (2^-8 + 4 delta + 2^-18) A + 2^-8 |ref|,  and
 |lse - ref| <= 2 delta + 2^-20 (1 + |ref|).
 An 8- or 4-bit cache is computed in f16, whose smallest step is 2^-24, so small terms keep an absolute
-error.  With few rows P' = p 2^(e - eref + 15): a key's term is off by at most 2^-25-15 |code| 2^eref, a
-code is at most 448 (2688) and the row that set eref has its largest value above half of that times
-2^eref, so by 2^-39 vmax, vmax the largest |v|.  With many rows P' = p 2^11 with p <= 16, off by 2^-36 of
+error.  With few rows P' = p 2^(e - eref + 11), p <= 16: a key's term is off by at most 2^-25-11 |code|
+2^eref, a code is at most 448 (2688) and the row that set eref has its largest value above half of that
+times 2^eref, so by 2^-35 vmax, vmax the largest |v|.  With many rows P' = p 2^11 with p <= 16, off by 2^-36 of
 values up to vmax, and V' holds vmax above 2^13, so it is off by 2^-38 vmax itself.  p of the largest
 logit is at least 1, hence sum p >= 1, and n keys add at most n 2^-35 vmax (a softmax so sharp that A
 itself is below 2^-28 meets it).
