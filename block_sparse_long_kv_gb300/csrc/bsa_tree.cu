@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr int NNT = D / 8;   // n-tiles of O
   static constexpr int TB = RB / 4;   // bytes of a key row per thread
   static constexpr int VB = RB / 8;   // bytes of a value row per lane group
-  static constexpr int LDO = D + 4;   // row of the merge buffer, in floats
+  static constexpr int LDO = D + 8;   // row of the merge buffer, in floats (the pad spreads the rows over the banks)
   static constexpr int OFF_O = STAGES * STAGE;
   static constexpr int OFF_ML = OFF_O + kRows * LDO * 4;            // [2][warps][16] floats
   static constexpr int OFF_E = OFF_ML + 2 * kWarps * kRows * 4;     // [warps] O's unit exponent
@@ -428,15 +428,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     const float unit_f = Q16 && eref != 0 ? exp2f(static_cast<float>(eref - C::UNIT1)) : 1.f;
     const float slo = m_lo == -INFINITY ? 0.f : ptx::ex2_approx(m_lo - mlo) * unit_f;
     const float shi = m_hi == -INFINITY ? 0.f : ptx::ex2_approx(m_hi - mhi) * unit_f;
-    for (int x = 0; x < kWarps; ++x) {  // one warp after another: a fixed order of the sums
+    // One warp after another: a fixed order of the sums.  Element [row][8 nt + c] is dimension c (D / 8) + nt.
+    // (One copy of the code: a flush runs once or twice per CTA, from a cold instruction cache.)
+#pragma unroll 1
+    for (int x = 0; x < kWarps; ++x) {
       if (warp == x) {
-        float *rlo = obuf + gq * C::LDO + 2 * tq * (D / 8), *rhi = rlo + 8 * C::LDO;
+        float *rlo = obuf + gq * C::LDO + 2 * tq, *rhi = rlo + 8 * C::LDO;
 #pragma unroll
         for (int nt = 0; nt < C::NNT; ++nt) {
-          rlo[nt] = (x > 0 ? rlo[nt] : 0.f) + o[nt][0] * slo;
-          rlo[D / 8 + nt] = (x > 0 ? rlo[D / 8 + nt] : 0.f) + o[nt][1] * slo;
-          rhi[nt] = (x > 0 ? rhi[nt] : 0.f) + o[nt][2] * shi;
-          rhi[D / 8 + nt] = (x > 0 ? rhi[D / 8 + nt] : 0.f) + o[nt][3] * shi;
+          float2 u = make_float2(0.f, 0.f), v = u;
+          if (x > 0) {
+            u = *reinterpret_cast<const float2 *>(rlo + 8 * nt);
+            v = *reinterpret_cast<const float2 *>(rhi + 8 * nt);
+          }
+          *reinterpret_cast<float2 *>(rlo + 8 * nt) = make_float2(fmaf(o[nt][0], slo, u.x), fmaf(o[nt][1], slo, u.y));
+          *reinterpret_cast<float2 *>(rhi + 8 * nt) = make_float2(fmaf(o[nt][2], shi, v.x), fmaf(o[nt][3], shi, v.y));
         }
       }
       __syncthreads();
@@ -445,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     const bool whole = rs >= x0 && re <= x1;
     const size_t slot = 2 * static_cast<size_t>(cta) + (rs <= x0 ? 0 : 1);
     constexpr int PIECES = D / 4;
+#pragma unroll 1
     for (int e = tid; e < kRows * PIECES; e += kThreads) {
       const int r = e / PIECES, d4 = 4 * (e % PIECES);
       const int row = arow_t * kRows + r, t = row / G;
@@ -455,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 #pragma unroll
       for (int x = 0; x < kWarps; ++x)
         if (wm[x][r] != -INFINITY) l = fmaf(ptx::ex2_approx(wm[x][r] - m), wl[x][r], l);
-      const float4 v = *reinterpret_cast<const float4 *>(obuf + r * C::LDO + d4);
+      const float *from = obuf + r * C::LDO + d4 / (D / 8) + 8 * (d4 % (D / 8));
+      const float4 v = make_float4(from[0], from[8], from[16], from[24]);
       if (whole) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + row % G;
@@ -798,6 +806,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
                                                                          int ctas) {
   constexpr int VL = D / 32;
   constexpr int U = 4;  // parts of a warp in flight
+  after_previous_kernel();
   __shared__ float red_o[kCombineWarps][D];
   __shared__ float red_m[kCombineWarps], red_l[kCombineWarps];
   const int r = blockIdx.y;
@@ -904,8 +913,9 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const int ctas = kSms * C::CTAS, rows = a.max_draft * a.group < kRows ? a.max_draft * a.group : kRows;
   const long long tiles = static_cast<long long>(a.batch) * a.c.hkv * ((a.max_draft * a.group + kRows - 1) / kRows);
   const int shared = static_cast<int>(tiles < ctas - 1 ? tiles : ctas - 1);  // at most: a run boundary each
-  tree_combine_kernel<D><<<dim3(shared, rows), kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, runs, ctas);
-  return cudaGetLastError();
+  return launch_after(tree_combine_kernel<D>, dim3(shared, rows), kCombineWarps * 32, stream, a,
+                      static_cast<const float *>(part_o), static_cast<const float *>(part_ml),
+                      static_cast<const TreeRun *>(runs), ctas);
 }
 
 }  // namespace

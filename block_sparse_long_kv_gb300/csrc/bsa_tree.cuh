@@ -1,9 +1,29 @@
 // Shared by the two drafted-token kernels: the records that their runs leave for the combine.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace bsa {
+
+// A kernel launched by launch_after may start before the one ahead of it in the stream has ended; it waits
+// here, before its first read, until that one has ended and its writes are visible.
+__device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a short kernel so that its launch overlaps the end of the kernel ahead of it.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 // What CTA c of an attention launch records of its run of units: the group (sequence * hkv + KV head) of its
 // first row tile (-1 without units), that tile, the tile's first unit and the one past its last, the units of

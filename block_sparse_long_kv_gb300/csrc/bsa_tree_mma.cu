@@ -1133,6 +1133,7 @@ template <int D, bool PAIR>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(const TreeArgs a, const float *part_o,
                                                                              const float *part_ml, const TreeRun *runs) {
   constexpr int NTQ = PAIR ? 2 : 1, NQ = kCombineDims / 4, U = 2;
+  after_previous_kernel();
   __shared__ float red_m[kCombineWarps][32], red_l[kCombineWarps][32];
   __shared__ float4 red_o[kCombineWarps][NQ][32];
   TreeRun run;
@@ -1268,8 +1269,10 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const int shared = static_cast<int>(tiles < kSms - 1 ? tiles : kSms - 1);  // at most: a run boundary each
   const int most = rows < kRows * C::NTQ ? rows : kRows * C::NTQ;
   const dim3 grid(shared, D / kCombineDims, (most + kCombineRows - 1) / kCombineRows);
-  tree_mma_combine_kernel<D, PAIR><<<grid, kCombineWarps * 32, 0, stream>>>(a, part_o, part_ml, runs);
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  const cudaError_t e = launch_after(tree_mma_combine_kernel<D, PAIR>, grid, kCombineWarps * 32, stream, a,
+                                     static_cast<const float *>(part_o), static_cast<const float *>(part_ml),
+                                     static_cast<const TreeRun *>(runs));
+  return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
 template <int D, int FMT>
