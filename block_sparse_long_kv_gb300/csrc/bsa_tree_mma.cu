@@ -14,12 +14,10 @@
 //          units; their results are merged when the segment ends
 // Warps:  0      TMEM owner; one thread issues S_t = Q_t K^T (both operands in
 //                shared memory) and O_t += P_t V (P from TMEM, over S_t)
-//         1, 2   copy 8- and 4-bit codes of K and of V by TMA, 32 rows at a time, and
-//                their scales, into two rings
-//         3      looks the units up (plan, list, page table) ahead of everyone
-//         4-5    loaders of K, 6-7 of V: codes from the ring into f16 tiles with the
-//                128-byte swizzle, a thread per row; bf16 pages by TMA; Q, partial
-//                chunks and drafted tokens by hand
+//         4-5    loaders of K, 6-7 of V: bf16 pages by TMA; 8- and 4-bit codes by
+//                cp.async into a ring of each thread's own pieces, from there into
+//                f16 tiles with the 128-byte swizzle; Q, partial chunks and drafted
+//                tokens by hand
 //         8-11, 12-15  the softmax lanes, one thread per query row
 //
 // An 8- or 4-bit cache is computed in f16.  With e the exponent of a key's row and
@@ -57,9 +55,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 128;     // rows of a tile
 constexpr int kUnit = 128;     // keys of a unit
 constexpr int kChunk = 64;     // keys of a page chunk
-constexpr int kBatch = 16;     // units looked up at a time, a chunk per lane
-constexpr int kBatches = 4;    // batches kept
-constexpr int kUnits = kBatch * kBatches;
+constexpr int kBatch = 32;     // units resolved at a time, one chunk per thread of the K loaders
 constexpr int kInfo = 8;       // units whose scales are kept
 constexpr int kRegMma = 40, kRegLoad = 88, kRegSoft = 192;
 static_assert(128 * (kRegMma + kRegLoad + 2 * kRegSoft) <= kThreads * 128, "register split exceeds the launch");
@@ -70,6 +66,7 @@ struct Cfg {
   static constexpr int RB = FMT == BSA_CACHE_BF16 ? 2 * D : FMT == BSA_CACHE_E4M3 ? D : D / 2;
   static constexpr int PER = FMT == BSA_CACHE_BF16 ? 0 : FMT == BSA_CACHE_E4M3 ? 1 : 1 + D / 16;
   static constexpr int PP = Q16 ? RB / 16 : 1;     // 16-byte pieces of a code row
+  static constexpr int NP = Q16 ? 2 * PP : 1;      // pieces of a unit per loader thread
   static constexpr int SHV = FMT == BSA_CACHE_E4M3 ? 6 : 4;  // 448 * 2^6 and 2688 * 2^4 stay below 2^16
   static constexpr int TH = Q16 ? 4 : 8;           // log2 of how far the reference may lag the maximum
   static constexpr int SHIFT = Q16 ? 15 - TH : 0;
@@ -78,36 +75,33 @@ struct Cfg {
   static constexpr uint32_t TILE = 128u * D * 2;
   static constexpr uint32_t CHUNK = 128u * 128;    // one swizzle chunk column of a tile
   static constexpr int KS = 2, VS = PAIR || Q16 ? 2 : 3;
-  // the rings of codes: slots of 32 rows, for K and for V; and of a unit's row exponents and group scales
-  static constexpr uint32_t SLOT = 32u * RB;
-  static constexpr int SLOTS_FIT = (PAIR ? (FMT == BSA_CACHE_E2M1 ? 10240 : 12288) : 20480) / (32 * RB);
-  static constexpr int SLOTS = SLOTS_FIT < 8 ? SLOTS_FIT : 8;
-  static constexpr uint32_t SCALES = 128u * PER;
+  static constexpr int GRP = 4;                    // pieces of a cp.async group
+  static constexpr int NG = Q16 ? NP / GRP : 1;    // groups of a unit
+  static constexpr int RING = 3;                   // groups in flight per thread
+  static constexpr uint32_t CODES = Q16 ? 128u * RING * GRP * 16 : 0;  // of the four loader warps
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = OFF_Q + NTQ * TILE;
   static constexpr uint32_t OFF_V = OFF_K + KS * TILE;
   static constexpr uint32_t OFF_CODE = OFF_V + VS * TILE;
-  static constexpr uint32_t OFF_SCALE = OFF_CODE + (Q16 ? 2u * SLOTS * SLOT : 0u);
-  static constexpr uint32_t OFF_BAR = OFF_SCALE + (Q16 ? 2u * 2u * SCALES : 0u);
+  static constexpr uint32_t OFF_BAR = OFF_CODE + CODES;
   static constexpr int NPC = 4;                    // P released in chunks of 32 keys
   static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS,
                        B_SF = B_VE + VS, B_PR = B_SF + 2, B_OD = B_PR + 2 * NPC, B_OE = B_OD + 2, B_UN = B_OE + 2,
-                       B_UE = B_UN + kBatches, B_IK = B_UE + kBatches, B_IV = B_IK + kInfo, B_RS = B_IV + kInfo,
-                       B_LK = B_RS + 2, B_LV = B_LK + 1, B_LA = B_LV + 1, B_LB = B_LA + 1, B_CF = B_LB + 1,
-                       B_CE = B_CF + 16, B_XF = B_CE + 16, B_XE = B_XF + 4, B_FIN = B_XE + 4, NBARS = B_FIN + 1;
+                       B_IK = B_UN + 2, B_IV = B_IK + kInfo, B_RS = B_IV + kInfo, B_LK = B_RS + 2, B_LV = B_LK + 1,
+                       B_LA = B_LV + 1, B_LB = B_LA + 1, B_FIN = B_LB + 1, NBARS = B_FIN + 1;
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag, scan sums
   static constexpr uint32_t OFF_INFO = OFF_MISC + 128;                        // [kInfo] K's scale, [kInfo] oref
   static constexpr uint32_t OFF_ROWS = OFF_INFO + kInfo * 8;                  // [2][NTQ * 128] row scales of Q
   static constexpr uint32_t OFF_RED = OFF_ROWS + 2 * NTQ * 128 * 4;           // [4] loader maxima
-  static constexpr uint32_t OFF_UNIT = OFF_RED + 32;                          // [kUnits] {int4, int4}
-  static constexpr uint32_t OFF_PRE = OFF_UNIT + kUnits * 32;             // [groups + 1] first unit
+  static constexpr uint32_t OFF_UNIT = OFF_RED + 32;                          // [2][kBatch] {int4, int4}
+  static constexpr uint32_t OFF_PRE = OFF_UNIT + 2 * kBatch * 32;             // [groups + 1] first unit
   static size_t smem(int groups) { return OFF_PRE + static_cast<size_t>(groups + 1) * 4 + 1024; }
   static constexpr uint32_t IDESC_S = Q16 ? ptx::idesc_bf16_f32(128, 128, false) & ~((1u << 7) | (1u << 10))
                                           : ptx::idesc_bf16_f32(128, 128, false);
   static constexpr uint32_t IDESC_O = Q16 ? ptx::idesc_bf16_f32(128, D, true) & ~((1u << 7) | (1u << 10))
                                           : ptx::idesc_bf16_f32(128, D, true);
   static constexpr int TM_O = 256;                 // S_0, S_1, O_0, O_1
-  static_assert(PER >= 0 && PP >= 1 && NCH >= 1 && (!Q16 || SLOTS >= 2) && OFF_CODE % 1024 == 0, "");
+  static_assert(PER >= 0 && NCH >= 1 && B_FIN < 64, "");
 };
 
 // 2^(e - 127); 0 for e <= 0.
@@ -150,12 +144,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, uint3
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
-}
-// Contiguous copy global -> shared, 16-byte aligned, completion counted in bytes on `bar`.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
 }
 // Offset of 16-byte unit u (of 8) of row r in swizzle chunk c of a tile at offset `tile`.
 __device__ __forceinline__ uint32_t swizzled(uint32_t tile, int c, int r, int u) {
@@ -318,20 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, G = a.group, groups = a.batch * a.c.hkv;
-  // the barrier and parity under which the batch of unit n has been looked up
-  auto batch_bar = [](int n) { return C::B_UN + (n / kBatch) % kBatches; };
-  auto batch_parity = [](int n) { return static_cast<uint32_t>(n / kUnits) & 1u; };
 
   if (tid == 0) {
     for (int x = 0; x < C::NBARS; ++x) {
-      // arrivals: 1 of a commit or a copying thread, 2 of the K or the V loaders' warps, 4 of all loaders or a
-      // softmax lane
+      // arrivals: 1 of a commit, 2 of the K or the V loaders' warps, 4 of all loaders or a softmax lane
       uint32_t count = 1;
       if (x == C::B_QF || (x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_UN) ||
           (x >= C::B_RS && x < C::B_LK) || x == C::B_LA || x == C::B_LB)
         count = 4;
-      else if ((x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) || (x >= C::B_UE && x < C::B_RS) ||
-               x == C::B_LK || x == C::B_LV || (x >= C::B_XE && x < C::B_FIN))
+      else if ((x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) || (x >= C::B_UN && x < C::B_RS) ||
+               x == C::B_LK || x == C::B_LV)
         count = 2;
       ptx::mbar_init(bar(x), count);
     }
@@ -498,17 +482,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         drain_bar(bar(C::B_FIN), 0);
       }
     }
-    if (warp == 3) {
-      // ================================================================ lookup of the units
-      // {group, row tile, 1 for drafted tokens, KV head} and the page and (keys | chunk of the page << 16) of
-      // both chunks; for drafted tokens the chunk is the unit's number among them.
-      for (int first = 0; first < x1 - x0; first += kBatch) {
-        const int k = first / kBatch;
-        // batch k takes the place of batch k - 4: the loaders of K, and with them everyone, are well past that
-        // one when they have begun batch k - 2
-        if (k >= 2 && !wait_warp(C::B_UE + (k - 2) % kBatches, static_cast<uint32_t>((k - 2) / kBatches) & 1)) break;
-        const int u = first + (lane >> 1), h = lane & 1;
-        if (u < x1 - x0) {
+    __syncwarp();
+  } else if (warp < 8) {
+    // ================================================================ loaders
+    ptx::setmaxnreg_dec<kRegLoad>();
+    const int kv = (warp - 4) >> 1;       // 0: K, 1: V
+    const int lt = (tid - 128) & 63;      // thread of the pair of warps
+    const int lw = warp - 4;
+    const int nu = x1 - x0;
+    const uint8_t *codes = kv == 0 ? a.k_codes : a.v_codes, *scales = kv == 0 ? a.k_scales : a.v_scales;
+    uint32_t pair_phase = 0;
+    auto sync_pair = [&]() -> bool {  // the two warps; bounded, unlike a named barrier
+      arrive_warp(C::B_LK + kv);
+      return wait_warp(C::B_LK + kv, pair_phase++ & 1);
+    };
+
+    // Units first .. first + kBatch - 1 of the run, one chunk per thread of the K loaders: {group, row
+    // tile, 1 for drafted tokens, KV head} and the page and (keys | chunk of the page << 16) of both chunks.
+    auto resolve = [&](int first) -> bool {
+      if (kv == 0) {
+        const int u = first + (lt >> 1), h = lt & 1;
+        if (u < nu) {
           const int x = x0 + u;
           int lo = 0, hi = groups - 1;
           while (lo < hi) {  // the last group with pre <= x
@@ -525,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int cpp = a.c.page / kChunk, kept = max(0, min(listed, pages));
           const int chunks = a.kv_cnt == nullptr ? (n + kChunk - 1) / kChunk : kept * cpp;
           const int cu = (chunks + 1) / 2, per = cu + (dr.len + kUnit - 1) / kUnit;
-          const int rt = (x - pre[lo]) / per, at = x - pre[lo] - rt * per;
+          const int rt = (x - pre[lo]) / per, k = x - pre[lo] - rt * per;
           int page = 0, w = 0, draft = 0;
-          if (at >= cu) {
+          if (k >= cu) {
             draft = 1;
-            w = max(0, min(kChunk, dr.len - (at - cu) * kUnit - h * kChunk)) | (at - cu) << 16;
+            w = max(0, min(kChunk, dr.len - (k - cu) * kUnit - h * kChunk)) | (k - cu) << 16;
           } else {
-            const int c = 2 * at + h, e = c >> (a.c.page_shift - 6), sub = c & (cpp - 1);
+            const int c = 2 * k + h, e = c >> (a.c.page_shift - 6), sub = c & (cpp - 1);
             if (e < kept) {
               const int j = a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
               if (j >= 0 && j < pages) {
@@ -545,134 +539,154 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          int4 *rec = unit + 2 * (u % kUnits);
+          int4 *rec = unit + 2 * (u % (2 * kBatch));
           if (h == 0) rec[0] = make_int4(lo, rt, draft, lo - b * a.c.hkv);
           reinterpret_cast<int2 *>(rec + 1)[h] = make_int2(page, w);
         }
-        arrive_warp(batch_bar(first));
+        arrive_warp(C::B_UN + (first / kBatch) % 2);
       }
-    }
-    if (Q16 && (warp == 1 || warp == 2) && lane == 0) {
-      // ================================================================ copies of codes and scales
-      const int kv = warp - 1;
-      const uint8_t *scales = kv == 0 ? a.k_scales : a.v_scales;
-      const CUtensorMap *map = kv == 0 ? &tm_k : &tm_v;
-      uint32_t coded = 0, issued = 0;  // units with codes, slots filled
-      bool ok = true;
-      for (int n = 0; ok && n < x1 - x0; ++n) {
-        if (n % kBatch == 0 && !(ok = wait_parked(bar(batch_bar(n)), batch_parity(n), ctl))) break;
-        const int4 d0 = unit[2 * (n % kUnits)], d1 = unit[2 * (n % kUnits) + 1];
-        if (d0.z) continue;
-        const int full = C::B_XF + 2 * kv + (coded & 1);
-        if (coded >= 2 && !(ok = wait_parked(bar(C::B_XE + 2 * kv + (coded & 1)), ((coded >> 1) - 1) & 1, ctl))) break;
-        ptx::mbar_arrive_expect_tx(bar(full), C::SCALES);
-        const uint32_t ex = base + C::OFF_SCALE + (2 * kv + (coded & 1)) * C::SCALES;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int tile = (h == 0 ? d1.x : d1.z) * a.c.hkv + d0.w, row = ((h == 0 ? d1.y : d1.w) >> 16) * kChunk;
-          const uint8_t *sc = scales + static_cast<size_t>(tile) * a.c.page * C::PER;
-          bulk_copy(ex + h * kChunk, sc + row, kChunk, bar(full));
-          if constexpr (FMT == BSA_CACHE_E2M1)
-            bulk_copy(ex + 128 + h * kChunk * (D / 16), sc + a.c.page + row * (D / 16), kChunk * (D / 16), bar(full));
-        }
-        ++coded;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t slot = issued % C::SLOTS, use = issued / C::SLOTS;
-          if (use > 0 && !(ok = wait_parked(bar(C::B_CE + 8 * kv + slot), (use - 1) & 1, ctl))) break;
-          ptx::mbar_arrive_expect_tx(bar(C::B_CF + 8 * kv + slot), C::SLOT);
-          tma_load_3d(base + C::OFF_CODE + (kv * C::SLOTS + slot) * C::SLOT, map, bar(C::B_CF + 8 * kv + slot), 0,
-                      ((q < 2 ? d1.y : d1.w) >> 16) * kChunk + 32 * (q & 1), (q < 2 ? d1.x : d1.z) * a.c.hkv + d0.w);
-          ++issued;
-        }
-      }
-      if (!ok) {
-        // let copies in flight land before the CTA's shared memory is released
-        for (uint32_t x = issued > C::SLOTS ? issued - C::SLOTS : 0; x < issued; ++x)
-          drain_bar(bar(C::B_CF + 8 * kv + x % C::SLOTS), (x / C::SLOTS) & 1);
-        for (uint32_t x = coded > 2 ? coded - 2 : 0; x < coded; ++x) drain_bar(bar(C::B_XF + 2 * kv + (x & 1)), (x >> 1) & 1);
-      }
-    }
-    __syncwarp();
-  } else if (warp < 8) {
-    // ================================================================ loaders
-    ptx::setmaxnreg_dec<kRegLoad>();
-    const int kv = (warp - 4) >> 1;       // 0: K, 1: V
-    const int lt = (tid - 128) & 63;      // thread of the pair of warps
-    const int lw = warp - 4;
-    const int nu = x1 - x0;
-    [[maybe_unused]] const uint8_t *codes = kv == 0 ? a.k_codes : a.v_codes;
-    uint32_t pair_phase = 0;
-    auto sync_pair = [&]() -> bool {  // the two warps; bounded, unlike a named barrier
-      arrive_warp(C::B_LK + kv);
-      return wait_warp(C::B_LK + kv, pair_phase++ & 1);
+      return wait_warp(C::B_UN + (first / kBatch) % 2, (first / kBatch / 2) & 1);
     };
 
-    // The unit's codes (`coded`: its number among the units with codes) into the f16 tile at offset `dst`, the
-    // rows scaled against `ref`.  Warp j of the pair takes the quarters j and j + 2, a lane a row: its 16-byte
-    // pieces sit under the copy's swizzle and go under the tile's, both free of bank conflicts.
-    auto convert = [&](uint32_t dst, int ref, uint32_t coded, int n0, int n1) -> bool {
+    // ---- codes of a unit: thread (p, r0) of the pair takes piece p of the rows r0 + STEP * i, those of a
+    // chunk together, in groups of four pieces.  A thread reads back only what it has copied itself.
+    constexpr int NP = C::NP, STEP = Q16 ? 128 / NP : 1, GRP = C::GRP, NG = C::NG;
+    // (the group scales sit in registers, which wants constant indices)
+    constexpr int UNROLL = FMT == BSA_CACHE_E2M1 ? NG : 1;
+    const int p = lt % C::PP, r0 = lt / C::PP;
+    const uint32_t ring = C::OFF_CODE + static_cast<uint32_t>(tid - 128) * 16;  // slots of 128 pieces
+    struct {             // the group to be copied next
+      int unit, group;   // its unit and place there
+      const uint8_t *code[2];  // the thread's first piece of both chunks of the unit
+      int n[2];          // keys of the chunks
+    } next;
+    next.unit = 0;
+    next.group = 0;
+    next.code[0] = next.code[1] = codes;
+    next.n[0] = next.n[1] = 0;
+    // Copies the next group of the run into ring slot `slot` (zeros for absent rows), as one cp.async group.
+    auto copy_group = [&](int slot) {
       if constexpr (Q16) {
-        constexpr int PP = C::PP;
-        const uint32_t ex = C::OFF_SCALE + (2 * kv + (coded & 1)) * C::SCALES;
-        const uint32_t dx = static_cast<uint32_t>(lane & 7) * 16;
-        const uint32_t sx = C::RB == 128 ? (lane & 7) * 16u : C::RB == 64 ? ((lane >> 1) & 3) * 16u : ((lane >> 2) & 1) * 16u;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          const int q = 2 * k + (lw & 1), r = 32 * q + lane;
-          const uint32_t at = 4 * coded + q, slot = at % C::SLOTS, use = at / C::SLOTS;
-          if (!wait_warp(C::B_CF + 8 * kv + slot, use & 1)) return false;
-          const uint32_t from = C::OFF_CODE + (kv * C::SLOTS + slot) * C::SLOT + static_cast<uint32_t>(lane) * C::RB;
-          uint4 w4[PP];
+        if (next.unit < nu) {
+          if (next.group == 0) {
+            const int4 d0 = unit[2 * (next.unit % (2 * kBatch))], d1 = unit[2 * (next.unit % (2 * kBatch)) + 1];
 #pragma unroll
-          for (int p = 0; p < PP; ++p) w4[p] = *reinterpret_cast<const uint4 *>(sb + from + ((p * 16u) ^ sx));
-          arrive_warp(C::B_CE + 8 * kv + slot);
-          const bool live = (r & 63) < (q < 2 ? n0 : n1);
-          const uint32_t f = pow2_f16x2(static_cast<int>(sb[ex + r]) - ref + C::SHV);
-          const uint32_t row = dst + static_cast<uint32_t>(r) * 128;
-          if (!live) {  // the copy holds whatever the page has there
-#pragma unroll
-            for (int c = 0; c < C::NCH; ++c)
-#pragma unroll
-              for (int u = 0; u < 8; ++u) put16(row + c * C::CHUNK + u * 16, make_uint4(0u, 0u, 0u, 0u));
-          } else if constexpr (FMT == BSA_CACHE_E4M3) {
-#pragma unroll
-            for (int p = 0; p < PP; ++p) {
-              const uint32_t w[4] = {w4[p].x, w4[p].y, w4[p].z, w4[p].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                h[2 * x] = mul_f16x2(e4m3x2_f16(w[x]), f);
-                h[2 * x + 1] = mul_f16x2(e4m3x2_f16(w[x] >> 16), f);
-              }
-              const uint32_t to = row + (p >> 2) * C::CHUNK;
-              put16(to + ((32u * (p & 3)) ^ dx), make_uint4(h[0], h[1], h[2], h[3]));
-              put16(to + ((32u * (p & 3) + 16u) ^ dx), make_uint4(h[4], h[5], h[6], h[7]));
+            for (int h = 0; h < 2; ++h) {
+              const int pg = h == 0 ? d1.x : d1.z, w = h == 0 ? d1.y : d1.w;
+              next.n[h] = d0.z ? -1 : w & 0xFFFF;
+              next.code[h] = codes + ((static_cast<size_t>(pg) * a.c.hkv + d0.w) * a.c.page + (w >> 16) * kChunk + r0) *
+                                         C::RB + p * 16;
             }
-          } else {
-            const uint32_t gs = ex + 128 + static_cast<uint32_t>(r) * (D / 16);
+          }
+          if (next.n[0] >= 0) {  // (drafted tokens have no codes)
 #pragma unroll
-            for (int p = 0; p < PP; ++p) {
-              const uint32_t w[4] = {w4[p].x, w4[p].y, w4[p].z, w4[p].w};
-              const uint32_t g2 = mul_f16x2(e4m3x2_f16(*reinterpret_cast<const uint16_t *>(sb + gs + 2 * p)), f);
-              const uint32_t ga = __byte_perm(g2, g2, 0x1010), gb = __byte_perm(g2, g2, 0x3232);
-              const uint32_t to = row + (p >> 1) * C::CHUNK;
+            for (int e = 0; e < GRP; ++e) {
+              // a group of an NG > 1 unit lies in one chunk, one of an NG == 1 unit in both
+              const int h = NG > 1 ? (next.group >= NG / 2 ? 1 : 0) : (e >= GRP / 2 ? 1 : 0);
+              const int i = NG > 1 ? (next.group % (NG > 1 ? NG / 2 : 1)) * GRP + e : e % (GRP / 2);
+              const uint8_t *from = (h == 0 ? next.code[0] : next.code[1]) + i * (STEP * C::RB);
+              const int live = r0 + STEP * i < (h == 0 ? next.n[0] : next.n[1]) ? 16 : 0;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + ring + (slot * GRP + e) * 2048u),
+                           "l"(from), "r"(live)
+                           : "memory");
+            }
+          }
+          if (++next.group == NG) next.group = 0, ++next.unit;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+    };
+    // exponents of the rows 4 lane .. + 3 of this unit and the next; of the next also which bytes are there
+    // (applied only when they are used: it would wait for the load)
+    uint32_t ew = 0u, ew_next = 0u, ew_mask = 0u;
+    uint16_t gw[FMT == BSA_CACHE_E2M1 ? NP : 1], gw_next[FMT == BSA_CACHE_E2M1 ? NP : 1];  // group scales of the pieces
+    auto fetch_scales = [&](int u) {
+      if constexpr (Q16) {
+        const int4 d0 = unit[2 * (u % (2 * kBatch))], d1 = unit[2 * (u % (2 * kBatch)) + 1];
+        {
+          const int pg = lane < 16 ? d1.x : d1.z, w = lane < 16 ? d1.y : d1.w;
+          const int rr = 4 * (lane & 15), live = (d0.z ? 0 : w & 0xFFFF) - rr;
+          const uint8_t *sc = scales + (static_cast<size_t>(pg) * a.c.hkv + d0.w) * a.c.page * C::PER;
+          ew_mask = live >= 4 ? 0xffffffffu : live <= 0 ? 0u : (1u << (8 * live)) - 1u;
+          ew_next = 0u;
+          if (live > 0) ew_next = __ldg(reinterpret_cast<const uint32_t *>(sc + (w >> 16) * kChunk + rr));
+        }
+        if constexpr (FMT == BSA_CACHE_E2M1) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t g = x < 2 ? ga : gb;
-                put16(to + ((64u * (p & 1) + 16u * x) ^ dx),
-                      make_uint4(mul_f16x2(e2m1x2_f16(w[x]), g), mul_f16x2(e2m1x2_f16(w[x] >> 8), g),
-                                 mul_f16x2(e2m1x2_f16(w[x] >> 16), g), mul_f16x2(e2m1x2_f16(w[x] >> 24), g)));
-              }
+          for (int h = 0; h < 2; ++h) {
+            const int pg = h == 0 ? d1.x : d1.z, w = h == 0 ? d1.y : d1.w;
+            const int row = (w >> 16) * kChunk, n = d0.z ? 0 : w & 0xFFFF;
+            const uint8_t *sc = scales + (static_cast<size_t>(pg) * a.c.hkv + d0.w) * a.c.page * C::PER;
+#pragma unroll
+            for (int i = 0; i < NP / 2; ++i) {
+              const int rr = r0 + STEP * i;
+              gw_next[h * (NP / 2) + i] =
+                  rr < n ? __ldg(reinterpret_cast<const uint16_t *>(sc + a.c.page + (row + rr) * (D / 16) + 2 * p)) : 0;
             }
           }
         }
       }
-      return true;
     };
     auto top_byte = [&](uint32_t w) -> int {
       const uint32_t m = __vmaxu4(w, w >> 16);
       return static_cast<int>(__reduce_max_sync(0xffffffffu, max(m & 0xFFu, (m >> 8) & 0xFFu)));
+    };
+    int slot = 0;  // ring slot of the group to be read next
+    // The unit's codes into the f16 tile at offset `dst`, rows scaled against `ref`; refills the ring.
+    auto convert = [&](uint32_t dst, int ref) {
+      if constexpr (Q16) {
+        // f16 factors of this lane's rows 4 lane .. + 3 (an absent row has exponent 0 and zero codes)
+        auto factor = [&](int x) { return pow2_f16x2(static_cast<int>((ew >> (8 * x)) & 0xFFu) - ref + C::SHV); };
+        const uint32_t f01 = __byte_perm(factor(0), factor(1), 0x5410), f23 = __byte_perm(factor(2), factor(3), 0x5410);
+        const bool upper = (r0 & 2) != 0;                      // STEP is a multiple of 8: the same for every i
+        const uint32_t pick = (r0 & 1) ? 0x3232u : 0x1010u;
+#pragma unroll(UNROLL)
+        for (int gr = 0; gr < NG; ++gr) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(C::RING - 1) : "memory");
+          uint4 cw[GRP];
+          uint32_t fs[GRP];
+#pragma unroll
+          for (int e = 0; e < GRP; ++e) {
+            cw[e] = *reinterpret_cast<const uint4 *>(sb + ring + (slot * GRP + e) * 2048);
+            const int from = ((r0 + STEP * (gr * GRP + e)) >> 2) & 31;
+            const uint32_t fa = __shfl_sync(0xffffffffu, f01, from), fb = __shfl_sync(0xffffffffu, f23, from);
+            fs[e] = __byte_perm(upper ? fb : fa, 0u, pick);
+          }
+#pragma unroll
+          for (int e = 0; e < GRP; ++e) {
+            const uint32_t w[4] = {cw[e].x, cw[e].y, cw[e].z, cw[e].w};
+            const uint32_t at = dst + static_cast<uint32_t>(r0 + STEP * (gr * GRP + e)) * 128;
+            auto put = [&](int c, int u, uint4 v) {  // unit u of swizzle chunk c
+              put16(at + static_cast<uint32_t>(c) * C::CHUNK + static_cast<uint32_t>((u ^ (r0 & 7)) * 16), v);
+            };
+            if constexpr (FMT == BSA_CACHE_E4M3) {
+              uint32_t h[8];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                h[2 * x] = mul_f16x2(e4m3x2_f16(w[x]), fs[e]);
+                h[2 * x + 1] = mul_f16x2(e4m3x2_f16(w[x] >> 16), fs[e]);
+              }
+              const uint4 s0 = make_uint4(h[0], h[1], h[2], h[3]), s1 = make_uint4(h[4], h[5], h[6], h[7]);
+              // the upper pieces store their halves in the other order: no two lanes meet in a bank
+              const int u = 2 * (p & 3), sw = (p >> 2) & 1;
+              put(p >> 2, u + sw, sw ? s1 : s0);
+              put(p >> 2, u + 1 - sw, sw ? s0 : s1);
+            } else {
+              const uint32_t g2 = mul_f16x2(e4m3x2_f16(gw[gr * GRP + e]), fs[e]);
+              const uint32_t ga = __byte_perm(g2, g2, 0x1010), gb = __byte_perm(g2, g2, 0x3232);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t gs = x < 2 ? ga : gb;
+                put(p >> 1, 4 * (p & 1) + x,
+                    make_uint4(mul_f16x2(e2m1x2_f16(w[x]), gs), mul_f16x2(e2m1x2_f16(w[x] >> 8), gs),
+                               mul_f16x2(e2m1x2_f16(w[x] >> 16), gs), mul_f16x2(e2m1x2_f16(w[x] >> 24), gs)));
+              }
+            }
+          }
+          copy_group(slot);
+          slot = slot == C::RING - 1 ? 0 : slot + 1;
+        }
+      }
     };
     // bf16 rows by hand: `n` keys of chunk h, from `from` (row stride in elements); zeros past n
     auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f) {
@@ -724,18 +738,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       return max(8, (__float_as_int(am) >> 23) + C::SHV - 14);
     };
 
-    bool ok = true;
-    uint32_t coded = 0;  // units with codes so far
+    bool ok = nu == 0 || resolve(0);
+    if (Q16 && ok && nu > 0) {
+      for (int x = 0; x < C::RING; ++x) copy_group(x);
+      fetch_scales(0);
+    }
+    constexpr int AHEAD = Q16 ? (NG - 1 + C::RING) / NG : 1;  // the furthest unit met while one is filled
     int n_seg = 0, seg_end = 0, oref = 0;
     uint32_t copies = 0;  // units whose TMA copies were issued
     const int stages = kv == 0 ? C::KS : C::VS;
     int st = -1, round = -1;  // stage of the unit, and times the stage was filled before
     for (int n = 0; ok && n < nu; ++n) {
-      if (n % kBatch == 0) {
-        if (!(ok = wait_warp(batch_bar(n), batch_parity(n)))) break;
-        if (kv == 0) arrive_warp(C::B_UE + (n / kBatch) % kBatches);
-      }
-      const int4 d0 = unit[2 * (n % kUnits)], d1 = unit[2 * (n % kUnits) + 1];
+      const int4 d0 = unit[2 * (n % (2 * kBatch))], d1 = unit[2 * (n % (2 * kBatch)) + 1];
       const int g = d0.w;
       if (n == seg_end) {  // a new segment: its rows of Q, a quarter of them to each loader warp
         const Segment s = segment_at<C::NTQ>(a, pre, groups, x0 + n, x1);
@@ -780,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (Q16) arrive_warp(C::B_RS + (n_seg & 1));
         ++n_seg;
       }
+      if ((n + AHEAD) % kBatch == 0 && n + AHEAD < nu && !(ok = resolve(n + AHEAD))) break;
 
       // ---- the unit's scales
       const size_t dstride = static_cast<size_t>(a.c.hkv) * D;
@@ -788,16 +803,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (d0.z) drafted += ((static_cast<size_t>(drafts_of(a, d0.x / a.c.hkv).start) + (d1.y >> 16) * kUnit) * a.c.hkv + g) * D;
       int ref = 0;
       if constexpr (Q16) {
+        ew = ew_next & ew_mask;
+        if constexpr (FMT == BSA_CACHE_E2M1) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) gw[i] = gw_next[i];
+        }
         if (d0.z) {
           ref = draft_ref(drafted, dstride, n0 + n1, ok);
           if (!ok) break;
         } else {
-          if (!(ok = wait_warp(C::B_XF + 2 * kv + (coded & 1), (coded >> 1) & 1))) break;
-          const uint32_t ex = C::OFF_SCALE + (2 * kv + (coded & 1)) * C::SCALES;
-          const uint32_t e4 = *reinterpret_cast<const uint32_t *>(sb + ex + 4 * lane);  // of the rows 4 lane .. + 3
-          const int there = (lane < 16 ? n0 : n1) - 4 * (lane & 15);
-          // bytes past the last key are nobody's
-          ref = top_byte(there >= 4 ? e4 : there <= 0 ? 0u : e4 & ((1u << (8 * there)) - 1u));
+          ref = top_byte(ew);
         }
         if (kv == 0) {
           if (lt == 0) info_k[n % kInfo] = exp2f(static_cast<float>(ref - C::SHV - 127));
@@ -805,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ref = oref = max(oref, ref);
           if (lt == 0) info_v[n % kInfo] = oref;
         }
+        if (n + 1 < nu) fetch_scales(n + 1);
       }
       arrive_warp((kv == 0 ? C::B_IK : C::B_IV) + n % kInfo);
 
@@ -837,10 +853,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = Q16 ? pow2_biased(254 + C::SHV - ref) : 1.f;
         store_rows(tile, 0, drafted, dstride, n0, f);
         store_rows(tile, 1, drafted + kChunk * dstride, dstride, n1, f);
+        for (int gr = 0; Q16 && gr < NG; ++gr) {  // the unit's empty groups
+          copy_group(slot);
+          slot = slot == C::RING - 1 ? 0 : slot + 1;
+        }
       } else if constexpr (Q16) {
-        if (!(ok = convert(tile, ref, coded, n0, n1))) break;
-        arrive_warp(C::B_XE + 2 * kv + (coded & 1));
-        ++coded;
+        convert(tile, ref);
       } else {
         if (by_tma != 3) {
 #pragma unroll 1
@@ -855,6 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (by_tma != 3) ptx::fence_proxy_async_smem();  // what was written by hand
       arrive_warp(full);
     }
+    if (Q16) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!Q16 && *abort_flag && (lw & 1) == 0 && lane == 0) {
       // let copies in flight land before the CTA's shared memory is released
       const uint32_t last = static_cast<uint32_t>(stages);
@@ -887,11 +906,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int oref = 0;  // O's unit (8- and 4-bit caches)
       int done = 0;  // units of this lane in the segment
       for (int i = 0; i < s.units; ++i, ++n) {
-        if (n % kBatch == 0 && !(ok = wait_warp(batch_bar(n), batch_parity(n)))) break;
+        if (n % kBatch == 0 && !(ok = wait_warp(C::B_UN + (n / kBatch) % 2, (n / kBatch / 2) & 1))) break;
         if (!(ok = wait_warp(C::B_IK + n % kInfo, (n / kInfo) & 1))) break;
         if (!(ok = wait_warp(C::B_IV + n % kInfo, (n / kInfo) & 1))) break;
         if (!PAIR && (i & 1) != t) continue;
-        const int4 d0 = unit[2 * (n % kUnits)], d1 = unit[2 * (n % kUnits) + 1];
+        const int4 d0 = unit[2 * (n % (2 * kBatch))], d1 = unit[2 * (n % (2 * kBatch)) + 1];
         const int n0 = d1.y & 0xFFFF, n1 = d1.w & 0xFFFF;
         float scl = rs;
         int oref_new = 0;
@@ -1207,21 +1226,15 @@ Workspace workspace_layout(int d) {
   return w;
 }
 
-// The cache's codes [pages * hkv, page, row] for TMA.  bf16: boxes of 64 dimensions and 128 rows (64 where a
-// page has no more), 128-byte swizzle.  Codes: boxes of 32 whole rows, swizzled over the row's bytes.
-bool code_map(EncodeTiledFn fn, CUtensorMap *map, const void *codes, const CacheDims &c) {
-  const bool wide = c.format == BSA_CACHE_BF16;
-  const cuuint64_t row = static_cast<cuuint64_t>(c.row);
-  const cuuint64_t dims[3] = {wide ? row / 2 : row, static_cast<cuuint64_t>(c.page),
+// Rows of a bf16 cache [pages * hkv, page, d]: box of 64 dimensions and 128 rows, or 64 where a page has no
+// more; 128-byte swizzle.
+bool chunk_map(EncodeTiledFn fn, CUtensorMap *map, const void *codes, const CacheDims &c) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page),
                               static_cast<cuuint64_t>(c.pages) * c.hkv};
-  const cuuint64_t strides[2] = {row, static_cast<cuuint64_t>(c.page) * row};
-  const cuuint32_t box[3] = {wide ? 64u : static_cast<cuuint32_t>(row), wide ? (c.page >= kUnit ? 128u : 64u) : 32u, 1u};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUtensorMapSwizzle swizzle = wide || row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : row == 64        ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                        : CU_TENSOR_MAP_SWIZZLE_32B;
-  return fn(map, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d) * 2, static_cast<cuuint64_t>(c.page) * c.d * 2};
+  const cuuint32_t box[3] = {64u, c.page >= kUnit ? 128u : 64u, 1u}, estr[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1229,10 +1242,12 @@ template <int D, int FMT, bool PAIR>
 bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   using C = Cfg<D, FMT, PAIR>;
   CUtensorMap mk{}, mv{};
-  cudaError_t e = cudaSuccess;
-  EncodeTiledFn fn = tensor_map_encoder(&e);
-  if (fn == nullptr || e != cudaSuccess || !code_map(fn, &mk, a.k_codes, a.c) || !code_map(fn, &mv, a.v_codes, a.c))
-    return BSA_ERR_CUDA;
+  if (!C::Q16) {
+    cudaError_t e = cudaSuccess;
+    EncodeTiledFn fn = tensor_map_encoder(&e);
+    if (fn == nullptr || e != cudaSuccess || !chunk_map(fn, &mk, a.k_codes, a.c) || !chunk_map(fn, &mv, a.v_codes, a.c))
+      return BSA_ERR_CUDA;
+  }
   const Workspace ws = workspace_layout(D);
   char *base = static_cast<char *>(workspace);
   float *part_o = reinterpret_cast<float *>(base + ws.part_o), *part_ml = reinterpret_cast<float *>(base + ws.part_ml);
@@ -1254,7 +1269,7 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const int shared = static_cast<int>(tiles < kSms - 1 ? tiles : kSms - 1);  // at most: a run boundary each
   const int most = rows < kRows * C::NTQ ? rows : kRows * C::NTQ;
   const dim3 grid(shared, D / kCombineDims, (most + kCombineRows - 1) / kCombineRows);
-  e = launch_after(tree_mma_combine_kernel<D, PAIR>, grid, kCombineWarps * 32, stream, a,
+  const cudaError_t e = launch_after(tree_mma_combine_kernel<D, PAIR>, grid, kCombineWarps * 32, stream, a,
                                      static_cast<const float *>(part_o), static_cast<const float *>(part_ml),
                                      static_cast<const TreeRun *>(runs));
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
