@@ -14,11 +14,13 @@
 //          units; their results are merged when the segment ends
 // Warps:  0      TMEM owner; one thread issues S_t = Q_t K^T (both operands in
 //                shared memory) and O_t += P_t V (P from TMEM, over S_t)
+//         1      looks up the units (page of every chunk, keys there), 32 at a time and a batch ahead
 //         4-5    loaders of K, 6-7 of V: bf16 pages by TMA; 8- and 4-bit codes by
 //                cp.async into a ring of each thread's own pieces, from there into
-//                f16 tiles with the 128-byte swizzle; Q, partial chunks and drafted
+//                f16 tiles with the 128-byte swizzle; partial chunks and drafted
 //                tokens by hand
-//         8-11, 12-15  the softmax lanes, one thread per query row
+//         8-11, 12-15  the softmax lanes, one thread per query row; a lane also brings in its
+//                rows of Q, the next segment's before it writes out the last one's result
 //
 // An 8- or 4-bit cache is computed in f16.  With e the exponent of a key's row and
 // kref the largest of the unit, K' = code * 2^(e - kref + SHV) is exact down to
@@ -55,7 +57,8 @@ constexpr int kThreads = 512;
 constexpr int kRows = 128;     // rows of a tile
 constexpr int kUnit = 128;     // keys of a unit
 constexpr int kChunk = 64;     // keys of a page chunk
-constexpr int kBatch = 32;     // units resolved at a time, one chunk per thread of the K loaders
+constexpr int kBatch = 32;     // units looked up at a time, one per lane
+constexpr int kLists = 3;      // batches kept
 constexpr int kInfo = 8;       // units whose scales are kept
 constexpr int kRegMma = 40, kRegLoad = 88, kRegSoft = 192;
 static_assert(128 * (kRegMma + kRegLoad + 2 * kRegSoft) <= kThreads * 128, "register split exceeds the launch");
@@ -85,16 +88,16 @@ struct Cfg {
   static constexpr uint32_t OFF_CODE = OFF_V + VS * TILE;
   static constexpr uint32_t OFF_BAR = OFF_CODE + CODES;
   static constexpr int NPC = 4;                    // P released in chunks of 32 keys
-  static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS,
+  static constexpr int B_QF = 0, B_QE = 2, B_KF = 3, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS,
                        B_SF = B_VE + VS, B_PR = B_SF + 2, B_OD = B_PR + 2 * NPC, B_OE = B_OD + 2, B_UN = B_OE + 2,
-                       B_IK = B_UN + 2, B_IV = B_IK + kInfo, B_RS = B_IV + kInfo, B_LK = B_RS + 2, B_LV = B_LK + 1,
-                       B_LA = B_LV + 1, B_LB = B_LA + 1, B_FIN = B_LB + 1, NBARS = B_FIN + 1;
+                       B_UG = B_UN + kLists, B_IK = B_UG + 1, B_IV = B_IK + kInfo, B_RS = B_IV + kInfo, B_LK = B_RS + 2,
+                       B_LV = B_LK + 1, B_LA = B_LV + 1, B_LB = B_LA + 1, B_FIN = B_LB + 1, NBARS = B_FIN + 1;
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag, scan sums
   static constexpr uint32_t OFF_INFO = OFF_MISC + 128;                        // [kInfo] K's scale, [kInfo] oref
   static constexpr uint32_t OFF_ROWS = OFF_INFO + kInfo * 8;                  // [2][NTQ * 128] row scales of Q
   static constexpr uint32_t OFF_RED = OFF_ROWS + 2 * NTQ * 128 * 4;           // [4] loader maxima
-  static constexpr uint32_t OFF_UNIT = OFF_RED + 32;                          // [2][kBatch] {int4, int4}
-  static constexpr uint32_t OFF_PRE = OFF_UNIT + 2 * kBatch * 32;             // [groups + 1] first unit
+  static constexpr uint32_t OFF_UNIT = OFF_RED + 32;                          // [kLists][kBatch] {int4, int4}
+  static constexpr uint32_t OFF_PRE = OFF_UNIT + kLists * kBatch * 32;        // [groups + 1] first unit
   static size_t smem(int groups) { return OFF_PRE + static_cast<size_t>(groups + 1) * 4 + 1024; }
   static constexpr uint32_t IDESC_S = Q16 ? ptx::idesc_bf16_f32(128, 128, false) & ~((1u << 7) | (1u << 10))
                                           : ptx::idesc_bf16_f32(128, 128, false);
@@ -133,6 +136,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ float amax8(const uint4 &v) {  // of eight bf16
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float am = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+  return am;
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -309,12 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int x = 0; x < C::NBARS; ++x) {
-      // arrivals: 1 of a commit, 2 of the K or the V loaders' warps, 4 of all loaders or a softmax lane
+      // arrivals: 1 of a commit or the lookup warp, 2 of the K or the V loaders' warps, 4 of a softmax lane, 8 of both
       uint32_t count = 1;
-      if (x == C::B_QF || (x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_UN) ||
-          (x >= C::B_RS && x < C::B_LK) || x == C::B_LA || x == C::B_LB)
+      if (x < C::B_QE || (x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_UN) || x == C::B_LA || x == C::B_LB)
         count = 4;
-      else if ((x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) || (x >= C::B_UN && x < C::B_RS) ||
+      else if (x >= C::B_RS && x < C::B_LK)
+        count = 8;
+      else if ((x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) || (x >= C::B_UG && x < C::B_RS) ||
                x == C::B_LK || x == C::B_LV)
         count = 2;
       ptx::mbar_init(bar(x), count);
@@ -429,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Segment s = segment_at<C::NTQ>(a, pre, groups, x, x1);
         x += s.units;
         if (!(ok = wait_parked(bar(C::B_QF), n_seg & 1, ctl))) break;
-        ++n_seg;
+        if (!PAIR && !(ok = wait_parked(bar(C::B_QF + 1), n_seg & 1, ctl))) break;
         for (int i = 0; i < s.units; ++i, ++n) {
           const uint32_t ks = n % C::KS, vs = n % C::VS;
           const bool last = i == s.units - 1;
@@ -443,9 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = issue_pv(1, pvs, i > 1))) break;
               ptx::mma_commit(bar(C::B_VE + pvs));
             }
+            if (i == 0) {
+              if (!(ok = wait_parked(bar(C::B_QF + 1), n_seg & 1, ctl))) break;
+              ptx::tc_fence_after();
+            }
             issue_s(1, ks);
             ptx::mma_commit(bar(C::B_KE + ks));
-            if (last) ptx::mma_commit(bar(C::B_QE));
             // V(n) has two stages only and is refilled late: it is waited for as late as possible
             if (!(ok = wait_parked(bar(C::B_VF + vs), (n / C::VS) & 1, ctl))) break;
             if (i == 0 && !(ok = o_free(0))) break;
@@ -475,11 +490,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
           }
         }
+        ++n_seg;
       }
       if (!ok) {
         // every MMA issued so far must finish before TMEM is released
         ptx::mma_commit(bar(C::B_FIN));
         drain_bar(bar(C::B_FIN), 0);
+      }
+    }
+    if (warp == 1) {
+      // ================================================================ lookups
+      // Per unit: {group, row tile, 1 for drafted tokens, KV head} and the page and (keys | chunk of the page <<
+      // 16) of both chunks.  Batch f replaces batch f - 3, which everyone has left once the K loaders have begun
+      // batch f - 1: the other warps are at most four units behind them.
+      const int nu = x1 - x0;
+      for (int f = 0; f * kBatch < nu; ++f) {
+        if (f >= 2 && !wait_warp(C::B_UG, f & 1)) break;
+        const int u = f * kBatch + lane;
+        if (u < nu) {
+          const int x = x0 + u;
+          int lo = 0, hi = groups - 1;
+          while (lo < hi) {  // the last group with pre <= x
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] <= x) lo = mid;
+            else hi = mid - 1;
+          }
+          const int b = lo / a.c.hkv;
+          // three rounds of memory: these three together, the list's entries, the table's
+          const int listed = a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + lo);
+          const int n = cached_of(a, b);
+          const Span dr = drafts_of(a, b);
+          const int pages = (n + a.c.page - 1) >> a.c.page_shift;
+          const int cpp = a.c.page / kChunk, kept = max(0, min(listed, pages));
+          const int chunks = a.kv_cnt == nullptr ? (n + kChunk - 1) / kChunk : kept * cpp;
+          const int cu = (chunks + 1) / 2, per = cu + (dr.len + kUnit - 1) / kUnit;
+          const int rt = (x - pre[lo]) / per, k = x - pre[lo] - rt * per;
+          int page[2] = {0, 0}, w[2] = {0, 0};
+          const int draft = k >= cu ? 1 : 0;
+          if (draft) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[h] = max(0, min(kChunk, dr.len - (k - cu) * kUnit - h * kChunk)) | (k - cu) << 16;
+          } else {
+            int j[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = (2 * k + h) >> (a.c.page_shift - 6);
+              j[h] = e >= kept ? -1 : a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (j[h] >= 0 && j[h] < pages) {
+                const int sub = (2 * k + h) & (cpp - 1);
+                const int pg = __ldg(a.table + static_cast<size_t>(b) * a.table_stride + j[h]);
+                if (pg >= 0 && pg < a.c.pages) {
+                  page[h] = pg;
+                  w[h] = max(0, min(kChunk, n - j[h] * a.c.page - sub * kChunk)) | sub << 16;
+                } else if (a.status != nullptr) {
+                  atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
+                }
+              }
+            }
+          }
+          int4 *rec = unit + 2 * (u % (kLists * kBatch));
+          rec[0] = make_int4(lo, rt, draft, lo - b * a.c.hkv);
+          rec[1] = make_int4(page[0], w[0], page[1], w[1]);
+        }
+        arrive_warp(C::B_UN + f % kLists);
       }
     }
     __syncwarp();
@@ -495,57 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto sync_pair = [&]() -> bool {  // the two warps; bounded, unlike a named barrier
       arrive_warp(C::B_LK + kv);
       return wait_warp(C::B_LK + kv, pair_phase++ & 1);
-    };
-
-    // Units first .. first + kBatch - 1 of the run, one chunk per thread of the K loaders: {group, row
-    // tile, 1 for drafted tokens, KV head} and the page and (keys | chunk of the page << 16) of both chunks.
-    auto resolve = [&](int first) -> bool {
-      if (kv == 0) {
-        const int u = first + (lt >> 1), h = lt & 1;
-        if (u < nu) {
-          const int x = x0 + u;
-          int lo = 0, hi = groups - 1;
-          while (lo < hi) {  // the last group with pre <= x
-            const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] <= x) lo = mid;
-            else hi = mid - 1;
-          }
-          const int b = lo / a.c.hkv;
-          // three rounds of memory: these three together, the list's entry, the table's
-          const int listed = a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + lo);
-          const int n = cached_of(a, b);
-          const Span dr = drafts_of(a, b);
-          const int pages = (n + a.c.page - 1) >> a.c.page_shift;
-          const int cpp = a.c.page / kChunk, kept = max(0, min(listed, pages));
-          const int chunks = a.kv_cnt == nullptr ? (n + kChunk - 1) / kChunk : kept * cpp;
-          const int cu = (chunks + 1) / 2, per = cu + (dr.len + kUnit - 1) / kUnit;
-          const int rt = (x - pre[lo]) / per, k = x - pre[lo] - rt * per;
-          int page = 0, w = 0, draft = 0;
-          if (k >= cu) {
-            draft = 1;
-            w = max(0, min(kChunk, dr.len - (k - cu) * kUnit - h * kChunk)) | (k - cu) << 16;
-          } else {
-            const int c = 2 * k + h, e = c >> (a.c.page_shift - 6), sub = c & (cpp - 1);
-            if (e < kept) {
-              const int j = a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
-              if (j >= 0 && j < pages) {
-                const int pg = __ldg(a.table + static_cast<size_t>(b) * a.table_stride + j);
-                if (pg >= 0 && pg < a.c.pages) {
-                  page = pg;
-                  w = max(0, min(kChunk, n - j * a.c.page - sub * kChunk)) | sub << 16;
-                } else if (a.status != nullptr) {
-                  atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-                }
-              }
-            }
-          }
-          int4 *rec = unit + 2 * (u % (2 * kBatch));
-          if (h == 0) rec[0] = make_int4(lo, rt, draft, lo - b * a.c.hkv);
-          reinterpret_cast<int2 *>(rec + 1)[h] = make_int2(page, w);
-        }
-        arrive_warp(C::B_UN + (first / kBatch) % 2);
-      }
-      return wait_warp(C::B_UN + (first / kBatch) % 2, (first / kBatch / 2) & 1);
     };
 
     // ---- codes of a unit: thread (p, r0) of the pair takes piece p of the rows r0 + STEP * i, those of a
@@ -569,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (Q16) {
         if (next.unit < nu) {
           if (next.group == 0) {
-            const int4 d0 = unit[2 * (next.unit % (2 * kBatch))], d1 = unit[2 * (next.unit % (2 * kBatch)) + 1];
+            const int4 d0 = unit[2 * (next.unit % (kLists * kBatch))], d1 = unit[2 * (next.unit % (kLists * kBatch)) + 1];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int pg = h == 0 ? d1.x : d1.z, w = h == 0 ? d1.y : d1.w;
@@ -602,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint16_t gw[FMT == BSA_CACHE_E2M1 ? NP : 1], gw_next[FMT == BSA_CACHE_E2M1 ? NP : 1];  // group scales of the pieces
     auto fetch_scales = [&](int u) {
       if constexpr (Q16) {
-        const int4 d0 = unit[2 * (u % (2 * kBatch))], d1 = unit[2 * (u % (2 * kBatch)) + 1];
+        const int4 d0 = unit[2 * (u % (kLists * kBatch))], d1 = unit[2 * (u % (kLists * kBatch)) + 1];
         {
           const int pg = lane < 16 ? d1.x : d1.z, w = lane < 16 ? d1.y : d1.w;
           const int rr = 4 * (lane & 15), live = (d0.z ? 0 : w & 0xFFFF) - rr;
@@ -714,14 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    auto amax8 = [](const uint4 &v) -> float {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float am = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-      return am;
-    };
     // the exponent reference of a unit of drafted rows: its largest element lands in [2^14, 2^15)
     auto draft_ref = [&](const uint16_t *from, size_t stride, int n, bool &ok) -> int {
       constexpr int PR = D / 8;
@@ -738,63 +755,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       return max(8, (__float_as_int(am) >> 23) + C::SHV - 14);
     };
 
-    bool ok = nu == 0 || resolve(0);
+    // the records of the batch that begins with unit u
+    auto looked_up = [&](int u) -> bool { return wait_warp(C::B_UN + u / kBatch % kLists, (u / kBatch / kLists) & 1); };
+    bool ok = nu == 0 || looked_up(0);
     if (Q16 && ok && nu > 0) {
       for (int x = 0; x < C::RING; ++x) copy_group(x);
       fetch_scales(0);
     }
     constexpr int AHEAD = Q16 ? (NG - 1 + C::RING) / NG : 1;  // the furthest unit met while one is filled
-    int n_seg = 0, seg_end = 0, oref = 0;
+    int seg_group = -1, seg_tile = -1, oref = 0;
     uint32_t copies = 0;  // units whose TMA copies were issued
     const int stages = kv == 0 ? C::KS : C::VS;
     int st = -1, round = -1;  // stage of the unit, and times the stage was filled before
     for (int n = 0; ok && n < nu; ++n) {
-      const int4 d0 = unit[2 * (n % (2 * kBatch))], d1 = unit[2 * (n % (2 * kBatch)) + 1];
+      const int4 d0 = unit[2 * (n % (kLists * kBatch))], d1 = unit[2 * (n % (kLists * kBatch)) + 1];
       const int g = d0.w;
-      if (n == seg_end) {  // a new segment: its rows of Q, a quarter of them to each loader warp
-        const Segment s = segment_at<C::NTQ>(a, pre, groups, x0 + n, x1);
-        const Span dr = drafts_of(a, s.grp / a.c.hkv);
-        seg_end = n + s.units;
-        oref = 0;
-        if (n_seg > 0 && !(ok = wait_warp(C::B_QE, (n_seg - 1) & 1))) break;
-        constexpr int LPR = D / 8, R = 32 / LPR, U = 8;  // lanes of a row, rows of a step, steps in flight
-        const int q = lane % LPR;
-#pragma unroll 1
-        for (int r = lw * 32 * C::NTQ; r < (lw + 1) * 32 * C::NTQ; r += R * U) {
-          uint4 v[U];
-#pragma unroll
-          for (int e = 0; e < U; ++e) {
-            const int row = s.rt * C::NTQ * kRows + r + e * R + lane / LPR, tok = row / G;
-            v[e] = make_uint4(0u, 0u, 0u, 0u);
-            if (tok < dr.len)
-              v[e] = __ldg(reinterpret_cast<const uint4 *>(
-                  a.q + (static_cast<size_t>(dr.start + tok) * a.hq + g * G + row % G) * D + q * 8));
-          }
-#pragma unroll
-          for (int e = 0; e < U; ++e) {
-            const int rr = r + e * R + lane / LPR;
-            if constexpr (Q16) {
-              float am = amax8(v[e]);
-#pragma unroll
-              for (int o = LPR / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-              const int ex = max(1, min(253, 268 - (__float_as_int(am) >> 23)));
-              const float f = pow2_biased(ex);
-              if (q == 0) row_scale[(n_seg & 1) * C::NTQ * 128 + rr] = pow2_biased(254 - ex);
-              uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = pack_f16x2(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x] & 0xFFFF0000u) * f);
-              v[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            put16(swizzled(C::OFF_Q + (rr >> 7) * C::TILE, q >> 3, rr & 127, q & 7), v[e]);
-          }
-        }
-        ptx::fence_proxy_async_smem();
-        arrive_warp(C::B_QF);
-        if constexpr (Q16) arrive_warp(C::B_RS + (n_seg & 1));
-        ++n_seg;
-      }
-      if ((n + AHEAD) % kBatch == 0 && n + AHEAD < nu && !(ok = resolve(n + AHEAD))) break;
+      if (d0.x != seg_group || d0.y != seg_tile) seg_group = d0.x, seg_tile = d0.y, oref = 0;  // a new segment
+      if (kv == 0 && n > 0 && n % kBatch == 0) arrive_warp(C::B_UG);
+      if ((n + AHEAD) % kBatch == 0 && n + AHEAD < nu && !(ok = looked_up(n + AHEAD))) break;
 
       // ---- the unit's scales
       const size_t dstride = static_cast<size_t>(a.c.hkv) * D;
@@ -889,28 +867,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (sub << 5) + lane;  // query row = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(sub << 5) << 16;
     const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + C::TM_O + t * 128;
+    // A segment's rows of Q, this warp's part of them: its own rows, or half of them where both lanes have the
+    // same rows.  The lane has seen the last S of the segment before (of both lanes: B_QE).
+    auto load_q = [&](const Segment &s, uint32_t seg) {
+      constexpr int LPR = D / 8, R = 32 / LPR, ROWS = PAIR ? 32 : 16;  // lanes of a row, rows of a step, of the warp
+      constexpr int U = ROWS / R < 8 ? ROWS / R : 8;                   // steps in flight
+      const Span dr = drafts_of(a, s.grp / a.c.hkv);
+      const int q = lane % LPR, first = PAIR ? t * kRows + sub * 32 : sub * 32 + t * 16, g = s.grp % a.c.hkv;
+#pragma unroll 1
+      for (int r = first; r < first + ROWS; r += R * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const int row = s.rt * C::NTQ * kRows + r + e * R + lane / LPR, tok = row / G;
+          v[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (tok < dr.len)
+            v[e] = __ldg(reinterpret_cast<const uint4 *>(
+                a.q + (static_cast<size_t>(dr.start + tok) * a.hq + g * G + row % G) * D + q * 8));
+        }
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const int rr = r + e * R + lane / LPR;
+          if constexpr (Q16) {
+            float am = amax8(v[e]);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            const int ex = max(1, min(253, 268 - (__float_as_int(am) >> 23)));
+            const float f = pow2_biased(ex);
+            if (q == 0) row_scale[(seg & 1) * C::NTQ * 128 + rr] = pow2_biased(254 - ex);
+            uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              w[x] = pack_f16x2(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x] & 0xFFFF0000u) * f);
+            v[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          put16(swizzled(C::OFF_Q + (rr >> 7) * C::TILE, q >> 3, rr & 127, q & 7), v[e]);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      arrive_warp(C::B_QF + t);
+      if constexpr (Q16 && !PAIR) arrive_warp(C::B_RS + (seg & 1));
+    };
     bool ok = true;
     uint32_t n = 0, mine = 0, n_seg = 0, lane_segs = 0;  // units of the run, of this lane; segments
+    Segment s{};
+    if (x0 < x1) {
+      s = segment_at<C::NTQ>(a, pre, groups, x0, x1);
+      load_q(s, 0);
+    }
     for (int x = x0; ok && x < x1; ++n_seg) {
-      const Segment s = segment_at<C::NTQ>(a, pre, groups, x, x1);
+      if (n_seg > 0) s = segment_at<C::NTQ>(a, pre, groups, x, x1);
       x += s.units;
       const Span dr = drafts_of(a, s.grp / a.c.hkv);
       const int row = (s.rt * C::NTQ + (PAIR ? t : 0)) * kRows + r, tok = row / G;
       const bool live = tok < dr.len;
       float rs = a.scale_log2;
       if constexpr (Q16) {
-        if (!(ok = wait_warp(C::B_RS + (n_seg & 1), (n_seg >> 1) & 1))) break;
+        if (!PAIR && !(ok = wait_warp(C::B_RS + (n_seg & 1), (n_seg >> 1) & 1))) break;
         rs *= row_scale[((n_seg & 1) * C::NTQ + (PAIR ? t : 0)) * 128 + r];
       }
       float m = -INFINITY, l = 0.f;
       int oref = 0;  // O's unit (8- and 4-bit caches)
       int done = 0;  // units of this lane in the segment
       for (int i = 0; i < s.units; ++i, ++n) {
-        if (n % kBatch == 0 && !(ok = wait_warp(C::B_UN + (n / kBatch) % 2, (n / kBatch / 2) & 1))) break;
+        if (n % kBatch == 0 && !(ok = wait_warp(C::B_UN + n / kBatch % kLists, (n / kBatch / kLists) & 1))) break;
         if (!(ok = wait_warp(C::B_IK + n % kInfo, (n / kInfo) & 1))) break;
         if (!(ok = wait_warp(C::B_IV + n % kInfo, (n / kInfo) & 1))) break;
         if (!PAIR && (i & 1) != t) continue;
-        const int4 d0 = unit[2 * (n % (2 * kBatch))], d1 = unit[2 * (n % (2 * kBatch)) + 1];
+        const int4 d0 = unit[2 * (n % (kLists * kBatch))], d1 = unit[2 * (n % (kLists * kBatch)) + 1];
         const int n0 = d1.y & 0xFFFF, n1 = d1.w & 0xFFFF;
         float scl = rs;
         int oref_new = 0;
@@ -1017,6 +1041,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done;
       }
       if (!ok) break;
+      if (x < x1) {  // the next segment's rows, so that its first products run beside what follows
+        if (!PAIR && !(ok = wait_warp(C::B_QE, n_seg & 1))) break;
+        load_q(segment_at<C::NTQ>(a, pre, groups, x, x1), n_seg + 1);
+      }
 
       // ---- the segment's result of this lane: rows to the output, or a part for the combine
       if (done > 0) {
