@@ -15,11 +15,11 @@
 // Warps:  0      TMEM owner; one thread issues S_t = Q_t K^T (both operands in
 //                shared memory) and O_t += P_t V (P from TMEM, over S_t)
 //         1      looks up the units (page of every chunk, keys there), 32 at a time and a batch ahead
-//         4-5    loaders of K, 6-7 of V: bf16 pages by TMA; 8- and 4-bit codes by
+//         4-7    loaders of K, 8-11 of V: bf16 pages by TMA; 8- and 4-bit codes by
 //                cp.async into a ring of each thread's own pieces, from there into
 //                f16 tiles with the 128-byte swizzle; partial chunks and drafted
 //                tokens by hand
-//         8-11, 12-15  the softmax lanes, one thread per query row; a lane also brings in its
+//         12-15, 16-19  the softmax lanes, one thread per query row; a lane also brings in its
 //                rows of Q, the next segment's before it writes out the last one's result
 //
 // An 8- or 4-bit cache is computed in f16.  With e the exponent of a key's row and
@@ -31,9 +31,16 @@
 // per unit.  P' = 2^(x - m + SHIFT) with the reference m at most 2^TH below the true
 // maximum, so P' <= 2^15.  Row sums are fp32 from unrounded values.
 //
-// What bounds it: with two row tiles a unit is 32 MMAs of 64 cycles (2048 cycles);
-// the f16 conversion of a unit writes 64 KB of shared memory beside the MMAs' own
-// 192 KB of operand reads.  Every mbarrier wait is bounded, as in the prefill kernel.
+// What bounds it: with two row tiles a unit is 32 MMAs of 64 cycles, 2048 cycles.  8 sequences of up to
+// 32768 cached tokens, 64 drafted tokens, 32 / 4 heads of 128 (84 units a CTA): bf16 206 us, e4m3 and e2m1
+// 268 (0.91 and 0.72 PFLOP/s; the MMAs alone 109), so 4600 to 6000 cycles a unit.  Half of them the issuing
+// thread waits for a softmax lane; it hardly ever waits for keys.  The lanes have a thousand instructions a
+// unit and share the schedulers with the conversion, and the instruction cache shows: a ready warp waits
+// for its code more often than for a pipe.  So code is kept short: logits are taken in two halves (the second
+// is read from TMEM again), which also frees the registers for eight loader warps instead of four
+// (e2m1 327 -> 268).  Measured and not kept: two threads a row (297), the conversion unrolled (355), deeper
+// rings (no change), waits that poll instead of parking (+4 %).
+// Every mbarrier wait is bounded, as in the prefill kernel.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -53,15 +60,16 @@ using wait::Ctl;
 using wait::drain_bar;
 
 constexpr int kSms = 152;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kLaunchRegs = 96;  // per thread
 constexpr int kRows = 128;     // rows of a tile
 constexpr int kUnit = 128;     // keys of a unit
 constexpr int kChunk = 64;     // keys of a page chunk
 constexpr int kBatch = 32;     // units looked up at a time, one per lane
 constexpr int kLists = 3;      // batches kept
 constexpr int kInfo = 8;       // units whose scales are kept
-constexpr int kRegMma = 40, kRegLoad = 88, kRegSoft = 192;
-static_assert(128 * (kRegMma + kRegLoad + 2 * kRegSoft) <= kThreads * 128, "register split exceeds the launch");
+constexpr int kRegMma = 56, kRegLoad = 80, kRegSoft = 128;
+static_assert(128 * (kRegMma + 2 * kRegLoad + 2 * kRegSoft) <= kThreads * kLaunchRegs, "register split exceeds the launch");
 
 template <int D, int FMT, bool PAIR>
 struct Cfg {
@@ -69,7 +77,7 @@ struct Cfg {
   static constexpr int RB = FMT == BSA_CACHE_BF16 ? 2 * D : FMT == BSA_CACHE_E4M3 ? D : D / 2;
   static constexpr int PER = FMT == BSA_CACHE_BF16 ? 0 : FMT == BSA_CACHE_E4M3 ? 1 : 1 + D / 16;
   static constexpr int PP = Q16 ? RB / 16 : 1;     // 16-byte pieces of a code row
-  static constexpr int NP = Q16 ? 2 * PP : 1;      // pieces of a unit per loader thread
+  static constexpr int NP = Q16 ? PP : 1;          // pieces of a unit per loader thread
   static constexpr int SHV = FMT == BSA_CACHE_E4M3 ? 6 : 4;  // 448 * 2^6 and 2688 * 2^4 stay below 2^16
   static constexpr int TH = Q16 ? 4 : 8;           // log2 of how far the reference may lag the maximum
   static constexpr int SHIFT = Q16 ? 15 - TH : 0;
@@ -78,10 +86,10 @@ struct Cfg {
   static constexpr uint32_t TILE = 128u * D * 2;
   static constexpr uint32_t CHUNK = 128u * 128;    // one swizzle chunk column of a tile
   static constexpr int KS = 2, VS = PAIR || Q16 ? 2 : 3;
-  static constexpr int GRP = 4;                    // pieces of a cp.async group
+  static constexpr int GRP = 2;                    // pieces of a cp.async group
   static constexpr int NG = Q16 ? NP / GRP : 1;    // groups of a unit
   static constexpr int RING = 3;                   // groups in flight per thread
-  static constexpr uint32_t CODES = Q16 ? 128u * RING * GRP * 16 : 0;  // of the four loader warps
+  static constexpr uint32_t CODES = Q16 ? 256u * RING * GRP * 16 : 0;  // of the eight loader warps
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = OFF_Q + NTQ * TILE;
   static constexpr uint32_t OFF_V = OFF_K + KS * TILE;
@@ -95,7 +103,7 @@ struct Cfg {
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag, scan sums
   static constexpr uint32_t OFF_INFO = OFF_MISC + 128;                        // [kInfo] K's scale, [kInfo] oref
   static constexpr uint32_t OFF_ROWS = OFF_INFO + kInfo * 8;                  // [2][NTQ * 128] row scales of Q
-  static constexpr uint32_t OFF_RED = OFF_ROWS + 2 * NTQ * 128 * 4;           // [4] loader maxima
+  static constexpr uint32_t OFF_RED = OFF_ROWS + 2 * NTQ * 128 * 4;           // [8] loader maxima
   static constexpr uint32_t OFF_UNIT = OFF_RED + 32;                          // [kLists][kBatch] {int4, int4}
   static constexpr uint32_t OFF_PRE = OFF_UNIT + kLists * kBatch * 32;        // [groups + 1] first unit
   static size_t smem(int groups) { return OFF_PRE + static_cast<size_t>(groups + 1) * 4 + 1024; }
@@ -320,15 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int x = 0; x < C::NBARS; ++x) {
-      // arrivals: 1 of a commit or the lookup warp, 2 of the K or the V loaders' warps, 4 of a softmax lane, 8 of both
+      // arrivals: 1 of a commit or the lookup warp, 4 of the K or the V loaders' warps or a softmax lane, 8 of both lanes
       uint32_t count = 1;
-      if (x < C::B_QE || (x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_UN) || x == C::B_LA || x == C::B_LB)
-        count = 4;
-      else if (x >= C::B_RS && x < C::B_LK)
+      if (x >= C::B_RS && x < C::B_LK)
         count = 8;
-      else if ((x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) || (x >= C::B_UG && x < C::B_RS) ||
-               x == C::B_LK || x == C::B_LV)
-        count = 2;
+      else if (x < C::B_QE || (x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) ||
+               (x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_UN) || (x >= C::B_UG && x < C::B_FIN))
+        count = 4;
       ptx::mbar_init(bar(x), count);
     }
     *abort_flag = 0;
@@ -559,27 +565,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ================================================================ loaders
     ptx::setmaxnreg_dec<kRegLoad>();
-    const int kv = (warp - 4) >> 1;       // 0: K, 1: V
-    const int lt = (tid - 128) & 63;      // thread of the pair of warps
+    const int kv = (warp - 4) >> 2;       // 0: K, 1: V
+    const int lt = (tid - 128) & 127;     // thread of the four warps
     const int lw = warp - 4;
     const int nu = x1 - x0;
     const uint8_t *codes = kv == 0 ? a.k_codes : a.v_codes, *scales = kv == 0 ? a.k_scales : a.v_scales;
-    uint32_t pair_phase = 0;
-    auto sync_pair = [&]() -> bool {  // the two warps; bounded, unlike a named barrier
+    uint32_t four_phase = 0;
+    auto sync_four = [&]() -> bool {  // the four warps; bounded, unlike a named barrier
       arrive_warp(C::B_LK + kv);
-      return wait_warp(C::B_LK + kv, pair_phase++ & 1);
+      return wait_warp(C::B_LK + kv, four_phase++ & 1);
     };
 
-    // ---- codes of a unit: thread (p, r0) of the pair takes piece p of the rows r0 + STEP * i, those of a
-    // chunk together, in groups of four pieces.  A thread reads back only what it has copied itself.
+    // ---- codes of a unit: thread (p, r0) of the four warps takes piece p of the rows r0 + STEP * i, those of a
+    // chunk together, in groups of two pieces.  A thread reads back only what it has copied itself.
     constexpr int NP = C::NP, STEP = Q16 ? 128 / NP : 1, GRP = C::GRP, NG = C::NG;
     // (the group scales sit in registers, which wants constant indices)
     constexpr int UNROLL = FMT == BSA_CACHE_E2M1 ? NG : 1;
     const int p = lt % C::PP, r0 = lt / C::PP;
-    const uint32_t ring = C::OFF_CODE + static_cast<uint32_t>(tid - 128) * 16;  // slots of 128 pieces
+    const uint32_t ring = C::OFF_CODE + static_cast<uint32_t>(tid - 128) * 16;  // slots of 256 pieces
     struct {             // the group to be copied next
       int unit, group;   // its unit and place there
       const uint8_t *code[2];  // the thread's first piece of both chunks of the unit
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int i = NG > 1 ? (next.group % (NG > 1 ? NG / 2 : 1)) * GRP + e : e % (GRP / 2);
               const uint8_t *from = (h == 0 ? next.code[0] : next.code[1]) + i * (STEP * C::RB);
               const int live = r0 + STEP * i < (h == 0 ? next.n[0] : next.n[1]) ? 16 : 0;
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + ring + (slot * GRP + e) * 2048u),
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + ring + (slot * GRP + e) * 4096u),
                            "l"(from), "r"(live)
                            : "memory");
             }
@@ -672,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t fs[GRP];
 #pragma unroll
           for (int e = 0; e < GRP; ++e) {
-            cw[e] = *reinterpret_cast<const uint4 *>(sb + ring + (slot * GRP + e) * 2048);
+            cw[e] = *reinterpret_cast<const uint4 *>(sb + ring + (slot * GRP + e) * 4096);
             const int from = ((r0 + STEP * (gr * GRP + e)) >> 2) & 31;
             const uint32_t fa = __shfl_sync(0xffffffffu, f01, from), fb = __shfl_sync(0xffffffffu, f23, from);
             fs[e] = __byte_perm(upper ? fb : fa, 0u, pick);
@@ -715,19 +721,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // bf16 rows by hand: `n` keys of chunk h, from `from` (row stride in elements); zeros past n
     auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f) {
-      constexpr int PR = D / 8, U = 8, TOTAL = kChunk * PR / 64;
+      constexpr int PR = D / 8, TOTAL = kChunk * PR / 128, U = TOTAL < 8 ? TOTAL : 8;
 #pragma unroll 1
       for (int b = 0; b < TOTAL; b += U) {
         uint4 v[U];
 #pragma unroll
         for (int e = 0; e < U; ++e) {
-          const int x = (b + e) * 64 + lt;
+          const int x = (b + e) * 128 + lt;
           v[e] = make_uint4(0u, 0u, 0u, 0u);
           if (x / PR < n) v[e] = __ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8));
         }
 #pragma unroll
         for (int e = 0; e < U; ++e) {
-          const int x = (b + e) * 64 + lt;
+          const int x = (b + e) * 128 + lt;
           if constexpr (Q16) {
             uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
@@ -744,14 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int PR = D / 8;
       float am = 0.f;
 #pragma unroll 8
-      for (int x = lt; x < n * PR; x += 64)
+      for (int x = lt; x < n * PR; x += 128)
         am = fmaxf(am, amax8(__ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8))));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
       if (lane == 0) red[lw] = am;
-      if (!(ok = sync_pair())) return 8;
-      am = fmaxf(red[2 * kv], red[2 * kv + 1]);
-      ok = sync_pair();
+      if (!(ok = sync_four())) return 8;
+      am = fmaxf(fmaxf(red[4 * kv], red[4 * kv + 1]), fmaxf(red[4 * kv + 2], red[4 * kv + 3]));
+      ok = sync_four();
       return max(8, (__float_as_int(am) >> 23) + C::SHV - 14);
     };
 
@@ -814,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!Q16) {
         if (!d0.z) by_tma = (n0 == kChunk ? 1u : 0u) | (n1 == kChunk ? 2u : 0u);
         if (a.c.page >= kUnit && by_tma != 3) by_tma = 0;
-        if ((lw & 1) == 0 && by_tma != 0) {
+        if ((lw & 3) == 0 && by_tma != 0) {
           // (announced without arriving: this warp may still have rows of the other chunk to write)
           if (lane == 0) mbar_expect_tx(bar(full), (by_tma == 3 ? 2u : 1u) * (C::TILE / 2));
           __syncwarp();
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       arrive_warp(full);
     }
     if (Q16) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (!Q16 && *abort_flag && (lw & 1) == 0 && lane == 0) {
+    if (!Q16 && *abort_flag && (lw & 3) == 0 && lane == 0) {
       // let copies in flight land before the CTA's shared memory is released
       const uint32_t last = static_cast<uint32_t>(stages);
       for (uint32_t n = copies > last ? copies - last : 0; n < copies; ++n)
@@ -862,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ================================================================ softmax lanes
     ptx::setmaxnreg_inc<kRegSoft>();
-    const int t = (warp - 8) >> 2;
+    const int t = (warp - 12) >> 2;
     const int sub = warp & 3;
     const int r = (sub << 5) + lane;  // query row = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(sub << 5) << 16;
@@ -967,22 +973,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = wait_warp(C::B_SF + t, mine & 1))) break;
         ptx::tc_fence_after();
-        uint32_t sr[128];
+        // the row's maximum first, keeping the first 64 logits only: what follows is a loop over halves, whose
+        // code the instruction cache holds
+        uint32_t sr[2][32];
         float pm[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32_max(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]), pm[c]);
-        ptx::tmem_wait_ld();
         if (partial) {
-#pragma unroll
+          pm[1] = pm[2] = pm[3] = -INFINITY;
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            pm[c] = -INFINITY;
+            ptx::tmem_ld32(tS + c * 32, sr[0]);
+            ptx::tmem_wait_ld();
+            const uint32_t seen = c < 2 ? (c == 0 ? vis[0] : vis[1]) : (c == 2 ? vis[2] : vis[3]);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!((vis[c] >> e) & 1u)) sr[c * 32 + e] = 0xFF800000u;
-              pm[c] = fmaxf(pm[c], __uint_as_float(sr[c * 32 + e]));
-            }
+            for (int e = 0; e < 32; ++e)
+              if ((seen >> e) & 1u) pm[1] = fmaxf(pm[1], __uint_as_float(sr[0][e]));
           }
+        } else {
+          ptx::tmem_ld32_max(tS + 64, sr[0], pm[2]);
+          ptx::tmem_ld32_max(tS + 96, sr[1], pm[3]);
+          ptx::tmem_wait_ld();
         }
+        float first[2];
+        ptx::tmem_ld32_max(tS, sr[0], first[0]);
+        ptx::tmem_ld32_max(tS + 32, sr[1], first[1]);
+        ptx::tmem_wait_ld();
+        pm[0] = partial ? pm[1] : first[0];
+        pm[1] = partial ? pm[1] : first[1];
         const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
         const float mt = mx == -INFINITY ? -INFINITY : mx * scl;
         // O moves to a new reference or a larger unit only when it has to
@@ -1003,34 +1019,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float bias = static_cast<float>(C::SHIFT) - mb;
         uint64_t acc[2] = {0ull, 0ull};
         const uint64_t scl2 = ptx::f32x2(scl, scl), bias2 = ptx::f32x2(bias, bias);
-#pragma unroll
-        for (int c = 0; c < C::NPC; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t y = ptx::fma_f32x2(
-                ptx::f32x2(__uint_as_float(sr[c * 32 + 2 * e]), __uint_as_float(sr[c * 32 + 2 * e + 1])), scl2, bias2);
-            float y0, y1;
-            ptx::f32x2_split(y, y0, y1);
-            const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
-            acc[e & 1] = ptx::add_f32x2(acc[e & 1], ptx::f32x2(p0, p1));
-            pk[e] = Q16 ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
-          }
-          ptx::tmem_st16(tS + c * 16, pk);
-          if (c == 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
-            for (int q = 0; q < D / 8; ++q) {
-              uint32_t ov[8];
-              ptx::tmem_ld8(tO + q * 8, ov);
-              ptx::tmem_wait_ld();
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) ptx::tmem_wait_ld();
+          if (partial) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * of);
-              ptx::tmem_st8(tO + q * 8, ov);
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t seen = half == 0 ? vis[c] : vis[2 + c];
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((seen >> e) & 1u)) sr[c][e] = 0xFF800000u;
             }
           }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          arrive_warp(C::B_PR + t * C::NPC + c);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t y = ptx::fma_f32x2(
+                  ptx::f32x2(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])), scl2, bias2);
+              float y0, y1;
+              ptx::f32x2_split(y, y0, y1);
+              const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
+              acc[e & 1] = ptx::add_f32x2(acc[e & 1], ptx::f32x2(p0, p1));
+              pk[e] = Q16 ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
+            }
+            ptx::tmem_st16(tS + half * 32 + c * 16, pk);  // over logits that have been read
+            if (c == 0 && half == 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+              for (int q = 0; q < D / 8; ++q) {
+                uint32_t ov[8];
+                ptx::tmem_ld8(tO + q * 8, ov);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * of);
+                ptx::tmem_st8(tO + q * 8, ov);
+              }
+            }
+            if (half == 0) ptx::tmem_ld32(tS + 64 + c * 32, sr[c]);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            arrive_warp(C::B_PR + t * C::NPC + half * 2 + c);
+          }
         }
         float s4[4];
         ptx::f32x2_split(acc[0], s4[0], s4[1]);
@@ -1283,10 +1313,10 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   TreeRun *runs = reinterpret_cast<TreeRun *>(base + ws.runs);
   auto kern = tree_mma_kernel<D, FMT, PAIR>;
   // setmaxnreg.inc waits until the registers it asks for are free: the split is only safe if the
-  // kernel really launches with 128 registers per thread
+  // kernel really launches with that many registers per thread
   cudaFuncAttributes fa{};
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSA_ERR_CUDA;
-  if (fa.numRegs != 128) return BSA_ERR_UNSUPPORTED;
+  if (fa.numRegs != kLaunchRegs) return BSA_ERR_UNSUPPORTED;
   const size_t smem = C::smem(a.batch * a.c.hkv);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return BSA_ERR_CUDA;
