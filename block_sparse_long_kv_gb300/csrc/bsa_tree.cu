@@ -756,7 +756,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 #pragma unroll
       for (int w = 0; w < C::NNT / 2; ++w) {
         const int dim = gq * (D / 8) + 2 * w;
-        const uint32_t v0 = word(vr[0], dim), v1 = word(vr[1], dim), v2 = word(vr[2], dim), v3 = word(vr[3], dim);
+        const uint32_t v0 = finite_bf16x2(word(vr[0], dim)), v1 = finite_bf16x2(word(vr[1], dim)),
+                       v2 = finite_bf16x2(word(vr[2], dim)), v3 = finite_bf16x2(word(vr[3], dim));
         mma<true>(o[2 * w], pa, __byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410));
         mma<true>(o[2 * w + 1], pa, __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x7632));
       }

@@ -71,4 +71,12 @@ __device__ __forceinline__ int shared_tile(const TreeRun *runs, int ctas, int x,
   return found_at;
 }
 
+// Infinities and NaN of two bf16 values become 0.  A drafted row that holds some is hidden from the rows of other
+// branches by p = 0 alone, and 0 times it would not be 0.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+  return w;
+}
+
 }  // namespace bsa

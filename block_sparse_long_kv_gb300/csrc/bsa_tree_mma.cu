@@ -145,6 +145,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint4 finite_bf16x8(const uint4 &v) {
+  return make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+}
 __device__ __forceinline__ float amax8(const uint4 &v) {  // of eight bf16
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float am = 0.f;
@@ -720,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // bf16 rows by hand: `n` keys of chunk h, from `from` (row stride in elements); zeros past n
-    auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f) {
+    auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f, bool drafted) {
       constexpr int PR = D / 8, TOTAL = kChunk * PR / 128, U = TOTAL < 8 ? TOTAL : 8;
 #pragma unroll 1
       for (int b = 0; b < TOTAL; b += U) {
@@ -734,6 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < U; ++e) {
           const int x = (b + e) * 128 + lt;
+          if (drafted) v[e] = finite_bf16x8(v[e]);
           if constexpr (Q16) {
             uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float am = 0.f;
 #pragma unroll 8
       for (int x = lt; x < n * PR; x += 128)
-        am = fmaxf(am, amax8(__ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8))));
+        am = fmaxf(am, amax8(finite_bf16x8(__ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8)))));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
       if (lane == 0) red[lw] = am;
@@ -835,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (d0.z) {
         const float f = Q16 ? pow2_biased(254 + C::SHV - ref) : 1.f;
-        store_rows(tile, 0, drafted, dstride, n0, f);
-        store_rows(tile, 1, drafted + kChunk * dstride, dstride, n1, f);
+        store_rows(tile, 0, drafted, dstride, n0, f, true);
+        store_rows(tile, 1, drafted + kChunk * dstride, dstride, n1, f, true);
         for (int gr = 0; Q16 && gr < NG; ++gr) {  // the unit's empty groups
           copy_group(slot);
           slot = slot == C::RING - 1 ? 0 : slot + 1;
@@ -850,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (by_tma >> h & 1) continue;
             const int nh = h == 0 ? n0 : n1, pg = h == 0 ? d1.x : d1.z, sub = (h == 0 ? d1.y : d1.w) >> 16;
             const size_t row = (static_cast<size_t>(pg) * a.c.hkv + g) * a.c.page + sub * kChunk;
-            store_rows(tile, h, reinterpret_cast<const uint16_t *>(codes) + row * D, D, nh, 1.f);
+            store_rows(tile, h, reinterpret_cast<const uint16_t *>(codes) + row * D, D, nh, 1.f, false);
           }
         }
       }

@@ -550,7 +550,11 @@ bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t t
  *   [total_draft, hq], nullable) the natural log of the normaliser.
  * The dot products use the held values exactly; softmax statistics and sums
  * are fp32.  One drafted token is a decode step.  Rows past cu_draft[batch] are
- * left as they were.
+ * left as they were.  A drafted token whose k_new or v_new holds Inf or NaN
+ * harms the tokens that attend to it alone.  With an 8- or 4-bit cache and more
+ * than 16 rows (drafted tokens x G) a sequence, the drafted keys (values) of one
+ * KV head are held in f16 under one power of two per 128 drafted tokens: elements
+ * 2^28 below the largest of them lose bits.
  *
  * Limits: hq % hkv == 0 with G in {1, 2, 4, 8, 16}; max_draft <= 256 drafted
  * tokens a sequence; max_cached tokens <= 4096 pages and <= table_stride pages;

@@ -432,3 +432,196 @@ def test_python_refusals():
         with pytest.raises(err):
             call(**kw)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- many query rows (drafted tokens x heads > 16)
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page", [64, 128, 256])
+def test_kept_pages_with_many_rows(fmt, page):
+    c = Case(fmt, [3000, 77, 0, 1025], [40, 33, 18, 64], 8, 2, 128, page, keep=0.4, seed=page)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("drafts", [20, 40])
+def test_bad_device_arguments_with_many_rows(drafts):
+    c = Case(C.E4M3, [300], [drafts], 8, 2, 128, 128)
+    bsa = c.bsa
+    ts = bsa.make_tree_shape(1, drafts, drafts, 300, 8, c.stride)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def run(cu=(0, drafts), cached=(300,), table=None, parents=None):
+        o = torch.full((drafts, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((drafts, 8), 5.0, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        bsa.tree_fwd(ts, c.cs, dev(cu), dev(cached), c.table.cuda() if table is None else table.cuda(),
+                     dev(c.parents[0] if parents is None else parents), c.q.cuda(), c.k_new.cuda(), c.v_new.cuda(), c.cache,
+                     None, None, 1 / math.sqrt(128), o, lse, dev_status=st)
+        torch.cuda.synchronize()
+        return o, lse, int(st.item())
+
+    o, lse, code = run()
+    assert code == 0
+    c.check(o, lse)
+    for cu in ((0, drafts + 1), (-1, drafts), (3, 1)):
+        o, lse, code = run(cu=cu)
+        assert code == 1 and (o == 5).all() and (lse == 5).all()
+    for n in (-1, 301):                                         # reads as an empty cache
+        o, lse, code = run(cached=(n,))
+        assert code == 1
+        keep, c.lists = c.lists, [[[], []]]
+        c.check(o, lse)
+        c.lists = keep
+    for bad in (-1, c.cs.pages, 1 << 30):                       # a page that is left out
+        t = c.table.clone()
+        t[0, 1] = bad
+        o, lse, code = run(table=t)
+        assert code == 1
+        c.lists = [[[0, 2], [0, 2]]]
+        c.check(o, lse)
+        c.lists = None
+    for bad in (2, 3, 1 << 30, -2):                             # a parent that reads as a root
+        par = list(c.parents[0])
+        par[2] = bad
+        o, lse, code = run(parents=par)
+        assert code == 1
+        par[2] = -1
+        c.check(o, lse, [par])
+
+
+@pytest.mark.parametrize("first", [19, 50])
+def test_rows_behind_the_last_sequence_stay_with_many_rows(first):
+    c = Case(C.E2M1, [300, 10], [first, 18], 8, 2, 128, 128)
+    bsa, t = c.bsa, first + 18
+    o = torch.full((t + 4, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((t + 4, 8), 5.0, device="cuda")
+    pad = lambda x: torch.cat([x, torch.full((4, *x.shape[1:]), float("nan"), dtype=x.dtype)]).cuda()
+    ts = bsa.make_tree_shape(2, t + 4, first, 300, 8, c.stride)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.tree_fwd(ts, c.cs, torch.tensor([0, first, t], dtype=torch.int32, device="cuda"),
+                 torch.tensor(c.lengths, dtype=torch.int32, device="cuda"), c.table.cuda(),
+                 torch.tensor(sum(c.parents, []) + [99] * 4, dtype=torch.int32, device="cuda"), pad(c.q), pad(c.k_new),
+                 pad(c.v_new), c.cache, None, None, 1 / math.sqrt(128), o, lse, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert (o[t:] == 5).all() and (lse[t:] == 5).all()
+    c.check(o[:t], lse[:t])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("drafts", [4, 20, 70])
+def test_a_branch_with_nan_and_inf_does_not_reach_the_others(fmt, drafts):
+    """Drafted tokens that nobody descends from hold infinities and NaN; every other token's result is that with
+    zeros in their place, bit for bit."""
+    c = Case(fmt, [200], [drafts], 8, 2, 128, 64)
+    leaves = [i for i in range(drafts) if i not in c.parents[0]][:3] if drafts > 4 else [3]
+    if drafts == 4:
+        c.parents[0] = [-1, 0, 1, 0]
+    bad = [float("nan"), float("inf"), -float("inf")]
+    clean = []
+    for x, poison in ((c.k_new, bad), (c.v_new, bad[::-1])):
+        for i, leaf in enumerate(leaves):
+            x[leaf] = 0
+            clean.append((x, leaf, poison[i]))
+    want, wl = c.run()
+    for x, leaf, value in clean:
+        x[leaf, :, ::3] = value
+    got, gl = c.run()
+    keep = [i for i in range(drafts) if i not in leaves]
+    assert torch.equal(got[keep], want[keep]) and torch.equal(gl[keep], wl[keep])
+    assert torch.isfinite(got[keep].float()).all() and torch.isfinite(gl[keep]).all()
+
+
+@pytest.mark.parametrize("fmt, batch, hkv, drafts", [(C.E4M3, 300, 4, 17), (C.BF16, 300, 4, 17), (C.E2M1, 1024, 4, 3),
+                                                     (C.E4M3, 1024, 4, 1)])
+def test_very_many_short_sequences(fmt, batch, hkv, drafts):
+    """Runs of a CTA that cross many row tiles, some of one unit only, up to the largest number of groups."""
+    lengths = [(7 * b) % 70 if b % 11 else 0 for b in range(batch)]
+    c = Case(fmt, lengths, [max(0, drafts - b % 3) for b in range(batch)], 8 * hkv, hkv, 64, 64, seed=batch)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("batch, drafts", [(38, 8), (3, 256)])
+def test_runs_of_many_units(fmt, batch, drafts):
+    """Every CTA walks more than 128 units: one row tile of 128 rows each, and sixteen tiles of 256."""
+    import block_sparse_long_kv_gb300 as bsa
+    hkv, group, d, page, pages, n = 2, 16, 64, 256, 40, 33000
+    hq, scale = hkv * group, 0.125
+    g = torch.Generator().manual_seed(drafts)
+    cs = bsa.make_cache_shape(pages, page, hkv, d, fmt)
+    cache = bsa.alloc_cache(cs)
+    k, v = bf(g, pages * page, hkv, d), bf(g, pages * page, hkv, d)
+    bsa.cache_write(cs, k.cuda(), v.cuda(), torch.arange(pages * page, dtype=torch.int32, device="cuda"), cache)
+    hk, hv = (torch.from_numpy(C.held(x.double().numpy(), fmt)).cuda() for x in (k, v))
+    stride = -(-n // page)
+    table = torch.randint(0, pages, (batch, stride), generator=g, dtype=torch.int32)
+    lengths = [n - 77 * b for b in range(batch)]
+    t = batch * drafts
+    q, kn, vn = bf(g, t, hq, d), bf(g, t, hkv, d), bf(g, t, hkv, d)
+    par = torch.tensor([max(-1, i - 1 - i % 3) for i in range(drafts)], dtype=torch.int32)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ts = bsa.make_tree_shape(batch, t, drafts, n, hq, stride)
+    o, lse = torch.empty(t, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(t, hq, device="cuda")
+    st = dev([0])
+    bsa.tree_fwd(ts, cs, dev([drafts * b for b in range(batch + 1)]), dev(lengths), table.cuda(), par.repeat(batch).cuda(),
+                 q.cuda(), kn.cuda(), vn.cuda(), cache, None, None, scale, o, lse, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    sees = torch.zeros(drafts, drafts, dtype=torch.bool)
+    for i in range(drafts):
+        p = i
+        while p >= 0:
+            sees[i, p] = True
+            p = int(par[p])
+    hidden = ~sees.cuda().repeat_interleave(group, 0)
+    for b in range(batch):
+        i = torch.arange(lengths[b])
+        at = (table[b].long()[i // page] * page + i % page).cuda()
+        rows = slice(b * drafts, (b + 1) * drafts)
+        for x in range(hkv):
+            qq = q[rows, x * group:(x + 1) * group].double().cuda().reshape(-1, d)
+            kk = torch.cat([hk[at, x], kn[rows, x].double().cuda()])
+            vv = torch.cat([hv[at, x], vn[rows, x].double().cuda()])
+            s = scale * qq @ kk.T
+            s[:, lengths[b]:].masked_fill_(hidden, -math.inf)
+            reach = (scale * qq.abs() @ kk.abs().T).amax(-1)
+            wl = torch.logsumexp(s, -1)
+            p = torch.exp(s - wl[:, None])
+            want, a = p @ vv, p @ vv.abs()
+            delta = 2 * (d + 8) * 2.0 ** -24 * reach + 2.0 ** -20
+            tol = (2.0 ** -8 + 4 * delta[:, None] + 2.0 ** -18) * a + 2.0 ** -8 * want.abs()
+            if fmt != C.BF16:
+                tol = tol + len(kk) * 2.0 ** -35 * vv.abs().max()
+            got = o[rows, x * group:(x + 1) * group].double().reshape(-1, d)
+            assert ((got - want).abs() <= tol).all(), (b, x)
+            gl = lse[rows, x * group:(x + 1) * group].double().reshape(-1)
+            assert ((gl - wl).abs() <= 2 * delta + 2.0 ** -20 * (1 + wl.abs())).all(), (b, x)
+
+
+@pytest.mark.parametrize("drafts", [[20, 18], [40, 33]])
+def test_two_captured_graphs_share_a_workspace(drafts):
+    """Replayed one after the other on one stream, each gives its eager call's bits."""
+    cases = [Case(f, [900, 300], drafts, 8, 2, 128, 64, seed=s) for f, s in ((C.E2M1, 1), (C.BF16, 2))]
+    bsa = cases[0].bsa
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ts = bsa.make_tree_shape(2, sum(drafts), max(drafts), 900, 8, cases[0].stride)
+    ws = torch.empty(max(bsa.tree_workspace_bytes(ts, c.cs) for c in cases), dtype=torch.uint8, device="cuda")
+    graphs, outs, held, want = [], [], [], [c.run() for c in cases]
+    for c in cases:
+        o, lse, st = torch.zeros(sum(drafts), 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(sum(drafts), 8, device="cuda"), dev([0])
+        args = (ts, c.cs, dev([0, drafts[0], sum(drafts)]), dev([900, 300]), c.table.cuda(), dev(sum(c.parents, [])), c.q.cuda(),
+                c.k_new.cuda(), c.v_new.cuda(), c.cache, None, None, 1 / math.sqrt(128), o, lse, ws, st)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            bsa.tree_fwd(*args)
+        graphs.append(graph)
+        outs.append((o, lse, st))
+        held.append(args)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (o, lse, st), (wo, wl) in zip(outs, want):
+        assert int(st.item()) == 0 and torch.equal(o, wo) and torch.equal(lse, wl)
