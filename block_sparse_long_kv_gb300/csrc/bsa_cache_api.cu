@@ -16,7 +16,7 @@ bool good4(const void *p) { return p != nullptr && aligned(p, 4); }
 bool status_ok(const int32_t *p) { return aligned(p, 4); }
 
 // Rows of `width` bf16 values at `stride` elements: a stride the 16-byte accesses can take.
-bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride <= (1ll << 40); }
+bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride <= (1ll << 30); }
 
 // Whether `tokens` rows of one array share a byte with rows of another.  Rows of one buffer at one
 // stride are compared by their columns; of other overlapping buffers nothing is known.

@@ -153,3 +153,10 @@ def test_tree_refusals(lib):
     assert tree(lib, ws=None) == WORKSPACE and tree(lib, ws=m) == WORKSPACE and tree(lib, nbytes=need - 1) == WORKSPACE
     bad = _lib.TreeShape(0, 9, 5, 1000, 16, 8)
     assert lib.bsa_tree_workspace_bytes(ctypes.byref(bad), ctypes.byref(c)) == 0
+
+
+def test_strides_past_the_limit(lib):
+    """Strides whose spans would not fit 64 bits for the largest token counts are refused."""
+    for big in ((1 << 30) + 8, 1 << 40, (1 << 62)):
+        assert rope(lib, stride_q=big) == INVALID and rope(lib, sko=big) == INVALID
+        assert write(lib, cshape(), ks=big) == INVALID and write(lib, cshape(), vs=big) == INVALID
