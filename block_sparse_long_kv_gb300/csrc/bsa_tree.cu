@@ -906,7 +906,8 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   TreeRun *runs = reinterpret_cast<TreeRun *>(base + ws.runs);
   auto kern = tree_attn_kernel<D, FMT>;
   const size_t smem = C::smem(a.batch * a.c.hkv);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_up(kern, C::smem(kMaxDecodeRows), 0, done);
   if (e != cudaSuccess) return e;
   kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, runs);
   e = cudaGetLastError();

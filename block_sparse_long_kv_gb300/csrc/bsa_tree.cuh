@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace bsa {
 
 // A kernel launched by launch_after may start before the one ahead of it in the stream has ended; it waits
@@ -23,6 +25,26 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cuda
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// Sets a kernel up once per device: its shared-memory limit, to the most that any call asks for (the limit belongs
+// to the process: one that followed each call's size could be lowered under another thread's launch), and a check
+// of its registers per thread (0: none).  `done` is the kernel's own, a bit per device.
+template <typename Kernel>
+cudaError_t set_up(Kernel kern, size_t most_smem, int registers, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if ((done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  if (registers != 0) {
+    cudaFuncAttributes fa{};
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs != registers) return cudaErrorNotSupported;
+  }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most_smem));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // What CTA c of an attention launch records of its run of units: the group (sequence * hkv + KV head) of its

@@ -60,6 +60,7 @@ using wait::Ctl;
 using wait::drain_bar;
 
 constexpr int kSms = 152;
+constexpr size_t kMaxSmem = 227 * 1024;  // a CTA may have
 constexpr int kThreads = 640;
 constexpr int kLaunchRegs = 96;  // per thread
 constexpr int kRows = 128;     // rows of a tile
@@ -1318,12 +1319,10 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   auto kern = tree_mma_kernel<D, FMT, PAIR>;
   // setmaxnreg.inc waits until the registers it asks for are free: the split is only safe if the
   // kernel really launches with that many registers per thread
-  cudaFuncAttributes fa{};
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSA_ERR_CUDA;
-  if (fa.numRegs != kLaunchRegs) return BSA_ERR_UNSUPPORTED;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t ready = set_up(kern, kMaxSmem, kLaunchRegs, done);
+  if (ready != cudaSuccess) return ready == cudaErrorNotSupported ? BSA_ERR_UNSUPPORTED : BSA_ERR_CUDA;
   const size_t smem = C::smem(a.batch * a.c.hkv);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return BSA_ERR_CUDA;
   kern<<<kSms, kThreads, smem, stream>>>(mk, mv, a, part_o, part_ml, lane_o, runs);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   const int rows = a.max_draft * a.group;
@@ -1341,7 +1340,7 @@ template <int D, int FMT>
 bsa_status launch_fmt(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   // two row tiles per unit halve the reads and conversions of the cache; the plan of very large batches
   // does not fit beside them in shared memory
-  const bool pair = a.max_draft * a.group > kRows && Cfg<D, FMT, true>::smem(a.batch * a.c.hkv) <= 227 * 1024;
+  const bool pair = a.max_draft * a.group > kRows && Cfg<D, FMT, true>::smem(a.batch * a.c.hkv) <= kMaxSmem;
   return pair ? launch_t<D, FMT, true>(a, workspace, stream) : launch_t<D, FMT, false>(a, workspace, stream);
 }
 

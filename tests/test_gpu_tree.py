@@ -625,3 +625,30 @@ def test_two_captured_graphs_share_a_workspace(drafts):
     torch.cuda.synchronize()
     for (o, lse, st), (wo, wl) in zip(outs, want):
         assert int(st.item()) == 0 and torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+def test_calls_from_two_threads_with_different_batches():
+    """The library is called without Python's lock: a small batch and one whose plan takes more shared memory."""
+    import threading
+    cases = [Case(C.E4M3, [300], [20], 8, 2, 128, 64, seed=1),
+             Case(C.E4M3, [10] * 400, [5] * 400, 8, 2, 128, 64, seed=2),
+             Case(C.E4M3, [300], [2], 8, 2, 128, 64, seed=3),
+             Case(C.E4M3, [10] * 400, [1] * 400, 8, 2, 128, 64, seed=4)]
+    want, got, failed = [c.run() for c in cases], [None] * 4, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got[i] = cases[i].run(stream=torch.cuda.current_stream())
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for (o, lse), (wo, wl) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
