@@ -445,8 +445,8 @@ bsa_status bsa_decode_step(const bsa_varlen_shape *shape, const bsa_select_param
  * in fp32, one rounding to bf16.  A token whose position is negative is left
  * out: its rows of q_out and k_out stay as they were.
  *
- * Strides are elements between tokens (multiples of 8, at least heads * d; the
- * heads of a token are contiguous), so q and k may be columns of a fused
+ * Strides are elements between tokens (multiples of 8, at least heads * d and at
+ * most 2^30; the heads of a token are contiguous), so q and k may be columns of a fused
  * projection's rows.  q_out may be q with the same stride, and k_out k; other
  * overlaps of an output with an input or the other output are refused
  * (BSA_ERR_INVALID_ARG).  Supported: head_dim in {64, 128}; rotary_dim a

@@ -652,3 +652,19 @@ def test_calls_from_two_threads_with_different_batches():
     assert not failed, failed
     for (o, lse), (wo, wl) in zip(got, want):
         assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("fmt, pages", [(C.BF16, 150000), (C.E4M3, 300000), (C.E2M1, 600000)])
+@pytest.mark.parametrize("drafts", [2, 20, 40])
+def test_pages_past_32_bit_offsets(fmt, pages, drafts):
+    c = Case(fmt, [500, 70], [drafts, 1], 8, 2, 128, 64, seed=drafts)
+    few = c.cs.pages
+    cs = c.bsa.make_cache_shape(pages, 64, 2, 128, fmt)
+    assert c.bsa.cache_code_bytes(cs) > 1 << 32
+    big = c.bsa.alloc_cache(cs)
+    for name, x in c.cache.items():
+        if x is not None:
+            big[name][pages - few:] = x
+    c.cs, c.cache = cs, big
+    c.table = torch.where(c.table >= 0, c.table + (pages - few), c.table)
+    c.check(*c.run())
