@@ -96,7 +96,7 @@ struct Cfg {
   static constexpr uint32_t OFF_V = OFF_K + KS * TILE;
   static constexpr uint32_t OFF_CODE = OFF_V + VS * TILE;
   static constexpr uint32_t OFF_BAR = OFF_CODE + CODES;
-  static constexpr int NPC = 4;                    // P released in chunks of 32 keys
+  static constexpr int NPC = 2;                    // P released in halves of 64 keys
   static constexpr int B_QF = 0, B_QE = 2, B_KF = 3, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS,
                        B_SF = B_VE + VS, B_PR = B_SF + 2, B_OD = B_PR + 2 * NPC, B_OE = B_OD + 2, B_UN = B_OE + 2,
                        B_UG = B_UN + kLists, B_IK = B_UG + 1, B_IV = B_IK + kInfo, B_RS = B_IV + kInfo, B_LK = B_RS + 2,
@@ -211,6 +211,17 @@ __device__ __forceinline__ bool try_wait_parked(uint32_t bar, uint32_t parity) {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool is_complete(uint32_t bar, uint32_t parity) {  // a look, without waiting
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -426,16 +437,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dv = dv0 + static_cast<uint64_t>(vs) * (C::TILE >> 4);
         const uint32_t dst = tmem + C::TM_O + t * 128, src = tmem + t * 128;
         const uint32_t parity = pv_count[t] & 1;
-        auto chunk = [&](auto at, uint32_t acc) -> bool {  // 32 keys: two MMAs of 16
+        auto chunk = [&](auto at, uint32_t acc) {  // 32 keys: two MMAs of 16
           constexpr int c = decltype(at)::value;
-          if (!wait_parked(bar(C::B_PR + t * C::NPC + c), parity, ctl)) return false;
-          ptx::tc_fence_after();
           mma_ts_at<16 * c, 256 * c>(dst, src, dv, C::IDESC_O, acc);
           mma_ts_at<16 * c + 8, 256 * c + 128>(dst, src, dv, C::IDESC_O, 1u);
-          return true;
         };
-        if (!chunk(Int<0>{}, accumulate ? 1u : 0u) || !chunk(Int<1>{}, 1u) || !chunk(Int<2>{}, 1u) || !chunk(Int<3>{}, 1u))
-          return false;
+        // both halves are looked at before the first product: mostly both are there, and a look between the
+        // products would leave the tensor core idle
+        const uint32_t p0 = bar(C::B_PR + t * C::NPC), p1 = p0 + 8;
+        const bool first = is_complete(p0, parity), second = is_complete(p1, parity);
+        if (!first && !wait_parked(p0, parity, ctl)) return false;
+        ptx::tc_fence_after();
+        chunk(Int<0>{}, accumulate ? 1u : 0u);
+        chunk(Int<1>{}, 1u);
+        if (!second) {
+          if (!wait_parked(p1, parity, ctl)) return false;
+          ptx::tc_fence_after();
+        }
+        chunk(Int<2>{}, 1u);
+        chunk(Int<3>{}, 1u);
         ++pv_count[t];
         return true;
       };
@@ -1062,10 +1082,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (half == 0) ptx::tmem_ld32(tS + 64 + c * 32, sr[c]);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            arrive_warp(C::B_PR + t * C::NPC + half * 2 + c);
           }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          arrive_warp(C::B_PR + t * C::NPC + half);
         }
         float s4[4];
         ptx::f32x2_split(acc[0], s4[0], s4[1]);
