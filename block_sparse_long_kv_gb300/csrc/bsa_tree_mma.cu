@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mma_commit(bar(C::B_SF + t));
       };
       uint32_t pv_count[2] = {0, 0};  // P V products issued for each lane
-      auto issue_pv = [&](int t, int vs, bool accumulate) -> bool {
+      // (nv: the unit whose V is waited for first, or -1)
+      auto issue_pv = [&](int t, int vs, bool accumulate, int nv) -> bool {
         const uint64_t dv = dv0 + static_cast<uint64_t>(vs) * (C::TILE >> 4);
         const uint32_t dst = tmem + C::TM_O + t * 128, src = tmem + t * 128;
         const uint32_t parity = pv_count[t] & 1;
@@ -445,7 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // both halves are looked at before the first product: mostly both are there, and a look between the
         // products would leave the tensor core idle
         const uint32_t p0 = bar(C::B_PR + t * C::NPC), p1 = p0 + 8;
+        const uint32_t vf = bar(C::B_VF + vs), v_parity = (static_cast<uint32_t>(nv) / C::VS) & 1;
+        const bool there = nv < 0 || is_complete(vf, v_parity);
         const bool first = is_complete(p0, parity), second = is_complete(p1, parity);
+        if (!there && !wait_parked(vf, v_parity, ctl)) return false;
         if (!first && !wait_parked(p0, parity, ctl)) return false;
         ptx::tc_fence_after();
         chunk(Int<0>{}, accumulate ? 1u : 0u);
@@ -460,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
+      bool k_there = false;  // K of the next unit was seen to be there
       uint32_t n = 0, n_seg = 0;
       uint32_t lane_segs[2] = {0, 0};  // segments in which the lane had a unit
       // the lane's first P V of a segment overwrites O: the last segment's must have been read
@@ -475,14 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < s.units; ++i, ++n) {
           const uint32_t ks = n % C::KS, vs = n % C::VS;
           const bool last = i == s.units - 1;
-          if (!(ok = wait_parked(bar(C::B_KF + ks), (n / C::KS) & 1, ctl))) break;
+          if (!k_there && !(ok = wait_parked(bar(C::B_KF + ks), (n / C::KS) & 1, ctl))) break;
+          k_there = false;
           ptx::tc_fence_after();
           if constexpr (PAIR) {
             issue_s(0, ks);
             if (i > 0) {
               const uint32_t pvs = (n - 1) % C::VS;
               if (i == 1 && !(ok = o_free(1))) break;
-              if (!(ok = issue_pv(1, pvs, i > 1))) break;
+              if (!(ok = issue_pv(1, pvs, i > 1, -1))) break;
               ptx::mma_commit(bar(C::B_VE + pvs));
             }
             if (i == 0) {
@@ -491,14 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             issue_s(1, ks);
             ptx::mma_commit(bar(C::B_KE + ks));
+            if (!last) k_there = is_complete(bar(C::B_KF + (n + 1) % C::KS), ((n + 1) / C::KS) & 1);
             // V(n) has two stages only and is refilled late: it is waited for as late as possible
-            if (!(ok = wait_parked(bar(C::B_VF + vs), (n / C::VS) & 1, ctl))) break;
             if (i == 0 && !(ok = o_free(0))) break;
-            if (!(ok = issue_pv(0, vs, i > 0))) break;
+            if (!(ok = issue_pv(0, vs, i > 0, static_cast<int>(n)))) break;
             if (last) {
               ptx::mma_commit(bar(C::B_OD));
               if (i == 0 && !(ok = o_free(1))) break;
-              if (!(ok = issue_pv(1, vs, i > 0))) break;
+              if (!(ok = issue_pv(1, vs, i > 0, -1))) break;
               ptx::mma_commit(bar(C::B_VE + vs));
               ptx::mma_commit(bar(C::B_OD + 1));
             }
@@ -510,10 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j == i && !last) break;
               const uint32_t nj = n - static_cast<uint32_t>(i - j), pvs = nj % C::VS;
               const int t = j & 1;
-              if (!(ok = wait_parked(bar(C::B_VF + pvs), (nj / C::VS) & 1, ctl))) break;
-              ptx::tc_fence_after();
               if (j == t && !(ok = o_free(t))) break;
-              if (!(ok = issue_pv(t, pvs, j >= 2))) break;
+              if (!(ok = issue_pv(t, pvs, j >= 2, static_cast<int>(nj)))) break;
               ptx::mma_commit(bar(C::B_VE + pvs));
               if (j + 2 >= s.units) ptx::mma_commit(bar(C::B_OD + t));
             }
