@@ -32,14 +32,17 @@
 // maximum, so P' <= 2^15.  Row sums are fp32 from unrounded values.
 //
 // What bounds it: with two row tiles a unit is 32 MMAs of 64 cycles, 2048 cycles.  8 sequences of up to
-// 32768 cached tokens, 64 drafted tokens, 32 / 4 heads of 128 (84 units a CTA): bf16 206 us, e4m3 and e2m1
-// 268 (0.91 and 0.72 PFLOP/s; the MMAs alone 109), so 4600 to 6000 cycles a unit.  Half of them the issuing
-// thread waits for a softmax lane; it hardly ever waits for keys.  The lanes have a thousand instructions a
-// unit and share the schedulers with the conversion, and the instruction cache shows: a ready warp waits
-// for its code more often than for a pipe.  So code is kept short: logits are taken in two halves (the second
-// is read from TMEM again), which also frees the registers for eight loader warps instead of four
-// (e2m1 327 -> 268).  Measured and not kept: two threads a row (297), the conversion unrolled (355), deeper
-// rings (no change), waits that poll instead of parking (+4 %).
+// 32768 cached tokens, 64 drafted tokens, 32 / 4 heads of 128 (84 units a CTA): bf16 205 us, e4m3 249, e2m1
+// 270 (0.94, 0.78 and 0.72 PFLOP/s; the MMAs alone 109).  From its logits to the last of P a lane takes 2400
+// cycles, of which the other lane's products cover two thirds; keys are hardly ever waited for.  The lanes have a
+// thousand instructions a unit and share the schedulers with the conversion, and the instruction cache shows: a
+// warp waits for its code as long as it issues.  So code is kept short: logits are taken in two halves (the
+// second is read from TMEM again), which also frees the registers for eight loader warps instead of four (e2m1
+// 327 -> 268).  The issuing thread looks at both halves of P, V and the next K before its products: a look between
+// them left the tensor core idle (e4m3 with P in quarters 256).
+// Measured and not kept: two threads a row (297), the conversion or the halves unrolled (355, 260), all 128 logits
+// in registers with four loader warps (bf16 190, e4m3 250, e2m1 293), running pointers in the loaders (257),
+// deeper rings (no change), waits that poll instead of parking (+4 %).
 // Every mbarrier wait is bounded, as in the prefill kernel.
 
 #include <cuda.h>

@@ -565,7 +565,7 @@ bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t t
  * smaller than its token sets it and reads as -1; list entries that name no
  * page of the sequence are left out.  workspace: bsa_tree_workspace_bytes bytes, 16-byte
  * aligned, the caller's alone while the call runs; its contents need no
- * initialisation and are dead afterwards.  cu_draft, cached, block_table and
+ * initialisation and are dead afterwards.  o and lse overlap no input.  cu_draft, cached, block_table and
  * parents 4-byte aligned, the rest 16-byte.
  * ------------------------------------------------------------------------ */
 typedef struct {
