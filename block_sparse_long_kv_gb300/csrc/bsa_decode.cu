@@ -690,6 +690,8 @@ __device__ __forceinline__ void decode_attn_run(
     l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
     l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
     l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
+    m_lo = ptx::part_max(m_lo, l_lo);
+    m_hi = ptx::part_max(m_hi, l_hi);
     if (tq == 0) {
       wm[warp][gq] = m_lo;
       wm[warp][gq + 8] = m_hi;
@@ -700,8 +702,8 @@ __device__ __forceinline__ void decode_attn_run(
     float mlo = -INFINITY, mhi = -INFINITY;
 #pragma unroll
     for (int x = 0; x < NW; ++x) {
-      mlo = fmaxf(mlo, wm[x][gq]);
-      mhi = fmaxf(mhi, wm[x][gq + 8]);
+      mlo = ptx::max_nan(mlo, wm[x][gq]);
+      mhi = ptx::max_nan(mhi, wm[x][gq + 8]);
     }
     const float slo = m_lo == -INFINITY ? 0.f : exp2f(m_lo - mlo);
     const float shi = m_hi == -INFINITY ? 0.f : exp2f(m_hi - mhi);
@@ -728,7 +730,7 @@ __device__ __forceinline__ void decode_attn_run(
     if (tid < G) {
       float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int x = 0; x < NW; ++x) m = fmaxf(m, wm[x][tid]);
+      for (int x = 0; x < NW; ++x) m = ptx::max_nan(m, wm[x][tid]);
 #pragma unroll
       for (int x = 0; x < NW; ++x)
         if (wm[x][tid] != -INFINITY) l = fmaf(exp2f(wm[x][tid] - m), wl[x][tid], l);
@@ -875,9 +877,9 @@ __device__ __forceinline__ void combine_head(int b, int h, const float *__restri
   const int r = b * hkv + h / grp, hl = h % grp;
   const int s0 = plan[1 + r], ns = plan[2 + r] - s0;
   float m = -INFINITY;
-  for (int s = lane; s < ns; s += 32) m = fmaxf(m, part_ml[(static_cast<size_t>(s0 + s) * grp + hl) * 2]);
+  for (int s = lane; s < ns; s += 32) m = ptx::max_nan(m, part_ml[(static_cast<size_t>(s0 + s) * grp + hl) * 2]);
 #pragma unroll
-  for (int offs = 16; offs > 0; offs >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, offs));
+  for (int offs = 16; offs > 0; offs >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, offs));
   for (int vw = warp; vw < kCombineWarps; vw += NWR) {
     float acc[VL];
 #pragma unroll
@@ -926,11 +928,11 @@ __device__ __forceinline__ void combine_head(int b, int h, const float *__restri
       a += red_o[wi][d];
       ls += red_l[wi];
     }
-    const float rr = ls > 0.f ? a / ls : 0.f;
+    const float rr = ls == 0.f ? 0.f : a / ls;  // (NaN where the sum is)
     const __nv_bfloat16 rb = __float2bfloat16_rn(rr);
     o[(static_cast<size_t>(b) * hq + h) * D + d] = *reinterpret_cast<const uint16_t *>(&rb);
     if (lse != nullptr && d == 0)
-      lse[static_cast<size_t>(b) * hq + h] = ls > 0.f ? (m + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+      lse[static_cast<size_t>(b) * hq + h] = ls == 0.f ? -INFINITY : (m + log2f(ls)) * 0.69314718055994531f;
   }
   __syncthreads();  // red_o / red_l are reused by the next head
 }

@@ -306,6 +306,16 @@ __device__ __forceinline__ void named_barrier(int id, int count) {
 
 // ---------------------------------------------------------------- math
 
+// The larger of two, NaN if either is (fmaxf gives the other one).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The maximum under which a softmax part (max m, sum l) is merged with others: NaN where the sum is, so that the
+// merge gives NaN too.  m itself, made by maxima that pass NaN over, may be any value then, -inf among them.
+__device__ __forceinline__ float part_max(float m, float l) { return l == l ? m : l; }
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -1,0 +1,58 @@
+"""Infinities and NaN go where the formulas take them: to every row that uses them, whatever the batch around
+it, and to no other.  Everything else keeps the bits that it has with zeros in their place."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from block_sparse_long_kv_gb300 import build
+    build.build()
+
+
+@pytest.mark.parametrize("n", [40, 9000])
+@pytest.mark.parametrize("group", [1, 8])
+def test_decode_of_a_query_with_nan(n, group):
+    """One decode row of NaN, in one CTA's run or split over many, in two calls and in the one-launch step."""
+    import block_sparse_long_kv_gb300 as bsa
+    hkv, d, block = 2, 128, 128
+    hq = hkv * group
+    g = torch.Generator().manual_seed(n)
+    s = bsa.make_varlen_shape(2, 2 * n, n, hq, hkv, d, block)
+    nbs = bsa.varlen_block_stride(s)
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    rnd = lambda *shape: torch.randn(*shape, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = rnd(2, hq, d), rnd(2 * n, hkv, d), rnd(2 * n, hkv, d)
+    meta = bsa.alloc_varlen_meta(s)
+    bsa.varlen_block_meta(s, cu, k, meta["centroid"], meta["radius"], meta["quant"], meta["alpha"])
+    used = -(-n // block)
+    idx = torch.arange(nbs, dtype=torch.int32, device="cuda").expand(2, hkv, nbs).contiguous()
+    cnt = torch.full((2, hkv), used, dtype=torch.int32, device="cuda")
+
+    def run(q):
+        o, lse = torch.zeros(2, hq, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, hq, device="cuda")
+        bsa.decode_fwd(s, cu, q, k, v, idx, cnt, 1 / math.sqrt(d), o, lse)
+        o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+        bsa.decode_step(s, bsa.SelectParams(0.5, 0.1, 0), cu, q, k, v, meta["centroid"], meta["radius"], meta["alpha"],
+                        1 / math.sqrt(d), idx.clone(), cnt.clone(), o2, lse2)
+        torch.cuda.synchronize()
+        return o, lse, o2, lse2
+
+    want = run(q)
+    h = hq - 1
+    q[1, h, 5] = NAN
+    got = run(q)
+    for x in got:
+        assert torch.isnan(x[1, h].float()).all()
+    for x, w in zip(got[:2], want[:2]):                        # (the step's selection sees the NaN too)
+        x[1, h] = w[1, h]
+        assert torch.equal(x, w)
+    for x, w in zip(got[2:], want[2:]):
+        assert torch.equal(x[0], w[0]) and torch.isfinite(x[0].float()).all()
