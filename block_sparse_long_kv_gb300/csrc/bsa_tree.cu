@@ -416,6 +416,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       l_lo += __shfl_xor_sync(0xffffffffu, l_lo, off);
       l_hi += __shfl_xor_sync(0xffffffffu, l_hi, off);
     }
+    m_lo = ptx::part_max(m_lo, l_lo);
+    m_hi = ptx::part_max(m_hi, l_hi);
     if (tq == 0) {
       wm[warp][gq] = m_lo;
       wm[warp][gq + 8] = m_hi;
@@ -426,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     float mlo = -INFINITY, mhi = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kWarps; ++x) {
-      mlo = fmaxf(mlo, wm[x][gq]);
-      mhi = fmaxf(mhi, wm[x][gq + 8]);
+      mlo = ptx::max_nan(mlo, wm[x][gq]);
+      mhi = ptx::max_nan(mhi, wm[x][gq + 8]);
     }
     const float unit_f = Q16 && eref != 0 ? exp2f(static_cast<float>(eref - C::UNIT1)) : 1.f;
     const float slo = m_lo == -INFINITY ? 0.f : ptx::ex2_approx(m_lo - mlo) * unit_f;
@@ -462,18 +464,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       if (t >= adr.len) continue;
       float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) m = fmaxf(m, wm[x][r]);
+      for (int x = 0; x < kWarps; ++x) m = ptx::max_nan(m, wm[x][r]);
 #pragma unroll
       for (int x = 0; x < kWarps; ++x)
         if (wm[x][r] != -INFINITY) l = fmaf(ptx::ex2_approx(wm[x][r] - m), wl[x][r], l);
       const float *from = obuf + r * C::LDO + d4 / (D / 8) + 8 * (d4 % (D / 8));
       const float4 v = make_float4(from[0], from[8], from[16], from[24]);
       if (whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
         const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + row % G;
         *reinterpret_cast<uint2 *>(a.o + at * D + d4) =
             make_uint2(ptx::pack_bf16x2(v.x * inv, v.y * inv), ptx::pack_bf16x2(v.z * inv, v.w * inv));
-        if (a.lse != nullptr && d4 == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.lse != nullptr && d4 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       } else {
         *reinterpret_cast<float4 *>(part_o + (slot * kRows + r) * D + d4) = v;
         if (d4 == 0) *reinterpret_cast<float2 *>(part_ml + (slot * kRows + r) * 2) = make_float2(m, l);
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (ml[u].x == -INFINITY) continue;
-      const float mn = fmaxf(m, ml[u].x);
+      const float mn = ptx::max_nan(m, ml[u].x);
       const float f = m == -INFINITY ? 0.f : exp2f(m - mn), wgt = exp2f(ml[u].x - mn);
       m = mn;
       l = fmaf(ml[u].y, wgt, l * f);
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   __syncthreads();
   float mm = -INFINITY, fw[kCombineWarps];
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) mm = fmaxf(mm, red_m[w]);
+  for (int w = 0; w < kCombineWarps; ++w) mm = ptx::max_nan(mm, red_m[w]);
 #pragma unroll
   for (int w = 0; w < kCombineWarps; ++w) fw[w] = red_m[w] == -INFINITY ? 0.f : exp2f(red_m[w] - mm);
   const size_t out = static_cast<size_t>(run.draft0 + t) * a.hq + (run.group % a.c.hkv) * a.group + row % a.group;
@@ -882,9 +884,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
       s = fmaf(red_o[w][d], fw[w], s);
       ls = fmaf(red_l[w], fw[w], ls);
     }
-    const __nv_bfloat16 v = __float2bfloat16_rn(ls > 0.f ? s / ls : 0.f);
+    const __nv_bfloat16 v = __float2bfloat16_rn(ls == 0.f ? 0.f : s / ls);
     a.o[out * D + d] = *reinterpret_cast<const uint16_t *>(&v);
-    if (a.lse != nullptr && d == 0) a.lse[out] = ls > 0.f ? (mm + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+    if (a.lse != nullptr && d == 0) a.lse[out] = ls == 0.f ? -INFINITY : (mm + log2f(ls)) * 0.69314718055994531f;
   }
 }
 

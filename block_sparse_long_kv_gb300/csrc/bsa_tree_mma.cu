@@ -1114,6 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         ++lane_segs;
       }
+      m = ptx::part_max(m, l);
       const bool whole = s.rs >= x0 && s.re <= x1;
       const size_t slot = (2 * static_cast<size_t>(cta) + (s.rs <= x0 ? 0 : 1)) * C::NTQ + (PAIR ? t : 0);
       float unit_f = 1.f;
@@ -1146,7 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(C::B_LA, n_seg & 1))) break;
         const float4 ml = mine_o[D / 4 * kRows + r];
         if (ml.z != 0.f && ml.x != -INFINITY) {
-          const float mm = fmaxf(m, ml.x);
+          const float mm = ptx::max_nan(m, ml.x);
           const float f0 = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mm);
           other_f = ptx::ex2_approx(ml.x - mm);
           l = l * f0 + ml.y * other_f;
@@ -1154,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mm;
         }
       }
-      const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
       const size_t out = static_cast<size_t>(dr.start + tok) * a.hq + (s.grp % a.c.hkv) * G + row % G;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1194,7 +1195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (whole) {
-        if (live && a.lse != nullptr) a.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (live && a.lse != nullptr) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       } else {
         *reinterpret_cast<float2 *>(part_ml + (slot * kRows + r) * 2) = make_float2(m, l);
       }
@@ -1259,7 +1260,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (ml[u].x == -INFINITY) continue;
-      const float mn = fmaxf(m, ml[u].x);
+      const float mn = ptx::max_nan(m, ml[u].x);
       const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(ml[u].x - mn);
       m = mn;
       l = fmaf(ml[u].y, w, l * f);
@@ -1280,7 +1281,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(co
   if (warp >= NQ) return;  // warp q finishes dimensions 4 (q0 + q) ..
   float mm = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) mm = fmaxf(mm, red_m[w][lane]);
+  for (int w = 0; w < kCombineWarps; ++w) mm = ptx::max_nan(mm, red_m[w][lane]);
   float ls = 0.f;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1295,11 +1296,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_mma_combine_kernel(co
     s.w = fmaf(v.w, f, s.w);
   }
   if (tok >= run.drafts) return;
-  const float inv = ls > 0.f ? 1.f / ls : 0.f;
+  const float inv = ls == 0.f ? 0.f : 1.f / ls;
   const size_t out = static_cast<size_t>(run.draft0 + tok) * a.hq + (run.group % a.c.hkv) * a.group + row % a.group;
   *reinterpret_cast<uint2 *>(a.o + out * D + 4 * (q0 + warp)) =
       make_uint2(ptx::pack_bf16x2(s.x * inv, s.y * inv), ptx::pack_bf16x2(s.z * inv, s.w * inv));
-  if (a.lse != nullptr && q0 + warp == 0) a.lse[out] = ls > 0.f ? (mm + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+  if (a.lse != nullptr && q0 + warp == 0) a.lse[out] = ls == 0.f ? -INFINITY : (mm + log2f(ls)) * 0.69314718055994531f;
 }
 
 struct Workspace {

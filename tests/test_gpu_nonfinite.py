@@ -5,8 +5,10 @@ import math
 import pytest
 import torch
 
+from test_gpu_tree import FMTS, Case
+
 pytestmark = pytest.mark.gpu
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -15,6 +17,29 @@ def built():
         pytest.skip("no CUDA device")
     from block_sparse_long_kv_gb300 import build
     build.build()
+
+
+# one row tile in one CTA, and tiles shared by many CTAs; few rows, up to 128 rows, more
+SPLITS = [[40], [9000], [700, 3000]]
+DRAFTS = [4, 20, 70]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lengths", SPLITS)
+@pytest.mark.parametrize("drafts", DRAFTS)
+def test_a_query_with_nan_gives_nan_however_its_tile_is_split(fmt, lengths, drafts):
+    c = Case(fmt, lengths, [drafts] * len(lengths), 8, 2, 128, 64, seed=drafts)
+    bad = [(1, 0, NAN), (2, 5, INF), (drafts * len(lengths) - 1, 7, NAN)]
+    for t, h, _ in bad:
+        c.q[t, h] = 0
+    o, lse = c.run()
+    for t, h, value in bad:
+        c.q[t, h, 3] = value
+    got, gl = c.run()
+    for t, h, _ in bad:
+        assert torch.isnan(got[t, h].float()).all() and torch.isnan(gl[t, h]), (t, h)
+        got[t, h], gl[t, h] = o[t, h], lse[t, h]
+    assert torch.equal(got, o) and torch.equal(gl, lse)
 
 
 @pytest.mark.parametrize("n", [40, 9000])
