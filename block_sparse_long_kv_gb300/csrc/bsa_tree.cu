@@ -220,6 +220,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   const int groups = a.batch * a.c.hkv;
   int *per = pre + groups + 1;
   __shared__ int wsum[kWarps];
+  __shared__ int not_finite_flag;  // drafted values of the tile held Inf or NaN
+  volatile int *not_finite_v = &not_finite_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
@@ -251,7 +253,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       pre[x] = run;
       run += c;
     }
-    if (tid == 0) pre[groups] = n;
+    if (tid == 0) {
+      pre[groups] = n;
+      *not_finite_v = 0;
+    }
     __syncthreads();
   }
   const int n_all = pre[groups];
@@ -456,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     const int rs = pre[arow_g] + arow_t * per[arow_g], re = rs + per[arow_g];
     const bool whole = rs >= x0 && re <= x1;
     const size_t slot = 2 * static_cast<size_t>(cta) + (rs <= x0 ? 0 : 1);
+    const bool lost = *not_finite_v != 0;
     constexpr int PIECES = D / 4;
 #pragma unroll 1
     for (int e = tid; e < kRows * PIECES; e += kThreads) {
@@ -469,7 +475,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       for (int x = 0; x < kWarps; ++x)
         if (wm[x][r] != -INFINITY) l = fmaf(ptx::ex2_approx(wm[x][r] - m), wl[x][r], l);
       const float *from = obuf + r * C::LDO + d4 / (D / 8) + 8 * (d4 % (D / 8));
-      const float4 v = make_float4(from[0], from[8], from[16], from[24]);
+      float4 v = make_float4(from[0], from[8], from[16], from[24]);
+      if (lost) {  // Inf and NaN of the drafted values the row sees
+        const uint16_t *vn = a.v_new + (static_cast<size_t>(adr.start) * a.c.hkv + arow_g % a.c.hkv) * D + d4;
+        for (int p = t; p >= 0; p = parent_of(a, adr.start, p)) {
+          const uint2 u = *reinterpret_cast<const uint2 *>(vn + static_cast<size_t>(p) * a.c.hkv * D);
+          v.x += not_finite(u.x);
+          v.y += not_finite(u.x >> 16);
+          v.z += not_finite(u.y);
+          v.w += not_finite(u.y >> 16);
+        }
+      }
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
         const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + row % G;
@@ -482,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       }
     }
     __syncthreads();  // obuf and wm are free again
+    if (tid == 0) *not_finite_v = 0;
   };
 
   // The softmax step of a 16-key slice: x holds the logits (log2 units, -inf where masked), and on
@@ -759,13 +776,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       const uint16_t *vr[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) vr[x] = row_of(a.v_new, k0 + 2 * tq + (x & 1) + 8 * (x >> 1));
+      uint32_t lost = 0u;  // not 0: Inf or NaN among the values
 #pragma unroll
       for (int w = 0; w < C::NNT / 2; ++w) {
         const int dim = gq * (D / 8) + 2 * w;
-        const uint32_t v0 = finite_bf16x2(word(vr[0], dim)), v1 = finite_bf16x2(word(vr[1], dim)),
-                       v2 = finite_bf16x2(word(vr[2], dim)), v3 = finite_bf16x2(word(vr[3], dim));
-        mma<true>(o[2 * w], pa, __byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410));
-        mma<true>(o[2 * w + 1], pa, __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x7632));
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = finite_bf16x2(word(vr[e], dim), lost);
+        mma<true>(o[2 * w], pa, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
+        mma<true>(o[2 * w + 1], pa, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+      }
+      if (__any_sync(0xffffffffu, lost != 0u)) {
+        if (lane == 0) *not_finite_v = 1;
       }
     }
     __syncthreads();  // dmask is free again

@@ -93,12 +93,18 @@ __device__ __forceinline__ int shared_tile(const TreeRun *runs, int ctas, int x,
   return found_at;
 }
 
-// Infinities and NaN of two bf16 values become 0.  A drafted row that holds some is hidden from the rows of other
-// branches by p = 0 alone, and 0 times it would not be 0.
-__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
-  return w;
+// Infinities and NaN of two bf16 values become 0.  A drafted value row that holds some is hidden from the rows of
+// other branches by p = 0 alone, and 0 times it would not be 0: P V runs without them, and the rows that do attend
+// to the token get them added to O, which is what p > 0 times them adds up to.  (A key's stay in its logit.)
+// `lost` gets a bit where there were any.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, uint32_t &lost) {
+  const uint32_t bad = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;  // an exponent of ones carries into its sign bit
+  lost |= bad;
+  return w & ~((bad >> 15) * 0xFFFFu);
+}
+// A bf16 value if it is Inf or NaN, else 0.
+__device__ __forceinline__ float not_finite(uint32_t bf16) {
+  return (bf16 & 0x7F80u) == 0x7F80u ? __uint_as_float(bf16 << 16) : 0.f;
 }
 
 }  // namespace bsa

@@ -105,8 +105,9 @@ struct Cfg {
                        B_UG = B_UN + kLists, B_IK = B_UG + 1, B_IV = B_IK + kInfo, B_RS = B_IV + kInfo, B_LK = B_RS + 2,
                        B_LV = B_LK + 1, B_LA = B_LV + 1, B_LB = B_LA + 1, B_FIN = B_LB + 1, NBARS = B_FIN + 1;
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag, scan sums
-  static constexpr uint32_t OFF_INFO = OFF_MISC + 128;                        // [kInfo] K's scale, [kInfo] oref
-  static constexpr uint32_t OFF_ROWS = OFF_INFO + kInfo * 8;                  // [2][NTQ * 128] row scales of Q
+  // [kInfo] K's scale, [kInfo] oref, [kInfo][4] whether a V loader warp met Inf or NaN in drafted rows
+  static constexpr uint32_t OFF_INFO = OFF_MISC + 128;
+  static constexpr uint32_t OFF_ROWS = OFF_INFO + kInfo * 12;                 // [2][NTQ * 128] row scales of Q
   static constexpr uint32_t OFF_RED = OFF_ROWS + 2 * NTQ * 128 * 4;           // [8] loader maxima
   static constexpr uint32_t OFF_UNIT = OFF_RED + 32;                          // [kLists][kBatch] {int4, int4}
   static constexpr uint32_t OFF_PRE = OFF_UNIT + kLists * kBatch * 32;        // [groups + 1] first unit
@@ -149,8 +150,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint4 finite_bf16x8(const uint4 &v) {
-  return make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+__device__ __forceinline__ uint4 finite_bf16x8(const uint4 &v, uint32_t &lost) {
+  return make_uint4(finite_bf16x2(v.x, lost), finite_bf16x2(v.y, lost), finite_bf16x2(v.z, lost), finite_bf16x2(v.w, lost));
 }
 __device__ __forceinline__ float amax8(const uint4 &v) {  // of eight bf16
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *scan = reinterpret_cast<int *>(sb + C::OFF_MISC + 16);  // [16]
   float *info_k = reinterpret_cast<float *>(sb + C::OFF_INFO);
   int *info_v = reinterpret_cast<int *>(info_k + kInfo);
+  uint32_t *lost_v = reinterpret_cast<uint32_t *>(info_v + kInfo);
   float *row_scale = reinterpret_cast<float *>(sb + C::OFF_ROWS);
   float *red = reinterpret_cast<float *>(sb + C::OFF_RED);
   int4 *unit = reinterpret_cast<int4 *>(sb + C::OFF_UNIT);
@@ -750,9 +752,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // bf16 rows by hand: `n` keys of chunk h, from `from` (row stride in elements); zeros past n
-    auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f, bool drafted) {
-      constexpr int PR = D / 8, TOTAL = kChunk * PR / 128, U = TOTAL < 8 ? TOTAL : 8;
+    // bf16 rows by hand: `n` keys of chunk h, from `from` (row stride in elements); zeros past n, and with `clean`
+    // in place of Inf and NaN.  Not 0 if there were any.  (Four pieces in flight: eight leave the codec spilling,
+    // 249 against 241 us for 64 drafts over e4m3.)
+    auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f, bool clean) -> uint32_t {
+      uint32_t lost = 0u;
+      constexpr int PR = D / 8, TOTAL = kChunk * PR / 128, U = 4;
 #pragma unroll 1
       for (int b = 0; b < TOTAL; b += U) {
         uint4 v[U];
@@ -765,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < U; ++e) {
           const int x = (b + e) * 128 + lt;
-          if (drafted) v[e] = finite_bf16x8(v[e]);
+          if (clean) v[e] = finite_bf16x8(v[e], lost);
           if constexpr (Q16) {
             uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
@@ -776,14 +781,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           put16(swizzled(dst, (x % PR) >> 3, h * kChunk + x / PR, x % PR & 7), v[e]);
         }
       }
+      return lost;
     };
-    // the exponent reference of a unit of drafted rows: its largest element lands in [2^14, 2^15)
+    // the exponent reference of a unit of drafted rows: its largest finite element lands in [2^14, 2^15)
     auto draft_ref = [&](const uint16_t *from, size_t stride, int n, bool &ok) -> int {
       constexpr int PR = D / 8;
       float am = 0.f;
-#pragma unroll 8
+      uint32_t lost = 0u;
+#pragma unroll 4
       for (int x = lt; x < n * PR; x += 128)
-        am = fmaxf(am, amax8(finite_bf16x8(__ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8)))));
+        am = fmaxf(am, amax8(finite_bf16x8(__ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8)), lost)));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
       if (lane == 0) red[lw] = am;
@@ -838,7 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n + 1 < nu) fetch_scales(n + 1);
       }
-      arrive_warp((kv == 0 ? C::B_IK : C::B_IV) + n % kInfo);
+      // (what a V loader has to say of drafted rows it knows when it has written them)
+      if (kv == 0 || !d0.z) arrive_warp((kv == 0 ? C::B_IK : C::B_IV) + n % kInfo);
 
       // ---- wait for the stage and fill it
       if (st + 1 == stages || st < 0) st = 0, ++round;
@@ -867,8 +875,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (d0.z) {
         const float f = Q16 ? pow2_biased(254 + C::SHV - ref) : 1.f;
-        store_rows(tile, 0, drafted, dstride, n0, f, true);
-        store_rows(tile, 1, drafted + kChunk * dstride, dstride, n1, f, true);
+        uint32_t lost = store_rows(tile, 0, drafted, dstride, n0, f, kv == 1);
+        lost |= store_rows(tile, 1, drafted + kChunk * dstride, dstride, n1, f, kv == 1);
+        if (kv == 1) {
+          const bool any = __any_sync(0xffffffffu, lost != 0u);
+          if (lane == 0) reinterpret_cast<uint8_t *>(lost_v + n % kInfo)[lw & 3] = any;
+          arrive_warp(C::B_IV + n % kInfo);
+        }
         for (int gr = 0; Q16 && gr < NG; ++gr) {  // the unit's empty groups
           copy_group(slot);
           slot = slot == C::RING - 1 ? 0 : slot + 1;
@@ -1113,6 +1126,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(C::B_OD + t, lane_segs & 1))) break;
         ptx::tc_fence_after();
         ++lane_segs;
+      }
+      // whether the segment's drafted values (its last units, two at most) held Inf or NaN; kInfo units are kept
+      bool lost = false;
+      for (int i = max(0, s.units - 2); i < s.units; ++i) {
+        const uint32_t u = n - static_cast<uint32_t>(s.units - i);
+        if ((PAIR || (i & 1) == t) && unit[2 * (u % (kLists * kBatch))].z != 0) lost |= lost_v[u % kInfo] != 0u;
+      }
+      if (lost) {  // warp-uniform; those that the row sees, into O
+        const uint16_t *vn = a.v_new + (static_cast<size_t>(dr.start) * a.c.hkv + s.grp % a.c.hkv) * D;
+#pragma unroll 1
+        for (int q = 0; q < D / 8; ++q) {
+          uint32_t ov[8];
+          ptx::tmem_ld8(tO + q * 8, ov);
+          ptx::tmem_wait_ld();
+          if (live)
+            for (int p = tok; p >= 0; p = parent_of(a, dr.start, p)) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4 *>(vn + static_cast<size_t>(p) * a.c.hkv * D + q * 8));
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                ov[e] = __float_as_uint(__uint_as_float(ov[e]) + not_finite(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu));
+            }
+          __syncwarp();
+          ptx::tmem_st8(tO + q * 8, ov);
+        }
+        ptx::tmem_wait_st();
       }
       m = ptx::part_max(m, l);
       const bool whole = s.rs >= x0 && s.re <= x1;

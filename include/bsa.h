@@ -550,8 +550,9 @@ bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t t
  *   [total_draft, hq], nullable) the natural log of the normaliser.
  * The dot products use the held values exactly; softmax statistics and sums
  * are fp32.  One drafted token is a decode step.  Rows past cu_draft[batch] are
- * left as they were.  A drafted token whose k_new or v_new holds Inf or NaN
- * harms the tokens that attend to it alone.  With an 8- or 4-bit cache and more
+ * left as they were.  Inf and NaN in q, k_new or v_new go where the formula takes
+ * them: into the rows that attend to them (of v_new into those dimensions of
+ * theirs), and into no other row.  With an 8- or 4-bit cache and more
  * than 16 rows (drafted tokens x G) a sequence, the drafted keys (values) of one
  * KV head are held in f16 under one power of two per 128 drafted tokens: elements
  * 2^28 below the largest of them lose bits.

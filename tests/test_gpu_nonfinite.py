@@ -19,6 +19,11 @@ def built():
     build.build()
 
 
+def same(a, b):
+    """Equal bits, NaN equal to NaN."""
+    return torch.equal(torch.nan_to_num(a.float(), 12345.0, 23456.0, -23456.0), torch.nan_to_num(b.float(), 12345.0, 23456.0, -23456.0))
+
+
 # one row tile in one CTA, and tiles shared by many CTAs; few rows, up to 128 rows, more
 SPLITS = [[40], [9000], [700, 3000]]
 DRAFTS = [4, 20, 70]
@@ -40,6 +45,60 @@ def test_a_query_with_nan_gives_nan_however_its_tile_is_split(fmt, lengths, draf
         assert torch.isnan(got[t, h].float()).all() and torch.isnan(gl[t, h]), (t, h)
         got[t, h], gl[t, h] = o[t, h], lse[t, h]
     assert torch.equal(got, o) and torch.equal(gl, lse)
+
+
+def descends(parents, j):
+    """The tokens that attend to drafted token j."""
+    out = []
+    for i in range(len(parents)):
+        p = i
+        while p > j:
+            p = parents[p]
+        if p == j:
+            out.append(i)
+    return out
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("length", [0, 40, 9000])
+@pytest.mark.parametrize("drafts", [4, 20, 70, 200])
+def test_a_drafted_value_with_inf_or_nan_reaches_those_that_attend_to_it(fmt, length, drafts):
+    """v_new of two tokens: the dimensions that hold Inf or NaN come out as the formula gives them, the others and
+    lse as with zeros there."""
+    c = Case(fmt, [length], [drafts], 8, 2, 128, 64, seed=drafts)
+    c.parents[0][1] = c.parents[0][2] = 0
+    tokens = [(1, slice(0, 128, 5), NAN), (drafts // 2, slice(2, 128, 7), INF), (drafts - 1, slice(3, 128, 11), -INF)]
+    for j, dims, _ in tokens:
+        c.v_new[j, 1, dims] = 0
+    want, wl = c.run()
+    want = want.float()
+    for j, dims, value in tokens:
+        c.v_new[j, 1, dims] = value
+        for i in descends(c.parents[0], j):
+            want[i, 4:, dims] += value
+    got, gl = c.run()
+    assert torch.isnan(want).any() and torch.isinf(want).any()
+    assert same(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("length", [0, 40, 9000])
+@pytest.mark.parametrize("drafts", [4, 20, 70, 200])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_a_drafted_key_with_inf_or_nan_reaches_those_that_attend_to_it(fmt, length, drafts, value):
+    """A key whose logit is NaN or +Inf makes its rows NaN; no other row changes."""
+    c = Case(fmt, [length], [drafts], 8, 2, 128, 64, seed=drafts)
+    c.parents[0][1] = c.parents[0][2] = 0
+    j = drafts // 2
+    c.k_new[j, 0, 9] = 0
+    c.q[:, :4, 9] = c.q[:, :4, 9].abs() + 1
+    want, wl = c.run()
+    c.k_new[j, 0, 9] = value
+    got, gl = c.run()
+    for i in descends(c.parents[0], j):
+        assert torch.isnan(got[i, :4].float()).all() and torch.isnan(gl[i, :4]).all(), i
+        got[i, :4], gl[i, :4] = want[i, :4], wl[i, :4]
+    assert torch.equal(got, want) and torch.equal(gl, wl)
 
 
 @pytest.mark.parametrize("n", [40, 9000])
