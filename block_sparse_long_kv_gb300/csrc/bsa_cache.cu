@@ -12,6 +12,9 @@
 // one (in the units of the codes).  x * (1 / s) is within 2^-20 of it; rounding
 // that to a multiple of 2^-13 restores the ties and moves nothing across one.
 //
+// Inf and NaN have no code in E4M3 but NaN's, and none in E2M1: there the group scale is NaN instead.  They do
+// not count in the row's amax, so the other elements (in E2M1 the other groups) keep their bits.
+//
 // Read.  D / 16 lanes take sixteen values of a row each and write two 16-byte words
 // of bf16; the values are exact (a code has at most six significant bits after its
 // group scale).
@@ -78,6 +81,20 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
       : "r"(a), "r"(b));
   return r;
 }
+// As above, but a NaN stays one.
+__device__ __forceinline__ uint32_t max_abs_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}"
+      : "=r"(r)
+      : "r"(a), "r"(b));
+  return r;
+}
+// Infinities become NaN (0 * x + x), all else stays.
+__device__ __forceinline__ uint32_t inf_to_nan_bf16x2(uint32_t a) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(r) : "r"(a), "r"(0u));
+  return r;
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -127,11 +144,23 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
       }
     } else {
       uint8_t *scales = (kv == 0 ? a.k_scales : a.v_scales) + tile * a.c.page * PER;
-      const uint32_t x[8] = {raw[kv][0].x, raw[kv][0].y, raw[kv][0].z, raw[kv][0].w,
-                             raw[kv][1].x, raw[kv][1].y, raw[kv][1].z, raw[kv][1].w};
-      const uint32_t m0 = max_abs_bf16x2(max_abs_bf16x2(x[0], x[1]), max_abs_bf16x2(x[2], x[3]));
-      const uint32_t m1 = max_abs_bf16x2(max_abs_bf16x2(x[4], x[5]), max_abs_bf16x2(x[6], x[7]));
-      const uint32_t mine = max_abs_bf16x2(m0, m1);
+      uint32_t x[8] = {raw[kv][0].x, raw[kv][0].y, raw[kv][0].z, raw[kv][0].w,
+                       raw[kv][1].x, raw[kv][1].y, raw[kv][1].z, raw[kv][1].w};
+      uint32_t mine;
+      bool lost = false;  // the group holds Inf or NaN
+      if constexpr (FMT == BSA_CACHE_E4M3) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = inf_to_nan_bf16x2(x[e]);
+        const uint32_t m0 = max_abs_bf16x2(max_abs_bf16x2(x[0], x[1]), max_abs_bf16x2(x[2], x[3]));
+        const uint32_t m1 = max_abs_bf16x2(max_abs_bf16x2(x[4], x[5]), max_abs_bf16x2(x[6], x[7]));
+        mine = max_abs_bf16x2(m0, m1);
+      } else {
+        const uint32_t m0 = max_abs_nan_bf16x2(max_abs_nan_bf16x2(x[0], x[1]), max_abs_nan_bf16x2(x[2], x[3]));
+        const uint32_t m1 = max_abs_nan_bf16x2(max_abs_nan_bf16x2(x[4], x[5]), max_abs_nan_bf16x2(x[6], x[7]));
+        mine = max_abs_nan_bf16x2(m0, m1);
+        lost = (mine & 0x7F80u) == 0x7F80u || (mine & 0x7F800000u) == 0x7F800000u;
+        if (lost) mine = 0u;
+      }
       uint32_t all = mine;
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) all = max_abs_bf16x2(all, __shfl_xor_sync(0xffffffffu, all, o));
@@ -153,7 +182,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
         // the lane's sixteen values are one group
         const int k = row_exponent(am, 0x280000, 11);  // 2688 = 1.3125 * 2^11
         const uint32_t inv = static_cast<uint32_t>(127 - k) * 0x00800080u;
-        const uint32_t s8 = e4m3x2(larger_half(mine) * pow2i(-k) / 6.f, 0.f);
+        const uint32_t s8 = lost ? 0x7Fu : e4m3x2(larger_half(mine) * pow2i(-k) / 6.f, 0.f);
         const float s = e4m3x2_f32(s8).x;
         const float f = s > 0.f ? __frcp_rn(s) : 0.f;
         const uint64_t f2 = ptx::f32x2(f, f), up = ptx::f32x2(1536.f, 1536.f), down = ptx::f32x2(-1536.f, -1536.f);

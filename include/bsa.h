@@ -490,7 +490,10 @@ bsa_status bsa_qk_norm_rope(const bsa_rope_shape *shape, const void *q, int64_t 
  *                   * 2^(127 - e) / 6), a code RN(x * 2^(127 - e) / scale)
  *                   saturated at 6 (0 where the scale is 0); even dimensions in
  *                   the low four bits of a byte
- * Roundings are to nearest, ties to even.  Every held value is a bf16 value
+ * Inf and NaN are held by BF16 alone: an E4M3 element that is either is held as
+ * NaN, and an E2M1 group with one as 16 NaN (its group scale); neither counts in a
+ * maximum.
+ * Roundings are to nearest, ties to even.  Every other held value is a bf16 value
  * (E4M3 and E2M1 down to bf16's smallest normal times the code's own range).
  * Supported: head_dim in {64, 128}; page in {64, 128, 256}; pages * page and
  * pages * hkv < 2^31.  Code and scale arrays 16-byte aligned; scale pointers are ignored (may

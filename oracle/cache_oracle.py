@@ -73,15 +73,22 @@ def quantise(x, fmt):
     if fmt == BF16:
         bits = np.ascontiguousarray(x, dtype=np.float32).view(np.uint32) >> 16
         return np.ascontiguousarray(bits.astype(np.uint16)).view(np.uint8), None, None
+    bad = ~np.isfinite(x)                                  # NaN's code; in E2M1 a NaN scale for the whole group
+    if fmt == E2M1:
+        bad = bad.reshape(*x.shape[:-1], x.shape[-1] // 16, 16).any(-1, keepdims=True) & np.ones(16, bool)
+        bad = bad.reshape(x.shape)
+    x = np.where(bad, 0.0, x)
     amax = np.abs(x).max(-1)
     k = _least_exponent(amax, 448.0 if fmt == E4M3 else 2688.0)
     y = x * np.ldexp(1.0, -k)[..., None]
     sign = np.signbit(x)
     if fmt == E4M3:
-        return (_nearest(np.abs(y), E4M3_VALUES) + 128 * sign).astype(np.uint8), (k + 127).astype(np.uint8), None
+        c = np.where(bad, 127, _nearest(np.abs(y), E4M3_VALUES) + 128 * sign)
+        return c.astype(np.uint8), (k + 127).astype(np.uint8), None
     g = y.reshape(*y.shape[:-1], y.shape[-1] // 16, 16)
     s8 = _nearest(np.abs(g).max(-1) / 6.0, E4M3_VALUES)
     s = E4M3_VALUES[s8][..., None]
+    s8 = np.where(bad.reshape(g.shape)[..., 0], 127, s8)
     c = np.where(s > 0, _nearest(np.abs(g) / np.where(s > 0, s, 1.0), E2M1_VALUES), 0)
     c = (c + 8 * (sign.reshape(g.shape) & (s > 0))).reshape(y.shape).astype(np.uint8)
     return c[..., 0::2] | (c[..., 1::2] << 4), (k + 127).astype(np.uint8), s8.astype(np.uint8)

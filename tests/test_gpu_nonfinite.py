@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from oracle import cache_oracle as C
 from test_gpu_tree import FMTS, Case
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +141,80 @@ def test_decode_of_a_query_with_nan(n, group):
         assert torch.equal(x, w)
     for x, w in zip(got[2:], want[2:]):
         assert torch.equal(x[0], w[0]) and torch.isfinite(x[0].float()).all()
+
+
+# ---------------------------------------------------------------- held in the cache
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_cache_holds_inf_and_nan_as_documented(fmt, d):
+    """Written and read back: BF16 as they are; E4M3 as NaN; E2M1 as NaN for the 16 dimensions of their group.
+    The other elements have the bytes of a row with zeros in their place."""
+    import block_sparse_long_kv_gb300 as bsa
+    n, hkv = 90, 2
+    g = torch.Generator().manual_seed(d)
+    x = (torch.randn(n, hkv, d, generator=g) * 10.0 ** torch.randint(-3, 3, (n, hkv, 1), generator=g)).to(torch.bfloat16)
+    bad = torch.zeros(n, hkv, d, dtype=torch.bool)
+    for t in range(n):
+        kind = t % 6
+        if kind < 3:
+            bad[t, t % hkv, torch.randperm(d, generator=g)[:1 + 3 * kind]] = True
+        elif kind == 3:
+            bad[t] = True                                      # nothing but Inf and NaN
+        elif kind == 4:
+            bad[t, :, 16:32] = True
+    clean = torch.where(bad, torch.zeros_like(x), x)
+    x = torch.where(bad, torch.tensor([NAN, INF, -INF]).to(torch.bfloat16)[torch.randint(0, 3, x.shape, generator=g)], x)
+    cs = bsa.make_cache_shape(2, 64, hkv, d, fmt)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    out = []
+    for rows in (x, clean):
+        cache = bsa.alloc_cache(cs)
+        for t in cache.values():
+            if t is not None:
+                t.fill_(0xA7)
+        bsa.cache_write(cs, rows.cuda(), -rows.cuda(), slots, cache)
+        ko, vo = torch.empty(n, hkv, d, dtype=torch.bfloat16, device="cuda"), torch.empty(n, hkv, d, dtype=torch.bfloat16, device="cuda")
+        bsa.cache_read(cs, torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                       torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), n, cache, ko, vo)
+        torch.cuda.synchronize()
+        out.append((cache, ko.cpu(), vo.cpu()))
+    (got, gk, gv), (want, wk, wv) = out
+    if fmt == C.BF16:
+        assert same(gk, x) and same(gv, -x)
+        return
+    lost = bad if fmt == C.E4M3 else bad.view(n, hkv, d // 16, 16).any(-1, keepdim=True).expand(n, hkv, d // 16, 16).reshape(n, hkv, d)
+    for a, b in ((gk, wk), (gv, wv)):
+        assert torch.isnan(a[lost].float()).all()
+        # in E2M1 the lost group's finite elements do not count in the row's exponent either
+        clear = ~lost if fmt == C.E4M3 else ~lost & ~lost.any(-1, keepdim=True)
+        assert torch.equal(a[clear], b[clear])
+    whole = bad.any(-1) & ~bad.all(-1) if fmt == C.E2M1 else torch.zeros(n, hkv, dtype=torch.bool)
+    if whole.any():                                            # those rows: as written with the whole group zero
+        zero = torch.where(lost, torch.zeros_like(x), x)
+        held = torch.from_numpy(C.held(zero.double().numpy(), fmt))
+        assert torch.equal(gk[~lost].double(), held[~lost])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("drafts", DRAFTS)
+def test_attention_over_held_nan(fmt, drafts):
+    """A cached key of NaN makes its head's rows NaN; a cached value of NaN the dimensions it is held in."""
+    c = Case(fmt, [300], [drafts], 8, 2, 128, 64, seed=drafts)
+    slots = c.table[0].numpy()[torch.arange(300).numpy() // 64] * 64 + torch.arange(300).numpy() % 64
+    c.v[100, 1, 20] = 0
+    if fmt == C.E2M1:
+        c.v[100, 1, 16:32] = 0
+    write = lambda: c.bsa.cache_write(c.cs, c.k.cuda(), c.v.cuda(), torch.from_numpy(slots.astype("int32")).cuda(), c.cache)
+    write()
+    want, wl = c.run()
+    c.k[200, 0, 7] = NAN
+    c.v[100, 1, 20] = NAN
+    write()
+    got, gl = c.run()
+    assert torch.isnan(got[:, :4].float()).all() and torch.isnan(gl[:, :4]).all()
+    assert torch.equal(gl[:, 4:], wl[:, 4:])
+    lost = torch.zeros(128, dtype=torch.bool)
+    lost[slice(16, 32) if fmt == C.E2M1 else 20] = True
+    assert torch.isnan(got[:, 4:][..., lost].float()).all()
+    assert torch.equal(got[:, 4:][..., ~lost], want[:, 4:][..., ~lost])

@@ -96,3 +96,18 @@ def test_siblings_do_not_see_each_other():
     o2, _, _, _ = C.tree_attention(q, kn2, vn2, k, v, [-1, 0, 0], 1.0)
     np.testing.assert_array_equal(o[[0, 2]], o2[[0, 2]])
     assert not np.array_equal(o[1], o2[1])
+
+
+@pytest.mark.parametrize("fmt", [C.E4M3, C.E2M1])
+def test_inf_and_nan_are_held_as_nan(fmt):
+    """The element's (E2M1: its group's) values are NaN, the others those of a row with zeros in their place."""
+    x = synth.bf16_to_f64(synth.bf16_bits(np.random.default_rng(7).normal(size=(40, 64)).astype(np.float32)))
+    bad = np.zeros(x.shape, bool)
+    for t in range(40):
+        bad[t, np.random.default_rng(t).permutation(64)[:t % 4]] = True
+    lost = bad if fmt == C.E4M3 else bad.reshape(40, 4, 16).any(-1, keepdims=True).repeat(16, -1).reshape(40, 64)
+    want = C.held(np.where(lost, 0.0, x), fmt)
+    x[bad] = np.random.default_rng(8).choice([np.nan, np.inf, -np.inf], size=bad.sum())
+    got = C.held(x, fmt)
+    assert np.isnan(got[lost]).all()
+    np.testing.assert_array_equal(got[~lost], want[~lost])
