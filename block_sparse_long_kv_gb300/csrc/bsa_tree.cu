@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
         } else if (a.status != nullptr) {
           atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
         }
+      } else if (j < 0 && a.status != nullptr) {
+        atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
       }
     }
     unit[u % (2 * kBatch)] = d;

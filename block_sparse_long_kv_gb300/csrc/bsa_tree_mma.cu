@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int e = (2 * k + h) >> (a.c.page_shift - 6);
-              j[h] = e >= kept ? -1 : a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
+              j[h] = e >= kept ? INT32_MAX : a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -587,6 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (a.status != nullptr) {
                   atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
                 }
+              } else if (j[h] < 0 && a.status != nullptr) {
+                atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
               }
             }
           }

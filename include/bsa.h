@@ -566,8 +566,10 @@ bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t t
  * device checks: an inconsistent cu_draft entry or cached[b] sets
  * BSA_ERR_INVALID_ARG in *dev_status and reads as no drafts / an empty cache, a
  * table entry outside the cache sets it and is left out, a parent that is not
- * smaller than its token sets it and reads as -1; list entries that name no
- * page of the sequence are left out.  workspace: bsa_tree_workspace_bytes bytes, 16-byte
+ * smaller than its token sets it and reads as -1.  Of a list, as many entries are
+ * read as the sequence has pages; one past its last page is left out (the list may
+ * have been selected with the new token's own block), a negative one sets
+ * BSA_ERR_INVALID_ARG too.  workspace: bsa_tree_workspace_bytes bytes, 16-byte
  * aligned, the caller's alone while the call runs; its contents need no
  * initialisation and are dead afterwards.  o and lse overlap no input.  cu_draft, cached, block_table and
  * parents 4-byte aligned, the rest 16-byte.

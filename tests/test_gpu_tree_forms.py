@@ -200,3 +200,45 @@ def test_more_groups_than_two_tiles_leave_room_for(fmt):
     c = Case(fmt, [(7 * b) % 40 if b % 9 else 0 for b in range(batch)], [max(0, drafts - (b % 4) * 11) for b in range(batch)],
              4 * hkv, hkv, 128, 64, seed=3)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("fmt", [C.BF16, C.E4M3])
+@pytest.mark.parametrize("drafts", [3, 20, 40])
+def test_a_negative_list_entry_is_reported(fmt, drafts):
+    """Entries past the sequence's last page are left out without a word (a selection made with the new token may
+    name the page that it will begin); a negative one is an error, reported, and its page left out."""
+    c = Case(fmt, [300], [drafts], 8, 2, 128, 64)
+    bsa = c.bsa
+    ts = bsa.make_tree_shape(1, drafts, drafts, 300, 8, c.stride)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def run(row, cnt):
+        idx = torch.full((1, 2, c.stride), 1 << 20, dtype=torch.int32)
+        idx[:, :, :len(row)] = torch.tensor(row, dtype=torch.int32)
+        o, lse = torch.zeros(drafts, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(drafts, 8, device="cuda")
+        st = dev([0])
+        bsa.tree_fwd(ts, c.cs, dev([0, drafts]), dev([300]), c.table.cuda(), dev(c.parents[0]), c.q.cuda(), c.k_new.cuda(),
+                     c.v_new.cuda(), c.cache, idx.cuda(), dev([[cnt, cnt]]), 1 / math.sqrt(128), o, lse, dev_status=st)
+        torch.cuda.synchronize()
+        return o, lse, int(st.item())
+
+    c.lists = [[[0, 3, 4], [0, 3, 4]]]                          # five pages in all
+    o, lse, code = run([0, 3, 4], 3)
+    assert code == 0
+    c.check(o, lse)
+    o, lse, code = run([0, 3, 4, 5], 4)
+    assert code == 0
+    c.check(o, lse)
+    c.lists = [[list(range(5)), list(range(5))]]
+    o, lse, code = run([0, 1, 2, 3, 4, 5], 6)                   # one entry more than the sequence has pages
+    assert code == 0
+    c.check(o, lse)
+    for bad in (-1, -(1 << 31)):
+        c.lists = [[[0, 3], [0, 3]]]
+        o, lse, code = run([bad, 0, 3], 3)
+        assert code == 1
+        c.check(o, lse)
+    o, lse, code = run([0, 3], -2)                              # a negative count is an empty list
+    assert code == 0
+    c.lists = [[[], []]]
+    c.check(o, lse)
