@@ -115,11 +115,12 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
   constexpr int RB = FMT == BSA_CACHE_BF16 ? 2 * D : FMT == BSA_CACHE_E4M3 ? D : D / 2;
   constexpr int PER = FMT == BSA_CACHE_BF16 ? 0 : FMT == BSA_CACHE_E4M3 ? 1 : 1 + D / 16;
   const uint32_t block = blockIdx.x / a.c.hkv, g = blockIdx.x - block * a.c.hkv;
-  const int t = static_cast<int>(block * (kCacheThreads / LPR) + threadIdx.x / LPR), c = threadIdx.x % LPR;
+  const uint32_t t = block * (kCacheThreads / LPR) + threadIdx.x / LPR;  // (the last stretch may pass 2^31 tokens)
+  const int c = threadIdx.x % LPR;
   uint4 raw[2][2];
   raw[0][0] = raw[0][1] = raw[1][0] = raw[1][1] = make_uint4(0u, 0u, 0u, 0u);
   int slot = -1;
-  if (t < a.tokens) {
+  if (t < static_cast<uint32_t>(a.tokens)) {
     slot = __ldg(a.slots + t);  // needed only when the rows have arrived
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -213,14 +214,9 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
   }
 }
 
-// CTAs of `heads` heads for every stretch of `per_cta` tokens, the heads of a stretch next to each other.
-unsigned cache_grid(int tokens, int per_cta, int heads) {
-  return (static_cast<unsigned>(tokens - 1) / per_cta + 1) * static_cast<unsigned>(heads);
-}
-
 template <int D, int FMT>
 cudaError_t write_t(const CacheWriteArgs &a, cudaStream_t stream) {
-  cache_write_kernel<D, FMT><<<cache_grid(a.tokens, kCacheThreads / (D / 16), a.c.hkv), kCacheThreads, 0, stream>>>(a);
+  cache_write_kernel<D, FMT><<<static_cast<unsigned>(cache_ctas(a.c, a.tokens)), kCacheThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -248,8 +244,9 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRe
   if (blockIdx.x == 0)  // every entry is checked, whether or not a row of it is met below
     for (int b = threadIdx.x; b < a.batch; b += kCacheThreads) seq_span(a.cu, b, a.max_seqlen, a.total, a.status);
   const uint32_t block = blockIdx.x / a.c.hkv, g = blockIdx.x - block * a.c.hkv;
-  const int t = static_cast<int>(block * (kCacheThreads / PPR) + threadIdx.x / PPR), c = threadIdx.x % PPR;
-  if (t >= a.total) return;
+  const uint32_t at = block * (kCacheThreads / PPR) + threadIdx.x / PPR;  // (the last stretch may pass 2^31 tokens)
+  if (at >= static_cast<uint32_t>(a.total)) return;
+  const int t = static_cast<int>(at), c = threadIdx.x % PPR;
   // the sequence that holds row t: the last b with cu[b] <= t
   int lo = 0, hi = a.batch - 1;
   while (lo < hi) {
@@ -313,11 +310,17 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRe
 
 template <int D, int FMT>
 cudaError_t read_t(const CacheReadArgs &a, cudaStream_t stream) {
-  cache_read_kernel<D, FMT><<<cache_grid(a.total, kCacheThreads / (D / 16), a.c.hkv), kCacheThreads, 0, stream>>>(a);
+  cache_read_kernel<D, FMT><<<static_cast<unsigned>(cache_ctas(a.c, a.total)), kCacheThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+// A CTA for every head of a stretch of tokens, the heads of a stretch next to each other.
+int64_t cache_ctas(const CacheDims &c, int tokens) {
+  const int per_cta = kCacheThreads / (c.d / 16);
+  return (static_cast<int64_t>(tokens) + per_cta - 1) / per_cta * c.hkv;
+}
 
 cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t stream) {
   const bool wide = a.c.d == 128;

@@ -36,6 +36,8 @@ struct CacheWriteArgs {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   int32_t *status;
 };
+// CTAs of a cache write or read of `tokens` tokens (at least one).
+int64_t cache_ctas(const CacheDims &c, int tokens);
 cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t stream);
 
 struct CacheReadArgs {

@@ -142,6 +142,7 @@ bsa_status bsa_cache_write(const bsa_cache_shape *shape, int32_t tokens, const v
   if (!cache_pointers_ok(a.c, k_codes, k_scales, v_codes, v_scales) || !status_ok(dev_status))
     return BSA_ERR_INVALID_ARG;
   if (tokens == 0) return BSA_OK;
+  if (bsa::cache_ctas(a.c, tokens) > INT32_MAX) return BSA_ERR_UNSUPPORTED;
   if (!good(k) || !good(v) || !good4(slots)) return BSA_ERR_INVALID_ARG;
   a.k = u16(k);
   a.v = u16(v);
@@ -168,8 +169,7 @@ bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t t
   if (batch < 1 || total_tokens < 1 || max_seqlen < 1 || table_stride < 1 || max_seqlen > total_tokens)
     return BSA_ERR_SHAPE;
   if ((static_cast<long long>(max_seqlen) + a.c.page - 1) / a.c.page > table_stride) return BSA_ERR_SHAPE;
-  // one thread per 16 values of K and of V, 256 to a CTA
-  if (static_cast<long long>(total_tokens) * a.c.hkv * (a.c.d / 16) / 256 >= INT32_MAX) return BSA_ERR_UNSUPPORTED;
+  if (bsa::cache_ctas(a.c, total_tokens) > INT32_MAX) return BSA_ERR_UNSUPPORTED;
   if (!cache_pointers_ok(a.c, k_codes, k_scales, v_codes, v_scales) || !good4(cu_seqlens) || !good4(block_table) ||
       !good(k_out) || !good(v_out) || !status_ok(dev_status))
     return BSA_ERR_INVALID_ARG;

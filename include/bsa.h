@@ -496,9 +496,11 @@ bsa_status bsa_qk_norm_rope(const bsa_rope_shape *shape, const void *q, int64_t 
  * Roundings are to nearest, ties to even.  Every other held value is a bf16 value
  * (E4M3 and E2M1 down to bf16's smallest normal times the code's own range).
  * Supported: head_dim in {64, 128}; page in {64, 128, 256}; pages * page and
- * pages * hkv < 2^31.  Code and scale arrays 16-byte aligned; scale pointers are ignored (may
- * be null) for BF16.  bsa_cache_code_bytes / bsa_cache_scale_bytes: bytes of
- * one codes and one scales array (0 for an invalid shape).
+ * pages * hkv < 2^31.  A call writes or reads at most 2^31 - 1 pieces of 1024 / d
+ * tokens of one head (BSA_ERR_UNSUPPORTED past that).  Code and scale arrays
+ * 16-byte aligned; scale pointers are ignored (may be null) for BF16.
+ * bsa_cache_code_bytes / bsa_cache_scale_bytes: bytes of one codes and one scales
+ * array (0 for an invalid shape).
  *
  * bsa_cache_write: token t's rows k[t], v[t] (bf16 [tokens, hkv, d], strides as
  * above) into slot slots[t] = page index * page + row; a negative slot leaves

@@ -160,3 +160,13 @@ def test_strides_past_the_limit(lib):
     for big in ((1 << 30) + 8, 1 << 40, (1 << 62)):
         assert rope(lib, stride_q=big) == INVALID and rope(lib, sko=big) == INVALID
         assert write(lib, cshape(), ks=big) == INVALID and write(lib, cshape(), vs=big) == INVALID
+
+
+def test_grids_past_the_limit(lib):
+    """A CTA is 64 threads: D / 16 of them to a row of one head.  Calls of more than 2^31 - 1 CTAs are refused."""
+    big = (1 << 31) - 1
+    for d, hkv, tokens in ((64, 16, big), (128, 8, big), (64, 4096, 1 << 24), (128, 4096, 1 << 22)):
+        s = cshape(head_dim=d, hkv=hkv, pages=10)
+        width = hkv * d
+        assert write(lib, s, tokens=tokens, ks=width, vs=width) == UNSUPPORTED, (d, hkv)
+        assert read(lib, s, total=tokens, most=30) == UNSUPPORTED, (d, hkv)
