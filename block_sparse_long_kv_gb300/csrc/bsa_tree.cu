@@ -124,60 +124,11 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two codes as f16, the low one in the low half (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-__device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 c, z;\n\tmov.b16 {c, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}"
-      : "=r"(r)
-      : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// 2^(e - 127); 0 for e <= 0.
-__device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(max(e, 0) << 23); }
-
 // The first of the two adjacent dimensions in word `which` of k-step ks of thread tq.
 template <int D, int FMT>
 __device__ __forceinline__ int frag_dim(int ks, int tq, int which) {
   if (FMT == BSA_CACHE_BF16 && D == 128) return (4 * (ks >> 1) + tq) * 8 + (ks & 1) * 4 + which * 2;
   return tq * (D / 4) + ks * 4 + which * 2;
-}
-
-struct Drafts {
-  int start, len;
-};
-__device__ __forceinline__ Drafts drafts_of(const TreeArgs &a, int b) {
-  const SeqSpan sp = seq_span(a.cu, b, a.max_draft, a.total, a.status);
-  return Drafts{sp.start, sp.len};
-}
-__device__ __forceinline__ int cached_of(const TreeArgs &a, int b) {
-  const int n = __ldg(a.cached + b);
-  if (n >= 0 && n <= a.max_cached) return n;
-  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-  return 0;
-}
-// The parent of drafted token i, checked.
-__device__ __forceinline__ int parent_of(const TreeArgs &a, int start, int i) {
-  if (a.parents == nullptr) return i - 1;
-  const int p = __ldg(a.parents + start + i);
-  if (p >= -1 && p < i) return p;
-  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-  return -1;
 }
 
 // Exclusive prefix sum over the CTA's threads in thread order; *total gets the sum.

@@ -1,4 +1,5 @@
-// Shared by the two drafted-token kernels: the records that their runs leave for the combine.
+// Shared by the two drafted-token kernels: the arguments they check, the f16 forms of the cache's codes, and the
+// records that their runs leave for the combine.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -6,7 +7,60 @@
 
 #include <atomic>
 
+#include "bsa_cache.h"
+#include "bsa_internal.h"
+
 namespace bsa {
+
+// 2^(e - 127); 0 for e <= 0.
+__device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(max(e, 0) << 23); }
+
+// Two codes as f16, the low one in the low half (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 c, z;\n\tmov.b16 {c, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}"
+      : "=r"(r)
+      : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A sequence's drafted tokens, its cached tokens and the parent of its drafted token i, checked: what is not as
+// documented sets *status and reads as none, none and a root.
+struct Drafts {
+  int start, len;
+};
+__device__ __forceinline__ Drafts drafts_of(const TreeArgs &a, int b) {
+  const SeqSpan sp = seq_span(a.cu, b, a.max_draft, a.total, a.status);
+  return Drafts{sp.start, sp.len};
+}
+__device__ __forceinline__ int cached_of(const TreeArgs &a, int b) {
+  const int n = __ldg(a.cached + b);
+  if (n >= 0 && n <= a.max_cached) return n;
+  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
+  return 0;
+}
+__device__ __forceinline__ int parent_of(const TreeArgs &a, int start, int i) {
+  if (a.parents == nullptr) return i - 1;
+  const int p = __ldg(a.parents + start + i);
+  if (p >= -1 && p < i) return p;
+  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
+  return -1;
+}
 
 // A kernel launched by launch_after may start before the one ahead of it in the stream has ended; it waits
 // here, before its first read, until that one has ended and its writes are visible.

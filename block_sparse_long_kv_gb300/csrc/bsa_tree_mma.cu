@@ -120,35 +120,10 @@ struct Cfg {
   static_assert(PER >= 0 && NCH >= 1 && B_FIN < 64, "");
 };
 
-// 2^(e - 127); 0 for e <= 0.
-__device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(max(e, 0) << 23); }
-
 // 2^k as f16 in both halves, 0 below the smallest subnormal; k <= 15.
 __device__ __forceinline__ uint32_t pow2_f16x2(int k) {
   const uint32_t h = k >= -14 ? static_cast<uint32_t>(k + 15) << 10 : k >= -24 ? 1u << (k + 24) : 0u;
   return h | h << 16;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-__device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 c, z;\n\tmov.b16 {c, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}"
-      : "=r"(r)
-      : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 __device__ __forceinline__ uint4 finite_bf16x8(const uint4 &v, uint32_t &lost) {
   return make_uint4(finite_bf16x2(v.x, lost), finite_bf16x2(v.y, lost), finite_bf16x2(v.z, lost), finite_bf16x2(v.w, lost));
@@ -242,27 +217,6 @@ __device__ __forceinline__ bool wait_parked(uint32_t bar, uint32_t parity, const
   }
 }
 
-struct Span {
-  int start, len;
-};
-__device__ __forceinline__ Span drafts_of(const TreeArgs &a, int b) {
-  const SeqSpan sp = seq_span(a.cu, b, a.max_draft, a.total, a.status);
-  return Span{sp.start, sp.len};
-}
-__device__ __forceinline__ int cached_of(const TreeArgs &a, int b) {
-  const int n = __ldg(a.cached + b);
-  if (n >= 0 && n <= a.max_cached) return n;
-  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-  return 0;
-}
-__device__ __forceinline__ int parent_of(const TreeArgs &a, int start, int i) {
-  if (a.parents == nullptr) return i - 1;
-  const int p = __ldg(a.parents + start + i);
-  if (p >= -1 && p < i) return p;
-  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-  return -1;
-}
-
 // Units of one row tile of group x, its row tiles, and the 64-key chunks of its kept pages.
 struct GroupPlan {
   int per, tiles, chunks;
@@ -272,7 +226,7 @@ __device__ __forceinline__ GroupPlan plan_of(const TreeArgs &a, int x) {
   const int b = x / a.c.hkv;
   const int listed = a.kv_cnt == nullptr ? 0 : __ldg(a.kv_cnt + x);  // (the loads in one round)
   const int n = cached_of(a, b);
-  const Span dr = drafts_of(a, b);
+  const Drafts dr = drafts_of(a, b);
   GroupPlan p;
   if (a.kv_cnt == nullptr) {
     p.chunks = (n + kChunk - 1) / kChunk;
@@ -406,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {  // the run's first row tile, for the combine
     if (x0 < x1) {
       const Segment s = segment_at<C::NTQ>(a, pre, groups, x0, x1);
-      const Span dr = drafts_of(a, s.grp / a.c.hkv);
+      const Drafts dr = drafts_of(a, s.grp / a.c.hkv);
       runs[cta] = TreeRun{s.grp, s.rt, s.rs, s.re, W, dr.start, dr.len, 0};
     } else {
       runs[cta].group = -1;
@@ -558,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // three rounds of memory: these three together, the list's entries, the table's
           const int listed = a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + lo);
           const int n = cached_of(a, b);
-          const Span dr = drafts_of(a, b);
+          const Drafts dr = drafts_of(a, b);
           const int pages = (n + a.c.page - 1) >> a.c.page_shift;
           const int cpp = a.c.page / kChunk, kept = max(0, min(listed, pages));
           const int chunks = a.kv_cnt == nullptr ? (n + kChunk - 1) / kChunk : kept * cpp;
@@ -925,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_q = [&](const Segment &s, uint32_t seg) {
       constexpr int LPR = D / 8, R = 32 / LPR, ROWS = PAIR ? 32 : 16;  // lanes of a row, rows of a step, of the warp
       constexpr int U = ROWS / R < 8 ? ROWS / R : 8;                   // steps in flight
-      const Span dr = drafts_of(a, s.grp / a.c.hkv);
+      const Drafts dr = drafts_of(a, s.grp / a.c.hkv);
       const int q = lane % LPR, first = PAIR ? t * kRows + sub * 32 : sub * 32 + t * 16, g = s.grp % a.c.hkv;
 #pragma unroll 1
       for (int r = first; r < first + ROWS; r += R * U) {
@@ -971,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = x0; ok && x < x1; ++n_seg) {
       if (n_seg > 0) s = segment_at<C::NTQ>(a, pre, groups, x, x1);
       x += s.units;
-      const Span dr = drafts_of(a, s.grp / a.c.hkv);
+      const Drafts dr = drafts_of(a, s.grp / a.c.hkv);
       const int row = (s.rt * C::NTQ + (PAIR ? t : 0)) * kRows + r, tok = row / G;
       const bool live = tok < dr.len;
       float rs = a.scale_log2;
