@@ -66,7 +66,7 @@ bsa_status check_tree(const bsa_tree_shape *s, const bsa::CacheDims &c, int *gro
   if (g != 1 && g != 2 && g != 4 && g != 8 && g != 16) return BSA_ERR_UNSUPPORTED;
   if (s->max_draft > 256 || pages > bsa::kMaxBlocks) return BSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(s->batch) * c.hkv > bsa::kMaxDecodeRows) return BSA_ERR_UNSUPPORTED;
-  // units of 64 keys over all tiles of 16 rows are counted in 32 bits
+  // the units of a plan are counted in 32 bits: at most these, of 64 keys and 16 rows
   const long long tiles = (static_cast<long long>(s->max_draft) * g + 15) / 16;
   const long long units = static_cast<long long>(pages) * (c.page / 64) + 4;
   if (tiles * units * s->batch * c.hkv > INT32_MAX) return BSA_ERR_UNSUPPORTED;

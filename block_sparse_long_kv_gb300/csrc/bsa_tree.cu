@@ -1,11 +1,12 @@
 // Attention of drafted tokens over the paged cache, split over the keys.
 //
 // Rows.  The drafted tokens of a sequence times the G heads of a KV group are
-// query rows that share every key: row r is token r / G, head r % G.  Sixteen
-// rows are one tile, the M of one m16n8k16 MMA.  The keys of a tile are laid
-// out in units of 64: the 64-key chunks of the kept pages, then the drafted
-// tokens.  The units of all tiles are laid end to end and cut into equal runs,
-// one per CTA, so that a short batch and a ragged one load every SM alike.
+// query rows that share every key: row r is token r / G, head r % G.  There are
+// at most sixteen, one tile, the M of one m16n8k16 MMA.  A group's keys are laid
+// out in units of 64: the 64-key chunks of the kept pages, then the (at most
+// sixteen) drafted tokens.  The units of all groups are laid end to end and cut
+// into equal runs, one per CTA, so that a short batch and a ragged one load every
+// SM alike.
 //
 // One CTA streams its run through a cp.async ring; each of its four warps owns
 // 16 keys of a chunk and keeps its own online softmax.  With few rows the
@@ -35,7 +36,7 @@
 // plan, the first chunk and the combine), e4m3 46, e2m1 43 (bound by the integer pipe that turns codes into
 // fragments: half of the issue slots, 44 % of the pipe's peak).
 //
-// Tiles that one CTA holds whole are written by it; of the others every CTA
+// Groups that one CTA holds whole are written by it; of the others every CTA
 // leaves an unnormalised part (O, max, sum), which tree_combine_kernel merges in
 // a fixed order, so the result does not depend on timing.
 
@@ -79,11 +80,10 @@ struct Cfg {
   static constexpr int LDO = D + 8;   // row of the merge buffer, in floats (the pad spreads the rows over the banks)
   static constexpr int OFF_O = STAGES * STAGE;
   static constexpr int OFF_ML = OFF_O + kRows * LDO * 4;            // [2][warps][16] floats
-  static constexpr int OFF_E = OFF_ML + 2 * kWarps * kRows * 4;     // [warps] O's unit exponent
-  static constexpr int OFF_MASK = OFF_E + 16;                       // [16] 64-bit masks of a drafted chunk
-  static constexpr int OFF_UNIT = OFF_MASK + kRows * 8;             // [2][kBatch] int4
-  static constexpr int OFF_PRE = OFF_UNIT + 2 * kBatch * 16;        // [groups + 1] first unit, [groups] units per tile
-  static size_t smem(int groups) { return OFF_PRE + static_cast<size_t>(2 * groups + 1) * 4; }
+  static constexpr int OFF_MASK = OFF_ML + 2 * kWarps * kRows * 4;  // [16] the drafted tokens that a row sees
+  static constexpr int OFF_UNIT = OFF_MASK + kRows * 4;             // [2][kBatch] int4
+  static constexpr int OFF_PRE = OFF_UNIT + 2 * kBatch * 16;        // [groups + 1] first unit
+  static size_t smem(int groups) { return OFF_PRE + static_cast<size_t>(groups + 1) * 4; }
 };
 
 // 16-byte chunk permutations of the staged rows (an XOR of the chunk index), such that the eight
@@ -153,8 +153,8 @@ __device__ __forceinline__ int cta_scan(int c, int *total, int *wsum) {
   return off + inc - c;
 }
 
-// A unit: .x the group (b * hkv + g), .y the row tile, .z the cache tile (page * hkv + g; -1: drafted
-// tokens), .w keys in the low half and first key (chunk of the page, or of the drafts) in units of 64 in the high half.
+// A unit: .x the group (b * hkv + g), .y the cache tile (page * hkv + g; -1: drafted tokens, or nothing), .z its
+// keys, .w its 64-key chunk of the page.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(const TreeArgs a, float *part_o, float *part_ml,
                                                                         TreeRun *runs) {
@@ -164,14 +164,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   float *obuf = reinterpret_cast<float *>(smem + C::OFF_O);
   float(*wm)[kRows] = reinterpret_cast<float(*)[kRows]>(smem + C::OFF_ML);
   float(*wl)[kRows] = wm + kWarps;
-  int *we = reinterpret_cast<int *>(smem + C::OFF_E);
-  unsigned long long *dmask = reinterpret_cast<unsigned long long *>(smem + C::OFF_MASK);
+  uint32_t *dmask = reinterpret_cast<uint32_t *>(smem + C::OFF_MASK);
   int4 *unit = reinterpret_cast<int4 *>(smem + C::OFF_UNIT);
   int *pre = reinterpret_cast<int *>(smem + C::OFF_PRE);
   const int groups = a.batch * a.c.hkv;
-  int *per = pre + groups + 1;
   __shared__ int wsum[kWarps];
-  __shared__ int not_finite_flag;  // drafted values of the tile held Inf or NaN
+  __shared__ int not_finite_flag;  // drafted values of the group held Inf or NaN
   volatile int *not_finite_v = &not_finite_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -179,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   const int cta = blockIdx.x, G = a.group;
   const int cpp = a.c.page / kKeys;
 
-  // ---- the plan: units per tile and first unit of every group
+  // ---- the plan: first unit of every group
   {
     const int each = (groups + kThreads - 1) / kThreads;
     const int g0 = min(groups, tid * each), g1 = min(groups, g0 + each);
@@ -193,8 +191,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       const int kept = max(0, min(listed, pages));
       // without a list the chunks past the last token are not units at all
       const int ku = a.kv_cnt == nullptr ? (n + kKeys - 1) / kKeys : kept * cpp;
-      per[x] = ku + (dr.len + kKeys - 1) / kKeys;
-      pre[x] = dr.len > 0 ? per[x] * ((dr.len * G + kRows - 1) / kRows) : 0;
+      pre[x] = dr.len > 0 ? ku + 1 : 0;
       local += pre[x];
     }
     int n;
@@ -229,23 +226,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       if (pre[mid] <= x) lo = mid;
       else hi = mid - 1;
     }
-    const int local = x - pre[lo], b = lo / a.c.hkv;
+    const int b = lo / a.c.hkv, k = x - pre[lo];
     const int n = cached_of(a, b);
-    const Drafts dr = drafts_of(a, b);
-    const int rt = local / per[lo], k = local - rt * per[lo];
-    const int ku = per[lo] - (dr.len + kKeys - 1) / kKeys;
-    int4 d = make_int4(lo, rt, -1, 0);
-    if (k >= ku) {
-      const int c = k - ku;
-      d.w = min(kKeys, dr.len - c * kKeys) | c << 16;
+    int4 d = make_int4(lo, -1, 0, 0);
+    if (k == pre[lo + 1] - pre[lo] - 1) {
+      d.z = drafts_of(a, b).len;
     } else {
       const int e = k >> (a.c.page_shift - 6), sub = k & (cpp - 1);
       const int j = a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
       if (j >= 0 && j < (n + a.c.page - 1) >> a.c.page_shift) {
         const int pg = __ldg(a.table + static_cast<size_t>(b) * a.table_stride + j);
         if (pg >= 0 && pg < a.c.pages) {
-          d.z = pg * a.c.hkv + (lo - b * a.c.hkv);
-          d.w = max(0, min(kKeys, n - j * a.c.page - sub * kKeys)) | sub << 16;
+          d.y = pg * a.c.hkv + (lo - b * a.c.hkv);
+          d.z = max(0, min(kKeys, n - j * a.c.page - sub * kKeys));
+          d.w = sub;
         } else if (a.status != nullptr) {
           atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
         }
@@ -265,11 +259,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   auto issue = [&](int u) {
     if (u < nu) {
       const int4 d = unit[u % (2 * kBatch)];
-      const int n = d.w & 0xFFFF;
-      if (d.z >= 0 && n > 0) {
+      const int n = d.z;
+      if (d.y >= 0 && n > 0) {
         const uint32_t st = static_cast<uint32_t>(u % C::STAGES) * C::STAGE;
-        const int sub = d.w >> 16;
-        const size_t at = (static_cast<size_t>(d.z) * a.c.page + sub * kKeys) * C::RB + tid * 16;
+        const int sub = d.w;
+        const size_t at = (static_cast<size_t>(d.y) * a.c.page + sub * kKeys) * C::RB + tid * 16;
         const uint8_t *ks = a.k_codes + at, *vs = a.v_codes + at;
         if (n == kKeys) {
 #pragma unroll
@@ -287,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
         }
         if constexpr (C::PER > 0) {
           // the exponents of the chunk's 64 rows, then their group scales
-          const size_t sc = static_cast<size_t>(d.z) * a.c.page * C::PER;
+          const size_t sc = static_cast<size_t>(d.y) * a.c.page * C::PER;
           constexpr int PS = kKeys * C::PER / 16;
           if (tid < PS) {
             const size_t from = tid < kKeys / 16 ? sc + sub * kKeys + tid * 16
@@ -308,20 +302,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
   float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
   float sc_lo = a.scale_log2, sc_hi = a.scale_log2;  // logit scales of the rows gq and gq + 8
   int eref = 0;  // O is in units of 2^(eref - UNIT1); 0: nothing yet
-  int arow_g = -1, arow_t = -1;
+  int arow_g = -1;
   Drafts adr{0, 0};
 
-  // the row's first element of q, k or v style rows; null past the drafts
+  // row r of q; null past the drafts
   auto q_row = [&](int r) -> const uint16_t * {
-    const int row = arow_t * kRows + r, t = row / G;
+    const int t = r / G;
     if (t >= adr.len) return nullptr;
     const int g = arow_g % a.c.hkv;
-    return a.q + (static_cast<size_t>(adr.start + t) * a.hq + g * G + row % G) * D;
+    return a.q + (static_cast<size_t>(adr.start + t) * a.hq + g * G + r % G) * D;
   };
 
-  auto start_tile = [&](int grp, int rt) {
+  auto start_group = [&](int grp) {
     arow_g = grp;
-    arow_t = rt;
     adr = drafts_of(a, grp / a.c.hkv);
     const uint16_t *qlo = q_row(gq), *qhi = q_row(gq + 8);
     float am_lo = 0.f, am_hi = 0.f;
@@ -367,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     eref = 0;
   };
 
-  // Merges the four warps' O, max and sum of the tile, and writes the rows or the part.
+  // Merges the four warps' O, max and sum of the group, and writes the rows or the part.
   auto flush = [&]() {
 #pragma unroll
     for (int off = 1; off <= 2; off <<= 1) {
@@ -411,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       }
       __syncthreads();
     }
-    const int rs = pre[arow_g] + arow_t * per[arow_g], re = rs + per[arow_g];
+    const int rs = pre[arow_g], re = pre[arow_g + 1];
     const bool whole = rs >= x0 && re <= x1;
     const size_t slot = 2 * static_cast<size_t>(cta) + (rs <= x0 ? 0 : 1);
     const bool lost = *not_finite_v != 0;
@@ -419,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 #pragma unroll 1
     for (int e = tid; e < kRows * PIECES; e += kThreads) {
       const int r = e / PIECES, d4 = 4 * (e % PIECES);
-      const int row = arow_t * kRows + r, t = row / G;
+      const int t = r / G;
       if (t >= adr.len) continue;
       float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -441,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       }
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
-        const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + row % G;
+        const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + r % G;
         *reinterpret_cast<uint2 *>(a.o + at * D + d4) =
             make_uint2(ptx::pack_bf16x2(v.x * inv, v.y * inv), ptx::pack_bf16x2(v.z * inv, v.w * inv));
         if (a.lse != nullptr && d4 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
@@ -677,26 +670,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     }
   };
 
-  // A chunk of at most 64 drafted tokens: bf16 straight from global memory (once per tile).
-  auto drafted_chunk = [&](int chunk, int n) {
-    if (tid < kRows) {
-      const int t = (arow_t * kRows + tid) / G;
-      unsigned long long bits = 0ull;
-      if (t < adr.len)
-        for (int p = t; p >= 0; p = parent_of(a, adr.start, p))
-          if (p >> 6 == chunk) bits |= 1ull << (p & 63);
-      dmask[tid] = bits;
-    }
-    __syncthreads();
-    const int k0 = warp * 16;
-    if (k0 < n) {
+  // The n <= 16 drafted tokens: bf16 straight from global memory, by the first warp.
+  auto drafted_chunk = [&](int n) {
+    if (warp == 0) {
+      if (lane < kRows) {
+        const int t = lane / G;
+        uint32_t bits = 0u;
+        if (t < adr.len)
+          for (int p = t; p >= 0; p = parent_of(a, adr.start, p)) bits |= 1u << p;
+        dmask[lane] = bits;
+      }
+      __syncwarp();
       const int g = arow_g % a.c.hkv;
-      const size_t first = static_cast<size_t>(adr.start) + chunk * kKeys;
       auto row_of = [&](const uint16_t *base, int key) -> const uint16_t * {
-        return key < n ? base + ((first + key) * a.c.hkv + g) * D : nullptr;
+        return key < n ? base + (static_cast<size_t>(adr.start + key) * a.c.hkv + g) * D : nullptr;
       };
       const uint16_t *qlo = q_row(gq), *qhi = q_row(gq + 8);
-      const uint16_t *kr[2] = {row_of(a.k_new, k0 + gq), row_of(a.k_new, k0 + 8 + gq)};
+      const uint16_t *kr[2] = {row_of(a.k_new, gq), row_of(a.k_new, 8 + gq)};
       auto word = [](const uint16_t *row, int dim) -> uint32_t {
         return row != nullptr ? *reinterpret_cast<const uint32_t *>(row + dim) : 0u;
       };
@@ -710,13 +700,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
         mma<true>(s[0], qf, word(kr[0], da), word(kr[0], db));
         mma<true>(s[1], qf, word(kr[1], da), word(kr[1], db));
       }
-      const unsigned long long b_lo = dmask[gq] >> k0, b_hi = dmask[gq + 8] >> k0;
+      const uint32_t b_lo = dmask[gq], b_hi = dmask[gq + 8];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = nt * 8 + 2 * tq + (e & 1);
-          s[nt][e] = ((e < 2 ? b_lo : b_hi) >> key) & 1ull ? s[nt][e] * a.scale_log2 : -INFINITY;
+          s[nt][e] = ((e < 2 ? b_lo : b_hi) >> key) & 1u ? s[nt][e] * a.scale_log2 : -INFINITY;
         }
       float fo = 1.f;
       if constexpr (Q16) {  // O to units of 1
@@ -728,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
                               ptx::pack_bf16x2(s[1][0], s[1][1]), ptx::pack_bf16x2(s[1][2], s[1][3])};
       const uint16_t *vr[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) vr[x] = row_of(a.v_new, k0 + 2 * tq + (x & 1) + 8 * (x >> 1));
+      for (int x = 0; x < 4; ++x) vr[x] = row_of(a.v_new, 2 * tq + (x & 1) + 8 * (x >> 1));
       uint32_t lost = 0u;  // not 0: Inf or NaN among the values
 #pragma unroll
       for (int w = 0; w < C::NNT / 2; ++w) {
@@ -739,44 +729,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
         mma<true>(o[2 * w], pa, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
         mma<true>(o[2 * w + 1], pa, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
       }
-      if (__any_sync(0xffffffffu, lost != 0u)) {
-        if (lane == 0) *not_finite_v = 1;
-      }
+      if (__any_sync(0xffffffffu, lost != 0u) && lane == 0) *not_finite_v = 1;  // (flush reads it behind a barrier)
     }
-    __syncthreads();  // dmask is free again
   };
 
   resolve(0);
   __syncthreads();
-  if (tid == 0) {  // the run's first tile, for the combine
-    const int4 d = unit[0];
-    const int rs = pre[d.x] + d.y * per[d.x];
-    const Drafts dr = drafts_of(a, d.x / a.c.hkv);
-    runs[cta] = TreeRun{d.x, d.y, rs, rs + per[d.x], W, dr.start, dr.len, 0};
+  if (tid == 0) {  // the run's first group, for the combine
+    const int grp = unit[0].x;
+    const Drafts dr = drafts_of(a, grp / a.c.hkv);
+    runs[cta] = TreeRun{grp, 0, pre[grp], pre[grp + 1], W, dr.start, dr.len, 0};
   }
 #pragma unroll
   for (int x = 0; x < C::STAGES - 1; ++x) issue(x);
   for (int u = 0; u < nu; ++u) {
     if ((u + C::STAGES - 1) % kBatch == 0) resolve(u + C::STAGES - 1);  // its buffer's units are all behind u
     const int4 d = unit[u % (2 * kBatch)];
-    if (d.x != arow_g || d.y != arow_t) {  // (Q's loads beside the unit's)
+    if (d.x != arow_g) {  // (Q's loads beside the unit's)
       if (arow_g >= 0) flush();
-      start_tile(d.x, d.y);
+      start_group(d.x);
     }
     cp_wait<C::STAGES - 2>();  // unit u has landed
     __syncthreads();           // for every thread; and unit u - 1's stage and a resolved batch are free to use
     issue(u + C::STAGES - 1);
-    const int n = d.w & 0xFFFF;
-    if (n > 0) {
-      if (d.z >= 0) cached_chunk(smem + (u % C::STAGES) * C::STAGE, n);
-      else drafted_chunk(d.w >> 16, n);
+    if (d.z > 0) {
+      if (d.y >= 0) cached_chunk(smem + (u % C::STAGES) * C::STAGE, d.z);
+      else drafted_chunk(d.z);
     }
   }
   cp_wait<0>();  // only empty groups can remain
   flush();
 }
 
-// The row tiles that several CTAs share.  CTA x takes the x-th of them in the order of their first CTA: it
+// The groups that several CTAs share.  CTA x takes the x-th of them in the order of their first CTA: it
 // begins in the run of CTA c - 1 and goes on in CTA c's, which has recorded it.  Row r:
 // O = sum w_p O_p / sum w_p l_p over its parts p = c - 1 .., w_p = 2^(m_p - max m).  Warp w sums the parts
 // w, w + 8, .. against its own maximum, and the eight sums are added in order.
@@ -795,11 +780,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   TreeRun run;
   const int c = shared_tile(runs, ctas, blockIdx.x, &run);
   if (c < 0) return;
-  const int row = run.tile * kRows + r, t = row / a.group;
+  const int t = r / a.group;
   if (t >= run.drafts) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int p0 = c - 1, np = (run.last - 1) / run.run - p0 + 1;
-  // every part after the first begins its CTA's run; the first may be that CTA's last tile
+  // every part after the first begins its CTA's run; the first may be that CTA's last group
   auto at = [&](int p) {
     return (2 * static_cast<size_t>(p0 + p) + (p > 0 || run.first == p0 * run.run ? 0 : 1)) * kRows + r;
   };
@@ -851,7 +836,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   for (int w = 0; w < kCombineWarps; ++w) mm = ptx::max_nan(mm, red_m[w]);
 #pragma unroll
   for (int w = 0; w < kCombineWarps; ++w) fw[w] = red_m[w] == -INFINITY ? 0.f : exp2f(red_m[w] - mm);
-  const size_t out = static_cast<size_t>(run.draft0 + t) * a.hq + (run.group % a.c.hkv) * a.group + row % a.group;
+  const size_t out = static_cast<size_t>(run.draft0 + t) * a.hq + (run.group % a.c.hkv) * a.group + r % a.group;
   for (int d = threadIdx.x; d < D; d += kCombineWarps * 32) {
     float s = 0.f, ls = 0.f;
 #pragma unroll
@@ -893,10 +878,9 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, runs);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int ctas = kSms * C::CTAS, rows = a.max_draft * a.group < kRows ? a.max_draft * a.group : kRows;
-  const long long tiles = static_cast<long long>(a.batch) * a.c.hkv * ((a.max_draft * a.group + kRows - 1) / kRows);
-  const int shared = static_cast<int>(tiles < ctas - 1 ? tiles : ctas - 1);  // at most: a run boundary each
-  return launch_after(tree_combine_kernel<D>, dim3(shared, rows), kCombineWarps * 32, stream, a,
+  const int ctas = kSms * C::CTAS, groups = a.batch * a.c.hkv;
+  const int shared = groups < ctas - 1 ? groups : ctas - 1;  // at most: a run boundary each
+  return launch_after(tree_combine_kernel<D>, dim3(shared, a.max_draft * a.group), kCombineWarps * 32, stream, a,
                       static_cast<const float *>(part_o), static_cast<const float *>(part_ml),
                       static_cast<const TreeRun *>(runs), ctas);
 }
