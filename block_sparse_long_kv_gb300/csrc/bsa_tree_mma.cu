@@ -302,9 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int x = 0; x < C::NBARS; ++x) {
-      // arrivals: 1 of a commit or the lookup warp, 4 of the K or the V loaders' warps or a softmax lane, 8 of both lanes
+      // arrivals: 1 of a commit or the lookup warp, 2 of a commit and the thread that issues it (what it has seen is
+      // then seen behind the barrier), 4 of the K or the V loaders' warps or a softmax lane, 8 of both lanes
       uint32_t count = 1;
-      if (x >= C::B_RS && x < C::B_LK)
+      if (x >= C::B_OD && x < C::B_OE)
+        count = 2;
+      else if (x >= C::B_RS && x < C::B_LK)
         count = 8;
       else if (x < C::B_QE || (x >= C::B_KF && x < C::B_KE) || (x >= C::B_VF && x < C::B_VE) ||
                (x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_UN) || (x >= C::B_UG && x < C::B_FIN))
@@ -422,6 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pv_count[t];
         return true;
       };
+      auto done_with = [&](int t) {  // lane t's O of the segment
+        ptx::mma_commit(bar(C::B_OD + t));
+        ptx::mbar_arrive(bar(C::B_OD + t));
+      };
       bool ok = true;
       bool k_there = false;  // K of the next unit was seen to be there
       uint32_t n = 0, n_seg = 0;
@@ -461,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == 0 && !(ok = o_free(0))) break;
             if (!(ok = issue_pv(0, vs, i > 0, static_cast<int>(n)))) break;
             if (last) {
-              ptx::mma_commit(bar(C::B_OD));
+              done_with(0);
               if (i == 0 && !(ok = o_free(1))) break;
               if (!(ok = issue_pv(1, vs, i > 0, -1))) break;
               ptx::mma_commit(bar(C::B_VE + vs));
-              ptx::mma_commit(bar(C::B_OD + 1));
+              done_with(1);
             }
           } else {
             issue_s(i & 1, ks);
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j == t && !(ok = o_free(t))) break;
               if (!(ok = issue_pv(t, pvs, j >= 2, static_cast<int>(nj)))) break;
               ptx::mma_commit(bar(C::B_VE + pvs));
-              if (j + 2 >= s.units) ptx::mma_commit(bar(C::B_OD + t));
+              if (j + 2 >= s.units) done_with(t);
             }
             if (!ok) break;
           }
@@ -801,8 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n + 1 < nu) fetch_scales(n + 1);
       }
-      // (what a V loader has to say of drafted rows it knows when it has written them)
-      if (kv == 0 || !d0.z) arrive_warp((kv == 0 ? C::B_IK : C::B_IV) + n % kInfo);
+      arrive_warp((kv == 0 ? C::B_IK : C::B_IV) + n % kInfo);
 
       // ---- wait for the stage and fill it
       if (st + 1 == stages || st < 0) st = 0, ++round;
@@ -834,9 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t lost = store_rows(tile, 0, drafted, dstride, n0, f, kv == 1);
         lost |= store_rows(tile, 1, drafted + kChunk * dstride, dstride, n1, f, kv == 1);
         if (kv == 1) {
+          // read behind B_OD, whose issuing thread has waited for this stage of V
           const bool any = __any_sync(0xffffffffu, lost != 0u);
           if (lane == 0) reinterpret_cast<uint8_t *>(lost_v + n % kInfo)[lw & 3] = any;
-          arrive_warp(C::B_IV + n % kInfo);
         }
         for (int gr = 0; Q16 && gr < NG; ++gr) {  // the unit's empty groups
           copy_group(slot);
