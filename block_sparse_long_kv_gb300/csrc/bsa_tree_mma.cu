@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int PR = D / 8;
       float am = 0.f;
       uint32_t lost = 0u;
-#pragma unroll 4
+#pragma unroll 2
       for (int x = lt; x < n * PR; x += 128)
         am = fmaxf(am, amax8(finite_bf16x8(__ldg(reinterpret_cast<const uint4 *>(from + (x / PR) * stride + (x % PR) * 8)), lost)));
 #pragma unroll
