@@ -18,8 +18,8 @@
 //
 // 131072 tokens x 36 heads of 128 out of the rows of a fused projection: 386 us, 6.3 TB/s.  The arithmetic is done on
 // pairs of fp32 values: with single ones the instructions, not the loads, set the time (396 us).
-// Six steps in flight on 24 warps per SM: four on 32 warps spill (399), four on 24 do not
-// cover the loads (416), eight on 16 leave too few warps (451).  Heads of a token spread
+// Six steps in flight on 24 warps per SM (4 to 12 bytes spill in the norm's forms): four on 32 warps spill more
+// (399), four on 24 do not cover the loads (416), eight on 16 leave too few warps (451).  Heads of a token spread
 // over two warps repeat the angles: 431.
 
 #include <cuda_bf16.h>
@@ -45,7 +45,8 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 
 // f / 2 pi modulo one turn, in units of 2^-64 turns: f = m * 2^e with an integer m of 24 bits, times
 // 2^64 / 2 pi as an integer of 62 bits, shifted.  Integer arithmetic: the double-precision pipe of this part
-// is slow enough to show in a step.  For |f| < 2^16 the result is within |f| units.
+// is slow enough to show in a step.  For |f| < 2^16 the result is within 1 + |f| units (the shift drops up to one,
+// the 62-bit constant is half a unit off), which the largest position takes to 2^-33 (1 + |f|) turns.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
   constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
   const uint32_t u = __float_as_uint(f);

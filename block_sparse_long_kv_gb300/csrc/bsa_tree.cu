@@ -29,12 +29,15 @@
 // P of an 8- or 4-bit cache is P' = p * 2^(e - eref + SHIFT) in f16, e the exponent
 // of the key's V row and eref the largest seen, O held in units of 2^(eref - SHIFT):
 // SHIFT = 15 - TH keeps P' within f16 and leaves 25 powers of two below the largest
-// product at f16's full 2^-11, 10 more with fewer bits.  P of a bf16 cache is bf16, 2^-8
-// relative at any size.  Sums and statistics are fp32 from unrounded p.
+// product at f16's full 2^-11, 10 more with fewer bits.  (The lag TH costs four of
+// those; without it O is rescaled in most steps.)  P of a bf16 cache and of the drafted
+// tokens is bf16, 2^-8 relative at any size: one token over 131072 is 0.0023 off in
+// relative norm where fp32 weights would leave 0.0016, the rounding of the result.
+// Sums and statistics are fp32 from unrounded p.
 //
-// One token over 131072 cached, 32 / 4 heads of 128: bf16 60 us (269 MB: 4.5 TB/s; about 18 us of it are the
-// plan, the first chunk and the combine), e4m3 46, e2m1 43 (bound by the integer pipe that turns codes into
-// fragments: half of the issue slots, 44 % of the pipe's peak).
+// One token over 131072 cached, 32 / 4 heads of 128: bf16 55 us (269 MB: 4.9 TB/s; about 15 us of it are the
+// plan, the first chunk and the combine), e4m3 43, e2m1 44.  Over codes no unit is saturated: half of the issue
+// slots and 44 % of the integer pipe are taken, at three warps a scheduler, which do not cover the latencies.
 //
 // Groups that one CTA holds whole are written by it; of the others every CTA
 // leaves an unnormalised part (O, max, sum), which tree_combine_kernel merges in
@@ -892,9 +895,9 @@ size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft
 }
 
 bsa_status launch_tree(const TreeArgs &a, void *workspace, cudaStream_t stream) {
-  // More rows than one tile would read the cache once for each here.  8 x 32768 cached tokens, 32 / 4 heads of 128:
-  // 16 rows take 85 us (bf16) and 61 (e4m3) here, so 32 about twice that; 88 and 115 on tcgen05.  (Single short
-  // sequences with 32 rows would be 2 to 4 us faster here: 15.5 against 17.4 over 2048 tokens.)
+  // More rows than one tile would read the cache once for each here.  8 x 32768 cached tokens, 32 / 4 heads of 128,
+  // bf16 / e4m3 / e2m1: 16 rows take 78 / 57 / 60 us here, so 32 would take about twice that; 87 / 109 / 103 on
+  // tcgen05.  (A form with several row tiles took 15.5 us for 32 rows over one sequence of 2048, tcgen05 15 to 17.)
   if (a.max_draft * a.group > kRows) return launch_tree_mma(a, workspace, stream);
   cudaError_t e;
   const bool wide = a.c.d == 128;

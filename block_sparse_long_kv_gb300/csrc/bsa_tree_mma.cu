@@ -24,21 +24,25 @@
 //
 // An 8- or 4-bit cache is computed in f16.  With e the exponent of a key's row and
 // kref the largest of the unit, K' = code * 2^(e - kref + SHV) is exact down to
-// rows 2^-20 below the largest, and 2^(kref - 127 - SHV) joins the logit scale; V
-// likewise against oref, the largest exponent of the segment so far, O being held
+// e = kref - 21 (E4M3) or kref - 18 (E2M1, whose least value is half of 2^-9), and below
+// that off by at most 2^-36 of the largest row's largest element (group scale and
+// product are each half of 2^-24 off, in units of 2^-SHV); 2^(kref - 127 - SHV) joins the
+// logit scale.  V likewise against oref, the largest exponent of the segment so far
+// (drafted rows count too, and are held against it), O being held
 // in units of 2^(oref - 127 - SHV - SHIFT).  Q rows become f16 after a power of
 // two that brings their largest element to [2^14, 2^15), drafted K and V after one
 // per unit.  P' = 2^(x - m + SHIFT) with the reference m at most 2^TH below the true
 // maximum, so P' <= 2^15.  Row sums are fp32 from unrounded values.
 //
 // What bounds it: with two row tiles a unit is 32 MMAs of 64 cycles, 2048 cycles.  8 sequences of up to
-// 32768 cached tokens, 64 drafted tokens, 32 / 4 heads of 128 (84 units a CTA): bf16 205 us, e4m3 249, e2m1
-// 270 (0.94, 0.78 and 0.72 PFLOP/s; the MMAs alone 109).  From its logits to the last of P a lane takes 2400
+// 32768 cached tokens, 64 drafted tokens, 32 / 4 heads of 128 (84 units a CTA): bf16 207 us, e4m3 243, e2m1
+// 256 (0.93, 0.80 and 0.76 PFLOP/s; the MMAs alone 109).  From its logits to the last of P a lane takes 2400
 // cycles, of which the other lane's products cover two thirds; keys are hardly ever waited for.  The lanes have a
 // thousand instructions a unit and share the schedulers with the conversion, and the instruction cache shows: a
 // warp waits for its code as long as it issues.  So code is kept short: logits are taken in two halves (the
 // second is read from TMEM again), which also frees the registers for eight loader warps instead of four (e2m1
-// 327 -> 268).  The issuing thread looks at both halves of P, V and the next K before its products: a look between
+// 327 -> 268); and the loaders' handling of drafted rows, which is rare, keeps few loads in flight, or the codec beside
+// it spills (e4m3 243 -> 278).  The issuing thread looks at both halves of P, V and the next K before its products: a look between
 // them left the tensor core idle (e4m3 with P in quarters 256).
 // Measured and not kept: two threads a row (297), the conversion or the halves unrolled (355, 260), all 128 logits
 // in registers with four loader warps (bf16 190, e4m3 250, e2m1 293), running pointers in the loaders (257),
@@ -716,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // bf16 rows by hand: `n` keys of chunk h, from `from` (row stride in elements); zeros past n, and with `clean`
-    // in place of Inf and NaN.  Not 0 if there were any.  (Four pieces in flight: eight leave the codec spilling,
-    // 249 against 241 us for 64 drafts over e4m3.)
+    // in place of Inf and NaN.  Not 0 if there were any.  (Four pieces in flight: eight leave the codec
+    // spilling, 278 against 243 us for 64 drafts over e4m3.)
     auto store_rows = [&](uint32_t dst, int h, const uint16_t *from, size_t stride, int n, float f, bool clean) -> uint32_t {
       uint32_t lost = 0u;
       constexpr int PR = D / 8, TOTAL = kChunk * PR / 128, U = 4;

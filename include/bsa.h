@@ -451,7 +451,10 @@ bsa_status bsa_decode_step(const bsa_varlen_shape *shape, const bsa_select_param
  * overlaps of an output with an input or the other output are refused
  * (BSA_ERR_INVALID_ARG).  Supported: head_dim in {64, 128}; rotary_dim a
  * multiple of 16 in [0, head_dim] (with 0, inv_freq may be null and positions
- * only say which tokens count); tokens >= 0 (0 launches nothing).  inv_freq:
+ * only say which tokens count); hq and hkv at most 65536; tokens >= 0 (0 launches
+ * nothing).  Squares are fp32 too: a row with elements past 2^60 in size may come
+ * out as zeros or NaN, and with eps = 0 one whose elements are all below 2^-60 as
+ * Inf or NaN.  inv_freq:
  * fp32 [rotary_dim / 2], below 2^16 in size.  positions: int32 [tokens].  eps finite, >= 0.
  * q, k, outputs, weights 16-byte aligned; positions, inv_freq 4-byte aligned.
  * ------------------------------------------------------------------------ */
@@ -513,7 +516,7 @@ bsa_status bsa_qk_norm_rope(const bsa_rope_shape *shape, const void *q, int64_t 
  * of its tokens j * page ..), as bf16 values into the packed k_out, v_out
  * [total_tokens, hkv, d] at rows cu_seqlens[b] ..; what the varlen entry points
  * take.  cu_seqlens is checked as in a packed batch (at most max_seqlen tokens
- * a sequence, which table_stride must cover); a table entry outside the cache
+ * a sequence, which table_stride must cover, max_seqlen <= total_tokens); a table entry outside the cache
  * sets BSA_ERR_INVALID_ARG in *dev_status and leaves its rows, like those past
  * the last sequence, as they were.
  * ------------------------------------------------------------------------ */
@@ -553,18 +556,25 @@ bsa_status bsa_cache_read(const bsa_cache_shape *shape, int32_t batch, int32_t t
  *   - itself and its ancestors among the drafts:
  *   O[t][h] = sum_s softmax_s(scale * q . k_s) v_s;  lse[t][h] (fp32
  *   [total_draft, hq], nullable) the natural log of the normaliser.
- * The dot products use the held values exactly; softmax statistics and sums
- * are fp32.  One drafted token is a decode step.  Rows past cu_draft[batch] are
- * left as they were.  Inf and NaN in q, k_new or v_new go where the formula takes
- * them: into the rows that attend to them (of v_new into those dimensions of
- * theirs), and into no other row.  With an 8- or 4-bit cache and more
- * than 16 rows (drafted tokens x G) a sequence, the drafted keys (values) of one
- * KV head are held in f16 under one power of two per 128 drafted tokens: elements
- * 2^28 below the largest of them lose bits.
+ * Softmax statistics and sums are fp32.  One drafted token is a decode step.
+ * Rows past cu_draft[batch] are left as they were.  Inf and NaN in q, k_new or
+ * v_new go where the formula takes them: into the rows that attend to them (of
+ * v_new into those dimensions of theirs), and into no other row.
+ *
+ * What is rounded on the way.  Over a BF16 cache the products q . k are of the
+ * given values, and each weight p is rounded to bf16: a term p v of O is off by at
+ * most 2^-8 of itself.  Over an 8- or 4-bit cache
+ *   - an element of q is off by at most 2^-39 of the largest of its row;
+ *   - a term p v by at most 2^-11 of itself (2^-8 for drafted tokens with at most
+ *     16 rows, max_draft x G) and 2^-35 of the largest |v| among the sequence's
+ *     listed and drafted tokens, so a value 2^35 and more below the largest is lost;
+ *   - with more than 16 rows, an element of a key by at most 2^-36 of the largest
+ *     |k| of the up to 128 keys computed with it (rows whose exponent bytes differ
+ *     by at most 21 (E4M3) or 18 (E2M1) are exact).
  *
  * Limits: hq % hkv == 0 with G in {1, 2, 4, 8, 16}; max_draft <= 256 drafted
- * tokens a sequence; max_cached tokens <= 4096 pages and <= table_stride pages;
- * batch * hkv <= 4096.  max_draft and max_cached are upper bounds that the
+ * tokens a sequence and <= total_draft; softmax_scale > 0; max_cached tokens
+ * <= 4096 pages and <= table_stride pages; batch * hkv <= 4096.  max_draft and max_cached are upper bounds that the
  * device checks: an inconsistent cu_draft entry or cached[b] sets
  * BSA_ERR_INVALID_ARG in *dev_status and reads as no drafts / an empty cache, a
  * table entry outside the cache sets it and is left out, a parent that is not
