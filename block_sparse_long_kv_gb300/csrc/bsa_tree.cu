@@ -36,8 +36,9 @@
 // Sums and statistics are fp32 from unrounded p.
 //
 // One token over 131072 cached, 32 / 4 heads of 128: bf16 55 us (269 MB: 4.9 TB/s; about 15 us of it are the
-// plan, the first chunk and the combine), e4m3 43, e2m1 44.  Over codes no unit is saturated: half of the issue
-// slots and 44 % of the integer pipe are taken, at three warps a scheduler, which do not cover the latencies.
+// plan, the first chunk and the combine), e4m3 43, e2m1 44.  Over codes no unit is saturated: 42 to 49 %
+// of the issue slots and 39 to 44 % of the integer pipe are taken, at three warps a scheduler, which do not cover
+// the latencies.
 //
 // Groups that one CTA holds whole are written by it; of the others every CTA
 // leaves an unnormalised part (O, max, sum), which tree_combine_kernel merges in
