@@ -15,6 +15,7 @@ SELECT_TOKEN_MAX = 1   # bsa_select_params.flags: per-token query aggregation
 ROPE_PAIRS = 1         # bsa_rope_shape.flags: rotate adjacent dimensions
 ROPE_NO_NORM = 2       # bsa_rope_shape.flags: rotation only
 CACHE_BF16, CACHE_E4M3, CACHE_E2M1 = 0, 1, 2   # bsa_cache_shape.format
+PROBS_F32, PROBS_BF16 = 0, 1                   # type of bsa_verify's rows
 
 STATUS = {
     0: "BSA_OK", 1: "BSA_ERR_INVALID_ARG", 2: "BSA_ERR_SHAPE", 3: "BSA_ERR_UNSUPPORTED",
@@ -58,7 +59,20 @@ class TreeShape(ctypes.Structure):
                 ("max_cached", ctypes.c_int32), ("hq", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
 
 
+class SharedShape(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("batch", ctypes.c_int32), ("total_draft", ctypes.c_int32),
+                ("max_draft", ctypes.c_int32), ("max_cached", ctypes.c_int32), ("hq", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32)]
+
+
+class VerifyShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_draft", ctypes.c_int32), ("max_draft", ctypes.c_int32),
+                ("vocab", ctypes.c_int32)]
+
+
 _SP = ctypes.POINTER(Shape)
+_HP = ctypes.POINTER(SharedShape)
+_YP = ctypes.POINTER(VerifyShape)
 _RP = ctypes.POINTER(RopeShape)
 _CP = ctypes.POINTER(CacheShape)
 _TP = ctypes.POINTER(TreeShape)
@@ -117,6 +131,20 @@ SIGNATURES = {
     "bsa_tree_workspace_bytes": (ctypes.c_size_t, [_TP, _CP]),
     "bsa_tree_fwd": (ctypes.c_int, [_TP, _CP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                     ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "bsa_shared_workspace_bytes": (ctypes.c_size_t, [_HP, _CP]),
+    "bsa_shared_fwd": (ctypes.c_int, [_HP, _CP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float,
+                                      _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "bsa_cache_fork": (ctypes.c_int, [_CP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P,
+                                      _P, _P]),
+    "bsa_cache_trim": (ctypes.c_int, [_CP, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P]),
+    "bsa_cache_grow_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "bsa_cache_grow": (ctypes.c_int, [_CP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P,
+                                      _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "bsa_cache_compact_workspace_bytes": (ctypes.c_size_t, [_CP]),
+    "bsa_cache_compact": (ctypes.c_int, [_CP, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                         ctypes.c_size_t, _P, _P]),
+    "bsa_verify": (ctypes.c_int, [_YP, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int32, _P, _P,
+                                  _P, _P, _P, _P, _P]),
     "bsa_selftest_wait_timeout": (ctypes.c_int, [_P, ctypes.c_uint64, ctypes.c_int32, _P]),
     "bsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "bsa_version": (ctypes.c_int32, []),

@@ -29,6 +29,9 @@ __all__ = [
     "CacheShape", "make_cache_shape", "CACHE_BF16", "CACHE_E4M3", "CACHE_E2M1", "cache_code_bytes",
     "cache_scale_bytes", "alloc_cache", "cache_write", "cache_read",
     "TreeShape", "make_tree_shape", "tree_workspace_bytes", "tree_fwd",
+    "SharedShape", "make_shared_shape", "shared_workspace_bytes", "shared_fwd",
+    "cache_fork", "cache_trim", "cache_grow_workspace_bytes", "cache_grow", "cache_compact_workspace_bytes",
+    "cache_compact", "VerifyShape", "make_verify_shape", "verify",
 ]
 
 Shape = _lib.Shape
@@ -40,6 +43,8 @@ ROPE_PAIRS, ROPE_NO_NORM = _lib.ROPE_PAIRS, _lib.ROPE_NO_NORM
 CacheShape = _lib.CacheShape
 CACHE_BF16, CACHE_E4M3, CACHE_E2M1 = _lib.CACHE_BF16, _lib.CACHE_E4M3, _lib.CACHE_E2M1
 TreeShape = _lib.TreeShape
+SharedShape = _lib.SharedShape
+VerifyShape = _lib.VerifyShape
 
 
 def make_shape(batch: int, seq: int, hq: int, hkv: int, head_dim: int, block: int) -> Shape:
@@ -510,6 +515,13 @@ def _rows(t, name, tokens, heads, d, dev):
     return t.data_ptr(), st if tokens > 1 else heads * d
 
 
+def _scratch(n, stream, device):
+    """n bytes, allocated on the call's stream, so that the allocator's order is that stream's."""
+    with torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream)
+                           else torch.cuda.ExternalStream(int(stream))):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def make_rope_shape(tokens: int, hq: int, hkv: int, head_dim: int, rotary_dim: int, eps: float = 1e-6,
                     flags: int = 0) -> RopeShape:
     return RopeShape(tokens, hq, hkv, head_dim, rotary_dim, eps, flags)
@@ -635,14 +647,167 @@ def tree_fwd(shape: TreeShape, cache_shape: CacheShape, cu_draft, cached, block_
             _addr(kv_cnt, "kv_cnt", i32, b * hkv, dev), softmax_scale, _addr(o, "o", bf16, t * hq * d, dev),
             _addr(lse, "lse", torch.float32, t * hq, dev))
     status = _addr(dev_status, "dev_status", i32, 1, dev)
-    if workspace is None:   # allocated on the call's stream, so that the allocator's order is that stream's
-        with torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream)
-                               else torch.cuda.ExternalStream(int(stream))):
-            workspace = torch.empty(tree_workspace_bytes(shape, cache_shape), dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        workspace = _scratch(tree_workspace_bytes(shape, cache_shape), stream, q.device)
     code = _lib.load().bsa_tree_fwd(
         ctypes.byref(shape), ctypes.byref(cache_shape), *args, _addr(workspace, "workspace", torch.uint8, 0, dev),
         workspace.numel(), status, _stream_of(stream, dev))
     _lib.check("bsa_tree_fwd", code)
+
+
+# ---------------------------------------------------------------- shared pages, page tables, verification
+
+def make_shared_shape(groups: int, batch: int, total_draft: int, max_draft: int, max_cached: int, hq: int,
+                      table_stride: int) -> SharedShape:
+    return SharedShape(groups, batch, total_draft, max_draft, max_cached, hq, table_stride)
+
+
+def shared_workspace_bytes(shape: SharedShape, cache_shape: CacheShape) -> int:
+    return int(_lib.load().bsa_shared_workspace_bytes(ctypes.byref(shape), ctypes.byref(cache_shape)))
+
+
+def shared_fwd(shape: SharedShape, cache_shape: CacheShape, cu_group, shared_pages, cu_draft, cached, block_table,
+               parents, q, k_new, v_new, cache: dict, softmax_scale, o, lse=None, workspace=None, dev_status=None,
+               stream=None):
+    """bsa_shared_fwd: tree_fwd over every cached token, for sequences whose tables begin with the same pages:
+    group y is the sequences cu_group[y] .. cu_group[y + 1] - 1 and shares its first shared_pages[y] pages."""
+    b, t, hq, hkv, d = shape.batch, shape.total_draft, shape.hq, cache_shape.hkv, cache_shape.head_dim
+    dev = torch.cuda.current_device()
+    i32, bf16 = torch.int32, torch.bfloat16
+    table, stride = _table(block_table, b, dev)
+    if stride != shape.table_stride:
+        raise ValueError(f"block_table has {stride} pages a sequence, the shape says {shape.table_stride}")
+    args = (_addr(cu_group, "cu_group", i32, shape.groups + 1, dev),
+            _addr(shared_pages, "shared_pages", i32, shape.groups, dev), _addr(cu_draft, "cu_draft", i32, b + 1, dev),
+            _addr(cached, "cached", i32, b, dev), table, _addr(parents, "parents", i32, t, dev),
+            _addr(q, "q", bf16, t * hq * d, dev), _addr(k_new, "k_new", bf16, t * hkv * d, dev),
+            _addr(v_new, "v_new", bf16, t * hkv * d, dev), *_cache(cache_shape, cache, dev), softmax_scale,
+            _addr(o, "o", bf16, t * hq * d, dev), _addr(lse, "lse", torch.float32, t * hq, dev))
+    status = _addr(dev_status, "dev_status", i32, 1, dev)
+    if workspace is None:
+        workspace = _scratch(shared_workspace_bytes(shape, cache_shape), stream, q.device)
+    code = _lib.load().bsa_shared_fwd(
+        ctypes.byref(shape), ctypes.byref(cache_shape), *args, _addr(workspace, "workspace", torch.uint8, 0, dev),
+        workspace.numel(), status, _stream_of(stream, dev))
+    _lib.check("bsa_shared_fwd", code)
+
+
+def cache_fork(shape: CacheShape, source, cached, block_table, refs, cached_out, table_out, dev_status=None, stream=None):
+    """bsa_cache_fork: row j of table_out (and cached_out) becomes row source[j] of block_table (-1: empty); the new
+    rows take the old ones' place in refs (int32 [pages])."""
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    at = _addr(source, "source", i32, 1, dev)
+    held = _addr(cached, "cached", i32, 1, dev)
+    batch, out = cached.numel(), source.numel()
+    table, stride = _table(block_table, batch, dev)
+    to, stride_out = _table(table_out, out, dev)
+    if stride_out != stride:
+        raise ValueError(f"table_out has {stride_out} pages a sequence, block_table {stride}")
+    code = _lib.load().bsa_cache_fork(
+        ctypes.byref(shape), batch, out, stride, at, held, table, _addr(refs, "refs", i32, shape.pages, dev),
+        _addr(cached_out, "cached_out", i32, out, dev), to, _addr(dev_status, "dev_status", i32, 1, dev),
+        _stream_of(stream, dev))
+    _lib.check("bsa_cache_fork", code)
+
+
+def cache_trim(shape: CacheShape, keep, cached, block_table, refs, dev_status=None, stream=None):
+    """bsa_cache_trim: sequence b keeps its first keep[b] tokens; the pages behind them are given up."""
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    at = _addr(keep, "keep", i32, 1, dev)
+    batch = keep.numel()
+    table, stride = _table(block_table, batch, dev)
+    code = _lib.load().bsa_cache_trim(
+        ctypes.byref(shape), batch, stride, at, _addr(cached, "cached", i32, batch, dev), table,
+        _addr(refs, "refs", i32, shape.pages, dev), _addr(dev_status, "dev_status", i32, 1, dev), _stream_of(stream, dev))
+    _lib.check("bsa_cache_trim", code)
+
+
+def cache_grow_workspace_bytes(batch: int) -> int:
+    return int(_lib.load().bsa_cache_grow_workspace_bytes(batch))
+
+
+def cache_grow(shape: CacheShape, cu_new, rank, grow, cached, block_table, refs, cache: dict, slots, workspace=None,
+               dev_status=None, stream=None):
+    """bsa_cache_grow: pages and slots (int32 [total_new]) for the tokens cu_new[b] .. cu_new[b + 1] - 1 of every
+    sequence, all of them or, with rank and grow (of verify), the grow[b] whose rank says so."""
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    cu = _addr(cu_new, "cu_new", i32, 2, dev)
+    to = _addr(slots, "slots", i32, 0, dev)
+    batch, total = cu_new.numel() - 1, slots.numel()
+    table, stride = _table(block_table, batch, dev)
+    args = (cu, _addr(rank, "rank", i32, total, dev), _addr(grow, "grow", i32, batch, dev),
+            _addr(cached, "cached", i32, batch, dev), table, _addr(refs, "refs", i32, shape.pages, dev),
+            *_cache(shape, cache, dev), to)
+    status = _addr(dev_status, "dev_status", i32, 1, dev)
+    if workspace is None:
+        workspace = _scratch(cache_grow_workspace_bytes(batch), stream, slots.device)
+    code = _lib.load().bsa_cache_grow(
+        ctypes.byref(shape), batch, total, stride, *args, _addr(workspace, "workspace", torch.uint8, 0, dev),
+        workspace.numel(), status, _stream_of(stream, dev))
+    _lib.check("bsa_cache_grow", code)
+
+
+def cache_compact_workspace_bytes(shape: CacheShape) -> int:
+    return int(_lib.load().bsa_cache_compact_workspace_bytes(ctypes.byref(shape)))
+
+
+def cache_compact(shape: CacheShape, cached, block_table, refs, cache: dict, live, workspace=None, dev_status=None,
+                  stream=None):
+    """bsa_cache_compact: the pages in use move to the front of the pool, and live (int32 [1]) says how many there
+    are."""
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    held = _addr(cached, "cached", i32, 1, dev)
+    batch = cached.numel()
+    table, stride = _table(block_table, batch, dev)
+    args = (held, table, _addr(refs, "refs", i32, shape.pages, dev), *_cache(shape, cache, dev),
+            _addr(live, "live", i32, 1, dev))
+    status = _addr(dev_status, "dev_status", i32, 1, dev)
+    if workspace is None:
+        workspace = _scratch(cache_compact_workspace_bytes(shape), stream, refs.device)
+    code = _lib.load().bsa_cache_compact(
+        ctypes.byref(shape), batch, stride, *args, _addr(workspace, "workspace", torch.uint8, 0, dev),
+        workspace.numel(), status, _stream_of(stream, dev))
+    _lib.check("bsa_cache_compact", code)
+
+
+def make_verify_shape(batch: int, total_draft: int, max_draft: int, vocab: int) -> VerifyShape:
+    return VerifyShape(batch, total_draft, max_draft, vocab)
+
+
+def _probs(t, name, rows, vocab, dtype, dev):
+    """(address, elements between rows) of [rows, vocab] probabilities; the rows may be strided."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, name, dev)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, vocab):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {(rows, vocab)}")
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {name} must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else vocab
+
+
+def verify(shape: VerifyShape, cu_draft, parents, tokens, p, q, u_accept, u_sample, count, rank, next_token,
+           dev_status=None, stream=None):
+    """bsa_verify: the drafted tokens that stand against the target's probabilities p [total_draft, vocab] (fp32 or
+    bf16, any stride between rows; q likewise, or None for tokens that were not drawn), and the token behind them."""
+    b, t, vocab = shape.batch, shape.total_draft, shape.vocab
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
+    dtype = p.dtype if isinstance(p, torch.Tensor) and p.dtype is torch.bfloat16 else f32
+    code = _lib.load().bsa_verify(
+        ctypes.byref(shape), _addr(cu_draft, "cu_draft", i32, b + 1, dev), _addr(parents, "parents", i32, t, dev),
+        _addr(tokens, "tokens", i32, t, dev), *_probs(p, "p", t, vocab, dtype, dev),
+        *((None, 0) if q is None else _probs(q, "q", t, vocab, dtype, dev)),
+        _lib.PROBS_F32 if dtype is f32 else _lib.PROBS_BF16, _addr(u_accept, "u_accept", f32, t, dev),
+        _addr(u_sample, "u_sample", f32, b, dev), _addr(count, "count", i32, b, dev), _addr(rank, "rank", i32, t, dev),
+        _addr(next_token, "next_token", i32, b, dev), _addr(dev_status, "dev_status", i32, 1, dev),
+        _stream_of(stream, dev))
+    _lib.check("bsa_verify", code)
 
 
 def selftest_wait_timeout(dev_status, limit_ns: int, ctas: int = 1, stream=None):

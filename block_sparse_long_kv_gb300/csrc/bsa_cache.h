@@ -60,10 +60,16 @@ struct TreeArgs {
   int batch, total, max_draft, max_cached, hq, group, table_stride;
   float scale_log2;
   int32_t *status;
+  // sequences that share pages (bsa_shared.cu only): [groups + 1] first sequences, [groups] shared pages
+  const int32_t *cu_group, *shared_pages;
+  int groups;
 };
 // Few query rows per KV head (bsa_tree.cu), and many (bsa_tree_mma.cu).
 size_t tree_mma_workspace_bytes(const CacheDims &c);
 bsa_status launch_tree_mma(const TreeArgs &a, void *workspace, cudaStream_t stream);
+// Sequences that share pages (bsa_shared.cu).
+size_t shared_workspace_bytes(const CacheDims &c, int groups, int batch, int total, int hq);
+bsa_status launch_shared(const TreeArgs &a, void *workspace, cudaStream_t stream);
 size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft);
 bsa_status launch_tree(const TreeArgs &a, void *workspace, cudaStream_t stream);
 

@@ -1,5 +1,5 @@
-// C entry points of the norm / rotation, the paged cache and the drafted-token
-// attention: argument checks on the host before anything is launched, then dispatch.
+// C entry points of the norm / rotation, the paged cache and its tables, the drafted-token
+// attention and the verification of drafted tokens: argument checks on the host before anything is launched, then dispatch.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -7,6 +7,7 @@
 #include "bsa.h"
 #include "bsa_cache.h"
 #include "bsa_internal.h"
+#include "bsa_pages.h"
 
 namespace {
 
@@ -72,6 +73,35 @@ bsa_status check_tree(const bsa_tree_shape *s, const bsa::CacheDims &c, int *gro
   if (tiles * units * s->batch * c.hkv > INT32_MAX) return BSA_ERR_UNSUPPORTED;
   *group = g;
   return BSA_OK;
+}
+
+bsa_status check_shared(const bsa_shared_shape *s, const bsa::CacheDims &c, int *group) {
+  if (s == nullptr) return BSA_ERR_INVALID_ARG;
+  if (s->groups < 1 || s->batch < 1 || s->total_draft < 1 || s->max_draft < 1 || s->max_cached < 0 || s->hq < 1 ||
+      s->table_stride < 1)
+    return BSA_ERR_SHAPE;
+  if (s->max_draft > s->total_draft || s->hq % c.hkv != 0) return BSA_ERR_SHAPE;
+  const long long pages = (static_cast<long long>(s->max_cached) + c.page - 1) / c.page;
+  if (pages > s->table_stride) return BSA_ERR_SHAPE;
+  const int g = s->hq / c.hkv;
+  if (g != 1 && g != 2 && g != 4 && g != 8 && g != 16) return BSA_ERR_UNSUPPORTED;
+  if (s->max_draft > 256) return BSA_ERR_UNSUPPORTED;
+  if ((static_cast<long long>(s->groups) + s->batch) * c.hkv > bsa::kMaxSharedJobs || s->batch > 65535)
+    return BSA_ERR_UNSUPPORTED;
+  // the units of a plan are counted in 32 bits: at most these, of 128 keys and 128 rows
+  const long long shared_tiles = static_cast<long long>(s->total_draft) * g / 128 + s->groups;
+  const long long own_tiles = (static_cast<long long>(s->max_draft) * g + 127) / 128 * s->batch;
+  const long long units = pages * (c.page / 64) + 4;
+  if (static_cast<long long>(s->total_draft) * s->hq > INT32_MAX) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<double>(shared_tiles + own_tiles) * static_cast<double>(units) * c.hkv > INT32_MAX)
+    return BSA_ERR_UNSUPPORTED;
+  *group = g;
+  return BSA_OK;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + nb && pb < pa + na;
 }
 
 const uint8_t *u8(const void *p) { return static_cast<const uint8_t *>(p); }
@@ -242,6 +272,186 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
   a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   a.status = dev_status;
   return bsa::launch_tree(a, workspace, cu_stream(stream));
+}
+
+size_t bsa_shared_workspace_bytes(const bsa_shared_shape *shape, const bsa_cache_shape *cache) {
+  bsa::CacheDims c;
+  int group;
+  if (check_cache(cache, &c) != BSA_OK || check_shared(shape, c, &group) != BSA_OK) return 0;
+  return bsa::shared_workspace_bytes(c, shape->groups, shape->batch, shape->total_draft, shape->hq);
+}
+
+bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *cache, const int32_t *cu_group,
+                          const int32_t *shared_pages, const int32_t *cu_draft, const int32_t *cached,
+                          const int32_t *block_table, const int32_t *parents, const void *q, const void *k_new,
+                          const void *v_new, const void *k_codes, const void *k_scales, const void *v_codes,
+                          const void *v_scales, float softmax_scale, void *o, float *lse, void *workspace,
+                          size_t workspace_bytes, int32_t *dev_status, bsa_stream_t stream) {
+  bsa::TreeArgs a{};
+  bsa_status st = check_cache(cache, &a.c);
+  if (st != BSA_OK) return st;
+  st = check_shared(shape, a.c, &a.group);
+  if (st != BSA_OK) return st;
+  if (!good4(cu_group) || !good4(shared_pages) || !good4(cu_draft) || !good4(cached) || !good4(block_table) ||
+      !aligned(parents, 4) || !good(q) || !good(k_new) || !good(v_new) || !good(o) || !aligned(lse, 16) ||
+      !status_ok(dev_status) || !cache_pointers_ok(a.c, k_codes, k_scales, v_codes, v_scales))
+    return BSA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || isinf(softmax_scale)) return BSA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 16) ||
+      workspace_bytes < bsa::shared_workspace_bytes(a.c, shape->groups, shape->batch, shape->total_draft, shape->hq))
+    return BSA_ERR_WORKSPACE;
+  a.cu = cu_draft;
+  a.cached = cached;
+  a.table = block_table;
+  a.parents = parents;
+  a.q = u16(q);
+  a.k_new = u16(k_new);
+  a.v_new = u16(v_new);
+  a.k_codes = u8(k_codes);
+  a.k_scales = u8(k_scales);
+  a.v_codes = u8(v_codes);
+  a.v_scales = u8(v_scales);
+  a.o = static_cast<uint16_t *>(o);
+  a.lse = lse;
+  a.batch = shape->batch;
+  a.total = shape->total_draft;
+  a.max_draft = shape->max_draft;
+  a.max_cached = shape->max_cached;
+  a.hq = shape->hq;
+  a.table_stride = shape->table_stride;
+  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  a.status = dev_status;
+  a.cu_group = cu_group;
+  a.shared_pages = shared_pages;
+  a.groups = shape->groups;
+  return bsa::launch_shared(a, workspace, cu_stream(stream));
+}
+
+bsa_status bsa_cache_fork(const bsa_cache_shape *shape, int32_t batch, int32_t batch_out, int32_t table_stride,
+                          const int32_t *source, const int32_t *cached, const int32_t *block_table, int32_t *refs,
+                          int32_t *cached_out, int32_t *table_out, int32_t *dev_status, bsa_stream_t stream) {
+  bsa::CacheDims c;
+  const bsa_status st = check_cache(shape, &c);
+  if (st != BSA_OK) return st;
+  if (batch < 1 || batch_out < 1 || table_stride < 1) return BSA_ERR_SHAPE;
+  if (static_cast<long long>(batch) + batch_out > 65535) return BSA_ERR_UNSUPPORTED;
+  if (!good4(source) || !good4(cached) || !good4(block_table) || !good4(refs) || !good4(cached_out) || !good4(table_out) ||
+      !status_ok(dev_status))
+    return BSA_ERR_INVALID_ARG;
+  const size_t in[4] = {4ull * batch_out, 4ull * batch, 4ull * batch * table_stride, 4ull * c.pages};
+  const void *from[4] = {source, cached, block_table, refs};
+  for (int i = 0; i < 4; ++i)
+    if (overlap(cached_out, 4ull * batch_out, from[i], in[i]) ||
+        overlap(table_out, 4ull * batch_out * table_stride, from[i], in[i]))
+      return BSA_ERR_INVALID_ARG;
+  const bsa::ForkArgs a{source, cached, block_table, refs, cached_out, table_out, dev_status, c.pages, c.page_shift,
+                        batch, batch_out, table_stride};
+  return bsa::launch_fork(a, cu_stream(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+bsa_status bsa_cache_trim(const bsa_cache_shape *shape, int32_t batch, int32_t table_stride, const int32_t *keep,
+                          int32_t *cached, int32_t *block_table, int32_t *refs, int32_t *dev_status,
+                          bsa_stream_t stream) {
+  bsa::CacheDims c;
+  const bsa_status st = check_cache(shape, &c);
+  if (st != BSA_OK) return st;
+  if (batch < 1 || table_stride < 1) return BSA_ERR_SHAPE;
+  if (!good4(keep) || !good4(cached) || !good4(block_table) || !good4(refs) || !status_ok(dev_status))
+    return BSA_ERR_INVALID_ARG;
+  const bsa::TrimArgs a{keep, cached, block_table, refs, dev_status, c.pages, c.page_shift, batch, table_stride};
+  return bsa::launch_trim(a, cu_stream(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+size_t bsa_cache_grow_workspace_bytes(int32_t batch) {
+  return batch < 1 || batch > bsa::kMaxDecodeRows ? 0 : bsa::grow_workspace_bytes(batch);
+}
+
+bsa_status bsa_cache_grow(const bsa_cache_shape *shape, int32_t batch, int32_t total_new, int32_t table_stride,
+                          const int32_t *cu_new, const int32_t *rank, const int32_t *grow, int32_t *cached,
+                          int32_t *block_table, int32_t *refs, void *k_codes, void *k_scales, void *v_codes,
+                          void *v_scales, int32_t *slots, void *workspace, size_t workspace_bytes,
+                          int32_t *dev_status, bsa_stream_t stream) {
+  bsa::GrowArgs a{};
+  const bsa_status st = check_cache(shape, &a.c);
+  if (st != BSA_OK) return st;
+  if (batch < 1 || total_new < 0 || table_stride < 1) return BSA_ERR_SHAPE;
+  if (batch > bsa::kMaxDecodeRows) return BSA_ERR_UNSUPPORTED;
+  if (total_new == 0) return BSA_OK;
+  if (!good4(cu_new) || !aligned(rank, 4) || !aligned(grow, 4) || !good4(cached) || !good4(block_table) || !good4(refs) ||
+      !good4(slots) || !status_ok(dev_status) || !cache_pointers_ok(a.c, k_codes, k_scales, v_codes, v_scales))
+    return BSA_ERR_INVALID_ARG;
+  if (!good(workspace) || workspace_bytes < bsa::grow_workspace_bytes(batch)) return BSA_ERR_WORKSPACE;
+  a.cu = cu_new;
+  a.rank = rank;
+  a.grow = grow;
+  a.cached = cached;
+  a.table = block_table;
+  a.refs = refs;
+  a.slots = slots;
+  a.planes[0] = static_cast<uint8_t *>(k_codes);
+  a.planes[1] = static_cast<uint8_t *>(v_codes);
+  a.planes[2] = static_cast<uint8_t *>(k_scales);
+  a.planes[3] = static_cast<uint8_t *>(v_scales);
+  a.jobs = static_cast<bsa::GrowJob *>(workspace);
+  a.status = dev_status;
+  a.batch = batch;
+  a.total = total_new;
+  a.stride = table_stride;
+  return bsa::launch_grow(a, cu_stream(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+size_t bsa_cache_compact_workspace_bytes(const bsa_cache_shape *shape) {
+  bsa::CacheDims c;
+  return check_cache(shape, &c) != BSA_OK ? 0 : bsa::compact_workspace_bytes(c.pages);
+}
+
+bsa_status bsa_cache_compact(const bsa_cache_shape *shape, int32_t batch, int32_t table_stride, const int32_t *cached,
+                             int32_t *block_table, int32_t *refs, void *k_codes, void *k_scales, void *v_codes,
+                             void *v_scales, int32_t *live, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_status, bsa_stream_t stream) {
+  bsa::CompactArgs a{};
+  const bsa_status st = check_cache(shape, &a.c);
+  if (st != BSA_OK) return st;
+  if (batch < 1 || table_stride < 1) return BSA_ERR_SHAPE;
+  if (!good4(cached) || !good4(block_table) || !good4(refs) || !good4(live) || !status_ok(dev_status) ||
+      !cache_pointers_ok(a.c, k_codes, k_scales, v_codes, v_scales))
+    return BSA_ERR_INVALID_ARG;
+  if (!good(workspace) || workspace_bytes < bsa::compact_workspace_bytes(a.c.pages)) return BSA_ERR_WORKSPACE;
+  a.cached = cached;
+  a.table = block_table;
+  a.refs = refs;
+  a.live = live;
+  a.planes[0] = static_cast<uint8_t *>(k_codes);
+  a.planes[1] = static_cast<uint8_t *>(v_codes);
+  a.planes[2] = static_cast<uint8_t *>(k_scales);
+  a.planes[3] = static_cast<uint8_t *>(v_scales);
+  a.work = static_cast<int32_t *>(workspace);
+  a.status = dev_status;
+  a.batch = batch;
+  a.stride = table_stride;
+  return bsa::launch_compact(a, cu_stream(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+bsa_status bsa_verify(const bsa_verify_shape *shape, const int32_t *cu_draft, const int32_t *parents,
+                      const int32_t *tokens, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                      int32_t type, const float *u_accept, const float *u_sample, int32_t *count, int32_t *rank,
+                      int32_t *next_token, int32_t *dev_status, bsa_stream_t stream) {
+  if (shape == nullptr) return BSA_ERR_INVALID_ARG;
+  const bsa_verify_shape &s = *shape;
+  if (s.batch < 1 || s.total_draft < 1 || s.max_draft < 1 || s.max_draft > s.total_draft || s.vocab < 1)
+    return BSA_ERR_SHAPE;
+  if (type != BSA_PROBS_F32 && type != BSA_PROBS_BF16) return BSA_ERR_UNSUPPORTED;
+  if (s.max_draft > 256 || s.batch > 65535 || s.vocab > 1 << 22) return BSA_ERR_UNSUPPORTED;
+  const unsigned size = type == BSA_PROBS_F32 ? 4 : 2;
+  if (p_stride < s.vocab || p_stride > 1ll << 30 || (q != nullptr && (q_stride < s.vocab || q_stride > 1ll << 30)))
+    return BSA_ERR_INVALID_ARG;
+  if (!good4(cu_draft) || !aligned(parents, 4) || !good4(tokens) || p == nullptr || !aligned(p, size) ||
+      !aligned(q, size) || !good4(u_accept) || !good4(u_sample) || !good4(count) || !good4(rank) || !good4(next_token) ||
+      !status_ok(dev_status))
+    return BSA_ERR_INVALID_ARG;
+  const bsa::VerifyArgs a{cu_draft, parents, tokens, p, q, p_stride, q_stride, u_accept, u_sample, count, rank,
+                          next_token, dev_status, s.batch, s.total_draft, s.max_draft, s.vocab};
+  return bsa::launch_verify(a, type == BSA_PROBS_BF16, cu_stream(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // extern "C"

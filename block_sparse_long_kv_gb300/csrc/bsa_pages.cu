@@ -1,0 +1,373 @@
+// Page tables of the cache: rows of pages with a count of the table entries that name each page.
+//
+// A page whose count is 0 is free, so the counts are all the state there is, and pages are given out lowest first.
+// Everything here is a few thousand integers; the calls are bound by launches and dependent reads, but for the copies
+// of rows (growth) and pages (compaction), which HBM bounds.
+#include <stdint.h>
+
+#include "bsa_pages.h"
+#include "bsa_tree.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPlanThreads = 1024;
+constexpr int kSms = 152;
+
+__device__ __forceinline__ void report(int32_t *status, bsa_status what) {
+  if (status != nullptr) atomicCAS(status, 0, static_cast<int32_t>(what));
+}
+
+// The cached tokens of row b, 0 (and a report) where its row of the table cannot hold them.
+__device__ __forceinline__ int held(const int32_t *cached, int b, int page_shift, int stride, int32_t *status) {
+  const int n = cached[b];
+  if (n >= 0 && (n == 0 || (n - 1) >> page_shift < stride)) return n;
+  report(status, BSA_ERR_INVALID_ARG);
+  return 0;
+}
+__device__ __forceinline__ int pages_of(int tokens, int page_shift) {
+  return tokens == 0 ? 0 : ((tokens - 1) >> page_shift) + 1;
+}
+// One table entry more or less names `page`.
+__device__ __forceinline__ void count_page(int32_t *refs, int pages, int page, int by, int32_t *status) {
+  if (page < 0 || page >= pages) report(status, BSA_ERR_INVALID_ARG);
+  else if (atomicAdd(refs + page, by) + by < 0) report(status, BSA_ERR_INVALID_ARG);
+}
+
+// ---------------------------------------------------------------- fork, trim
+
+// blockIdx.y < batch: a row of the old table, whose pages are named once less, and once more for every new row made
+// of it (one atomic for the difference); the rest: a row of the new table.
+__global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
+  const int b = blockIdx.y;
+  if (b < a.batch) {
+    int uses = 0;
+    for (int base = 0; base < a.batch_out; base += kThreads) {
+      const int j = base + static_cast<int>(threadIdx.x);
+      uses += __syncthreads_count(j < a.batch_out && a.source[j] == b);
+    }
+    const int have = pages_of(held(a.cached, b, a.page_shift, a.stride, a.status), a.page_shift);
+    if (uses == 1) return;
+    for (int j = blockIdx.x * kThreads + threadIdx.x; j < have; j += gridDim.x * kThreads)
+      count_page(a.refs, a.pages, a.table[static_cast<size_t>(b) * a.stride + j], uses - 1, a.status);
+    return;
+  }
+  const int row = b - a.batch;
+  int from = a.source[row];
+  if (from < -1 || from >= a.batch) {
+    report(a.status, BSA_ERR_INVALID_ARG);
+    from = -1;
+  }
+  const int n = from < 0 ? 0 : held(a.cached, from, a.page_shift, a.stride, a.status);
+  const int have = pages_of(n, a.page_shift);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.cached_out[row] = n;
+  for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.stride; j += gridDim.x * kThreads)
+    a.table_out[static_cast<size_t>(row) * a.stride + j] = j < have ? a.table[static_cast<size_t>(from) * a.stride + j] : -1;
+}
+
+__global__ void __launch_bounds__(kThreads) trim_kernel(const TrimArgs a) {
+  const int b = blockIdx.x;
+  const int n = held(a.cached, b, a.page_shift, a.stride, a.status), keep = a.keep[b];
+  __syncthreads();  // everyone has read the length
+  if (keep < 0 || keep > n) {
+    if (threadIdx.x == 0) report(a.status, BSA_ERR_INVALID_ARG);
+    return;
+  }
+  const int have = pages_of(n, a.page_shift);
+  for (int j = pages_of(keep, a.page_shift) + threadIdx.x; j < have; j += kThreads) {
+    int32_t *entry = a.table + static_cast<size_t>(b) * a.stride + j;
+    count_page(a.refs, a.pages, *entry, -1, a.status);
+    *entry = -1;
+  }
+  if (threadIdx.x == 0) a.cached[b] = keep;
+}
+
+// ---------------------------------------------------------------- sums over a block of kPlanThreads
+
+// The sum of the values of the threads before this one; *total the whole sum.  `warps`: [33] of shared memory.
+__device__ __forceinline__ int scan_block(int value, int *warps, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = value;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  __syncthreads();  // the last sums have been read
+  if (lane == 31) warps[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warps[lane], run = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    warps[lane] = run - w;
+    if (lane == 31) warps[32] = run;
+  }
+  __syncthreads();
+  *total = warps[32];
+  return warps[warp] + inc - value;
+}
+
+// ---------------------------------------------------------------- growth
+
+// One CTA plans: who needs how many pages (a copy of a shared last page among them, unless this is the last sequence
+// that holds it), whether there are enough, and which; sequences and pages in ascending order, so that the outcome is
+// that of one sequence after the other.
+__global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs a) {
+  extern __shared__ int sm[];
+  int *last = sm, *first = sm + a.batch;  // [batch] partial last page that gets tokens or -1, [batch + 1] first new page
+  __shared__ int warps[33];
+  __shared__ int carry;
+  const int tid = threadIdx.x, shift = a.c.page_shift, mask = a.c.page - 1;
+  auto wanted = [&](int b, int n) -> int {  // tokens sequence b grows by
+    const int t0 = a.cu[b], t1 = a.cu[b + 1];
+    if (t0 < 0 || t1 < t0 || t1 > a.total) {
+      report(a.status, BSA_ERR_INVALID_ARG);
+      return 0;
+    }
+    const int g = a.grow == nullptr ? t1 - t0 : a.grow[b];
+    if (g < 0 || g > t1 - t0 || n > INT32_MAX - g || pages_of(n + g, shift) > a.stride) {
+      report(a.status, BSA_ERR_INVALID_ARG);
+      return 0;
+    }
+    return g;
+  };
+  for (int b = tid; b < a.batch; b += kPlanThreads) {
+    const int n = held(a.cached, b, shift, a.stride, a.status), g = wanted(b, n);
+    int page = -1;
+    if (g > 0 && (n & mask) != 0) {
+      page = a.table[static_cast<size_t>(b) * a.stride + (n >> shift)];
+      if (page < 0 || page >= a.c.pages) {
+        report(a.status, BSA_ERR_INVALID_ARG);
+        page = -1;
+      }
+    }
+    last[b] = page;
+  }
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  for (int base = 0; base < a.batch; base += kPlanThreads) {
+    const int b = base + tid;
+    int need = 0;
+    if (b < a.batch) {
+      const int n = held(a.cached, b, shift, a.stride, nullptr), page = last[b];
+      int g = wanted(b, n);
+      const bool lost = g > 0 && (n & mask) != 0 && page < 0;  // its last page is not in the cache
+      if (lost) g = 0;
+      bool copy = false;
+      if (page >= 0) {
+        const int refs = a.refs[page];
+        int earlier = 0;
+        if (refs > 1)
+          for (int x = 0; x < b; ++x) earlier += last[x] == page ? 1 : 0;
+        copy = refs - earlier > 1;
+      }
+      need = g == 0 ? 0 : pages_of(n + g, shift) - pages_of(n, shift) + (copy ? 1 : 0);
+      a.jobs[b] = GrowJob{g > 0 ? n : -1, copy ? page : -1, -1, copy ? n & mask : 0};
+    }
+    int total;
+    const int before = scan_block(need, warps, &total);
+    if (b < a.batch) first[b] = carry + before;
+    __syncthreads();
+    if (tid == 0) carry += total;
+    __syncthreads();
+  }
+  const int total = carry;
+  if (tid == 0) first[a.batch] = total;
+  __syncthreads();
+  // the free pages, lowest first: counted until there are enough, then given out
+  for (int pass = 0; pass < 2 && total > 0; ++pass) {
+    int found = 0;
+    for (int base = 0; base < a.c.pages && found < total; base += kPlanThreads) {
+      const int p = base + tid;
+      const bool is_free = p < a.c.pages && a.refs[p] == 0;
+      int n;
+      const int k = found + scan_block(is_free ? 1 : 0, warps, &n);
+      if (pass == 1 && is_free && k < total) {
+        int lo = 0, hi = a.batch - 1;
+        while (lo < hi) {  // the last sequence whose first new page is at or before k: the one that gets it
+          const int mid = (lo + hi + 1) >> 1;
+          if (first[mid] <= k) lo = mid;
+          else hi = mid - 1;
+        }
+        GrowJob &job = a.jobs[lo];
+        const int copies = job.from >= 0 ? 1 : 0;
+        const int at = pages_of(job.start, shift) - copies + k - first[lo];
+        if (copies && k == first[lo]) job.to = p;
+        a.table[static_cast<size_t>(lo) * a.stride + at] = p;
+        a.refs[p] = 1;
+      }
+      found += n;
+    }
+    __syncthreads();
+    if (found < total) {  // not enough: nobody grows
+      if (tid == 0) report(a.status, BSA_ERR_WORKSPACE);
+      for (int b = tid; b < a.batch; b += kPlanThreads) a.jobs[b] = GrowJob{-1, -1, -1, 0};
+      return;
+    }
+  }
+  for (int b = tid; b < a.batch; b += kPlanThreads) {
+    const GrowJob job = a.jobs[b];
+    if (job.start < 0) continue;
+    if (job.from >= 0) atomicSub(a.refs + job.from, 1);
+    a.cached[b] = job.start + wanted(b, job.start);
+  }
+}
+
+// 16 bytes at a time, or bytes where the ends are not on such boundaries.
+__device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from, int bytes) {
+  const int wide = ((reinterpret_cast<uintptr_t>(to) | reinterpret_cast<uintptr_t>(from)) & 15) == 0 ? bytes / 16 : 0;
+  for (int i = threadIdx.x; i < wide; i += blockDim.x)
+    reinterpret_cast<uint4 *>(to)[i] = __ldg(reinterpret_cast<const uint4 *>(from) + i);
+  for (int i = wide * 16 + threadIdx.x; i < bytes; i += blockDim.x) to[i] = __ldg(from + i);
+}
+
+// The first blocks write the slots of the new tokens; then one for every (sequence, KV head, K or V) copies the rows
+// of a shared last page.
+__global__ void __launch_bounds__(kThreads) grow_rows_kernel(const GrowArgs a, int slot_blocks) {
+  after_previous_kernel();
+  if (static_cast<int>(blockIdx.x) < slot_blocks) {
+    for (int t = blockIdx.x * kThreads + threadIdx.x; t < a.total; t += slot_blocks * kThreads) {
+      int lo = 0, hi = a.batch - 1;
+      while (lo < hi) {  // the last sequence that begins at or before t
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.cu + mid) <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const int t0 = __ldg(a.cu + lo), t1 = __ldg(a.cu + lo + 1);
+      if (t < t0 || t >= t1) continue;  // past the last sequence: left as it was
+      const GrowJob job = a.jobs[lo];
+      int slot = -1;
+      if (job.start >= 0) {
+        const int g = a.cached[lo] - job.start, rank = a.rank == nullptr ? t - t0 : __ldg(a.rank + t);
+        if (rank >= 0 && rank < g) {
+          const int pos = job.start + rank;
+          const int page = a.table[static_cast<size_t>(lo) * a.stride + (pos >> a.c.page_shift)];
+          slot = (page << a.c.page_shift) + (pos & (a.c.page - 1));
+        }
+      }
+      a.slots[t] = slot;
+    }
+    return;
+  }
+  const int x = blockIdx.x - slot_blocks, per = 2 * a.c.hkv;
+  const int b = x / per, head = x % per / 2, kv = x & 1;
+  const GrowJob job = a.jobs[b];
+  if (job.to < 0) return;
+  const size_t tile_from = static_cast<size_t>(job.from) * a.c.hkv + head;
+  const size_t tile_to = static_cast<size_t>(job.to) * a.c.hkv + head;
+  const size_t codes = static_cast<size_t>(a.c.page) * a.c.row;
+  copy_bytes(a.planes[kv] + tile_to * codes, a.planes[kv] + tile_from * codes, job.rows * a.c.row);
+  if (a.c.per_row == 0) return;
+  const size_t scales = static_cast<size_t>(a.c.page) * a.c.per_row;
+  uint8_t *to = a.planes[2 + kv] + tile_to * scales;
+  const uint8_t *from = a.planes[2 + kv] + tile_from * scales;
+  copy_bytes(to, from, job.rows);
+  if (a.c.per_row > 1) copy_bytes(to + a.c.page, from + a.c.page, job.rows * (a.c.per_row - 1));
+}
+
+// ---------------------------------------------------------------- compaction
+
+// One CTA: with L pages in use, the pages in use from L on go, in order, to the free ones below L.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
+  __shared__ int warps[33];
+  const int tid = threadIdx.x, pages = a.c.pages;
+  int *holes = a.work + 4, *moved = holes + pages, *to = moved + pages;
+  int live = 0;
+  for (int base = 0; base < pages; base += kPlanThreads) live += __syncthreads_count(base + tid < pages && a.refs[base + tid] > 0);
+  int nh = 0, nm = 0;
+  for (int base = 0; base < pages; base += kPlanThreads) {
+    const int p = base + tid;
+    const bool used = p < pages && a.refs[p] > 0;
+    const bool hole = p < live && !used, mover = p >= live && used;
+    int n;
+    const int k = scan_block((hole ? 1 : 0) + (mover ? 0x10000 : 0), warps, &n);  // (at most 1024 of each a round)
+    if (hole) holes[nh + (k & 0xFFFF)] = p;
+    if (mover) moved[nm + (k >> 16)] = p;
+    if (p >= live && p < pages && !used) to[p] = -1;  // (no entry should name it)
+    nh += n & 0xFFFF;
+    nm += n >> 16;
+  }
+  __syncthreads();
+  for (int i = tid; i < nm; i += kPlanThreads) {
+    const int src = moved[i], dst = holes[i];
+    to[src] = dst;
+    a.refs[dst] = a.refs[src];
+    a.refs[src] = 0;
+  }
+  if (tid == 0) {
+    a.work[0] = nm;
+    a.work[1] = live;
+    *a.live = live;
+  }
+}
+
+// The first blocks rewrite the tables, all copy pages.
+__global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArgs a) {
+  after_previous_kernel();
+  const int pages = a.c.pages, moves = a.work[0], live = a.work[1];
+  const int *holes = a.work + 4, *moved = holes + pages, *to = moved + pages;
+  const long long entries = static_cast<long long>(a.batch) * a.stride;
+  for (long long e = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; e < entries;
+       e += static_cast<long long>(gridDim.x) * kThreads) {
+    const int b = static_cast<int>(e / a.stride), j = static_cast<int>(e % a.stride);
+    if (j >= pages_of(held(a.cached, b, a.c.page_shift, a.stride, a.status), a.c.page_shift)) continue;
+    const int p = a.table[e];
+    const int q = p >= 0 && p < live ? p : p >= live && p < pages ? to[p] : -1;
+    if (q < 0) report(a.status, BSA_ERR_INVALID_ARG);
+    else if (q != p) a.table[e] = q;
+  }
+  const size_t tile[2] = {static_cast<size_t>(a.c.hkv) * a.c.page * a.c.row,
+                          static_cast<size_t>(a.c.hkv) * a.c.page * a.c.per_row};
+  const int planes = a.c.per_row == 0 ? 2 : 4;
+  for (int plane = 0; plane < planes; ++plane) {
+    const size_t bytes = tile[plane >> 1];  // a page's, a multiple of 64
+    const size_t n16 = bytes / 16;
+    const long long all = static_cast<long long>(n16) * moves;
+    uint4 *at = reinterpret_cast<uint4 *>(a.planes[plane]);
+    for (long long e = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; e < all;
+         e += static_cast<long long>(gridDim.x) * kThreads) {
+      const int i = static_cast<int>(e / static_cast<long long>(n16));
+      const size_t o = static_cast<size_t>(e - static_cast<long long>(i) * static_cast<long long>(n16));
+      at[static_cast<size_t>(holes[i]) * n16 + o] = at[static_cast<size_t>(moved[i]) * n16 + o];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream) {
+  const int x = (a.stride + kThreads - 1) / kThreads;
+  fork_kernel<<<dim3(x < 8 ? x : 8, a.batch + a.batch_out), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_trim(const TrimArgs &a, cudaStream_t stream) {
+  trim_kernel<<<a.batch, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+size_t grow_workspace_bytes(int batch) { return static_cast<size_t>(batch) * sizeof(GrowJob); }
+
+cudaError_t launch_grow(const GrowArgs &a, cudaStream_t stream) {
+  grow_plan_kernel<<<1, kPlanThreads, (2 * a.batch + 1) * sizeof(int), stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int want = (a.total + kThreads - 1) / kThreads, slot_blocks = want < kSms ? want : kSms;
+  return launch_after(grow_rows_kernel, dim3(slot_blocks + a.batch * a.c.hkv * 2), kThreads, stream, a, slot_blocks);
+}
+
+size_t compact_workspace_bytes(int pages) { return (4 + 3 * static_cast<size_t>(pages)) * 4; }
+
+cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream) {
+  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(compact_move_kernel, dim3(kSms * 8), kThreads, stream, a);
+}
+
+}  // namespace bsa

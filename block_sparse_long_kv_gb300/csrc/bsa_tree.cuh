@@ -62,6 +62,78 @@ __device__ __forceinline__ int parent_of(const TreeArgs &a, int start, int i) {
   return -1;
 }
 
+// Sequences that share pages: group y is the sequences cu_group[y] .. cu_group[y + 1] - 1, whose tables begin with the
+// same shared_pages[y] pages.  What is not as documented sets *status; a group then shares none, and a sequence of no
+// group is on its own.
+__device__ __forceinline__ void report_arg(const TreeArgs &a) {
+  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
+}
+struct SharedGroup {
+  int first, last, pages;  // its sequences first .. last - 1
+};
+__device__ __forceinline__ SharedGroup shared_group(const TreeArgs &a, int y) {
+  SharedGroup s{__ldg(a.cu_group + y), __ldg(a.cu_group + y + 1), __ldg(a.shared_pages + y)};
+  if (s.first < 0 || s.last < s.first || s.last > a.batch) {
+    report_arg(a);
+    s.first = s.last = 0;
+  }
+  if (s.pages < 0 || s.pages > a.max_cached >> a.c.page_shift) {
+    report_arg(a);
+    s.pages = 0;
+  }
+  return s;
+}
+// The group of sequence b; -1 for none.
+__device__ __forceinline__ int group_of(const TreeArgs &a, int b) {
+  int lo = 0, hi = a.groups - 1;
+  while (lo < hi) {  // the last group that begins at or before b
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(a.cu_group + mid) <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  if (__ldg(a.cu_group + lo) <= b && b < __ldg(a.cu_group + lo + 1)) return lo;
+  report_arg(a);
+  return -1;
+}
+
+// Job x of a call over shared pages: first every group's rows over its shared pages, KV head by KV head, then every
+// sequence's rows over its own pages and its drafts.
+struct SharedJob {
+  Drafts rows;     // tokens of the rows
+  int seq;         // whose table row names the pages
+  int first_page;  // the first of them
+  int keys;        // cached tokens from there on
+  int draft_keys;  // and drafted tokens behind them
+};
+__device__ __forceinline__ SharedJob shared_job(const TreeArgs &a, int x) {
+  const int shared = a.groups * a.c.hkv;
+  SharedJob j{Drafts{0, 0}, 0, 0, 0, 0};
+  if (x < shared) {
+    const SharedGroup s = shared_group(a, x / a.c.hkv);
+    if (s.first == s.last || s.pages == 0) return j;
+    const int start = __ldg(a.cu + s.first), end = __ldg(a.cu + s.last);
+    if (start < 0 || end < start || end > a.total) {  // (its sequences report it)
+      return j;
+    }
+    j.rows = Drafts{start, end - start};
+    j.keys = s.pages << a.c.page_shift;
+    j.seq = s.first;  // the first that drafts a token
+    while (j.seq + 1 < s.last && __ldg(a.cu + j.seq + 1) == start) ++j.seq;
+    return j;
+  }
+  j.seq = (x - shared) / a.c.hkv;
+  j.rows = drafts_of(a, j.seq);
+  j.draft_keys = j.rows.len;
+  const int y = group_of(a, j.seq), n = cached_of(a, j.seq);
+  if (y >= 0) j.first_page = shared_group(a, y).pages;
+  j.keys = n - (j.first_page << a.c.page_shift);
+  if (j.keys < 0) {  // its table does not hold the group's pages
+    if (j.rows.len > 0) report_arg(a);
+    j.keys = 0;
+  }
+  return j;
+}
+
 // A kernel launched by launch_after may start before the one ahead of it in the stream has ended; it waits
 // here, before its first read, until that one has ended and its writes are visible.
 __device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

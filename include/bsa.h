@@ -600,6 +600,144 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
                         bsa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * bsa_shared_fwd - attention of sequences that share the first pages of their
+ * tables (continuations of one prompt), the shared pages read once for all.
+ *
+ * The arguments are those of bsa_tree_fwd without lists, and so is the result:
+ * token t attends to every cached token of its sequence and to its own path of
+ * the drafts.  What is added says which sequences share pages: group y is the
+ * sequences cu_group[y] .. cu_group[y+1]-1 (int32 [groups + 1], from 0 to
+ * batch; a group may be of one sequence, or empty), and the block tables of its
+ * sequences begin with the same shared_pages[y] pages (int32 [groups]; 0:
+ * none), all of them full: cached[b] >= shared_pages[y] * page.  The shared
+ * pages are read from the table of the group's first sequence that drafts a
+ * token; a sequence without drafts takes no part and needs no pages.
+ *
+ * What is rounded: as stated at bsa_tree_fwd for more than 16 rows.
+ *
+ * Limits: as bsa_tree_fwd, but max_cached may be any number of pages up to
+ * table_stride, and (groups + batch) * hkv <= 6144 instead of batch * hkv.  The
+ * device checks what bsa_tree_fwd's does, and: of a cu_group entry that is
+ * inconsistent, or a shared_pages entry below 0 or past max_cached, it sets
+ * BSA_ERR_INVALID_ARG in *dev_status and the group shares no pages; a sequence of no
+ * group, or of such a one, attends to all its pages by itself; one that drafts but holds fewer
+ * tokens than the group's pages sets it and attends to the group's pages.
+ * workspace: bsa_shared_workspace_bytes bytes, 16-byte aligned, the caller's
+ * alone while the call runs (two graphs that may replay at the same time need one each).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t groups, batch, total_draft, max_draft, max_cached, hq, table_stride;
+} bsa_shared_shape;
+
+size_t bsa_shared_workspace_bytes(const bsa_shared_shape *shape, const bsa_cache_shape *cache);
+bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *cache, const int32_t *cu_group,
+                          const int32_t *shared_pages, const int32_t *cu_draft, const int32_t *cached,
+                          const int32_t *block_table, const int32_t *parents, const void *q, const void *k_new,
+                          const void *v_new, const void *k_codes, const void *k_scales, const void *v_codes,
+                          const void *v_scales, float softmax_scale, void *o, float *lse, void *workspace,
+                          size_t workspace_bytes, int32_t *dev_status, bsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Page tables: which pages a sequence holds, and who else does.
+ *
+ * A row of block_table (int32 [batch, table_stride]) names the pages of a
+ * sequence's cached[b] tokens, ceil(cached[b] / page) of them; entries behind
+ * those are -1 or left as they were.  refs (int32 [pages]) counts the entries
+ * that name a page: 0 is a free page, and all zeros an empty pool.  These calls keep
+ * both in step; they run on the device alone, so a step that forks, grows and
+ * trims can be captured.  Free pages are given out lowest first, to sequences in ascending order.
+ *
+ * bsa_cache_fork: the rows of table_out [batch_out, table_stride] and
+ * cached_out [batch_out] take the place of those of block_table: row j is a
+ * copy of row source[j] (int32; -1: an empty row).  A row named several times is
+ * shared from then on, one that is not named gives up its pages.  refs is
+ * updated in place; the outputs overlap no input.
+ *
+ * bsa_cache_grow: sequence b gets the tokens cu_new[b] .. cu_new[b+1]-1 of
+ * total_new, or with `grow` (int32 [batch], nullable) the first grow[b] of as many
+ * places.  Pages are taken as needed, and a last page that is not full and
+ * that others share is replaced by a copy of its rows (the last sequence that
+ * still holds it keeps it).  slots[t] (int32 [total_new], for bsa_cache_write)
+ * is the place of token t: the position cached[b] + rank[t] (rank nullable: t -
+ * cu_new[b]), or -1 where rank[t] is not in [0, grow[b]).  cached, block_table
+ * and refs are updated in place, and rows of the cache are copied in all its
+ * arrays.  When the pool lacks pages nothing changes: *dev_status is set to
+ * BSA_ERR_WORKSPACE and every slot is -1.  A sequence whose row cannot hold the
+ * tokens (or whose cu_new, grow, cached or last page is inconsistent) sets
+ * BSA_ERR_INVALID_ARG and does not grow.  Slots past cu_new[batch] are left as
+ * they were.  batch <= 4096.
+ *
+ * bsa_cache_trim: sequence b keeps its first keep[b] tokens (int32 [batch],
+ * 0 <= keep[b] <= cached[b]; others set BSA_ERR_INVALID_ARG and change nothing
+ * for b); pages behind them are given up, their entries set to -1.
+ *
+ * bsa_cache_compact: with L pages in use, the pages in use from L on move, in
+ * ascending order, to the free ones below L, in ascending order; the tables and
+ * refs follow, and *live = L (int32).  Pages from L on are free afterwards.  block_table must hold every
+ * entry that refs counts.
+ *
+ * Entries and counts that do not fit together set BSA_ERR_INVALID_ARG and are
+ * left out.  All int32 arrays 4-byte aligned, workspaces 16-byte.
+ * ------------------------------------------------------------------------ */
+bsa_status bsa_cache_fork(const bsa_cache_shape *shape, int32_t batch, int32_t batch_out, int32_t table_stride,
+                          const int32_t *source, const int32_t *cached, const int32_t *block_table, int32_t *refs,
+                          int32_t *cached_out, int32_t *table_out, int32_t *dev_status, bsa_stream_t stream);
+size_t bsa_cache_grow_workspace_bytes(int32_t batch);
+bsa_status bsa_cache_grow(const bsa_cache_shape *shape, int32_t batch, int32_t total_new, int32_t table_stride,
+                          const int32_t *cu_new, const int32_t *rank, const int32_t *grow, int32_t *cached,
+                          int32_t *block_table, int32_t *refs, void *k_codes, void *k_scales, void *v_codes,
+                          void *v_scales, int32_t *slots, void *workspace, size_t workspace_bytes,
+                          int32_t *dev_status, bsa_stream_t stream);
+bsa_status bsa_cache_trim(const bsa_cache_shape *shape, int32_t batch, int32_t table_stride, const int32_t *keep,
+                          int32_t *cached, int32_t *block_table, int32_t *refs, int32_t *dev_status,
+                          bsa_stream_t stream);
+size_t bsa_cache_compact_workspace_bytes(const bsa_cache_shape *shape);
+bsa_status bsa_cache_compact(const bsa_cache_shape *shape, int32_t batch, int32_t table_stride, const int32_t *cached,
+                             int32_t *block_table, int32_t *refs, void *k_codes, void *k_scales, void *v_codes,
+                             void *v_scales, int32_t *live, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_status, bsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsa_verify - which drafted tokens stand, and the token behind them.
+ *
+ * Sequence b drafts tokens cu_draft[b] .. cu_draft[b+1]-1 (tokens: int32 ids;
+ * parents as in bsa_tree_fwd).  Its first token is settled (the one drawn last);
+ * every other hangs on its parent.  Row t of p [total_draft, p_stride] is the
+ * target's distribution over the vocabulary behind token t, row t of q
+ * [total_draft, q_stride] the one token t was drawn from (nullable: the tokens
+ * were not drawn, and q is 1 at token t).  From the first token on, the children
+ * of the node reached are tried in ascending order: with R = p[node] and M = 1 at
+ * first, child t is taken if u_accept[t] * M * q[t][x] < R[x], x = tokens[t], and
+ * becomes the node; if not, R = max(R - M q[t], 0) and M = sum R.  When no child is
+ * left, next_token[b] is drawn from R: the lowest j with R[0] + .. + R[j] >
+ * u_sample[b] * sum R (R = p[node] where the sum is 0).  The tokens' distribution is
+ * then that of p alone.
+ *   count[b]   tokens taken, the first among them (0 for a sequence without
+ *              drafts, with next_token -1)
+ *   rank[t]    token t's place in the path, 0 for the first, -1 if not taken; with
+ *              count what bsa_cache_grow takes as rank and grow
+ * p, q: fp32 or bf16 (`type`), probabilities in [0, 1] that add up to about 1 in
+ * every row; what is negative or NaN counts as 0, what is larger as 1.  u_accept
+ * [total_draft] and u_sample [batch] in [0, 1), fp32 (of u_sample, 1 and more or NaN takes the
+ * last token that has anything left).  Sums are exact in units of 2^-60.  Another root, a
+ * parent that is not smaller than its token or an id outside the vocabulary (the last two set
+ * BSA_ERR_INVALID_ARG in *dev_status) is not reached.  rank past cu_draft[batch] is left as it was.  Limits: max_draft <= 256
+ * and <= total_draft, vocab <= 2^22, batch <= 65535, strides in elements, at least vocab and at most 2^30; p and q
+ * aligned to their elements, the rest 4-byte.
+ * ------------------------------------------------------------------------ */
+#define BSA_PROBS_F32 0
+#define BSA_PROBS_BF16 1
+
+typedef struct {
+  int32_t batch, total_draft, max_draft, vocab;
+} bsa_verify_shape;
+
+bsa_status bsa_verify(const bsa_verify_shape *shape, const int32_t *cu_draft, const int32_t *parents,
+                      const int32_t *tokens, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                      int32_t type, const float *u_accept, const float *u_sample, int32_t *count, int32_t *rank,
+                      int32_t *next_token, int32_t *dev_status, bsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Self-test of the device wait limits (no compute).  Launches `ctas` CTAs
  * (1..8) whose first thread waits, through the bounded wait the attention
  * kernel uses, on an mbarrier that nothing completes.  CTA 0 gives up after
