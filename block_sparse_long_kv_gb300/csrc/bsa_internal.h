@@ -10,7 +10,6 @@
 namespace bsa {
 
 constexpr int kMaxBlocks = 4096;  // nb limit (select kernel keeps one score row in smem)
-constexpr int kMaxSharedJobs = 6144;  // (groups + batch) * hkv limit of attention over shared pages (likewise)
 constexpr int kMaxDecodeRows = 4096;  // batch * hkv limit of decode (its plan sits in smem)
 
 // A batch is either fixed-length (cu == nullptr: sequence b is tokens

@@ -358,7 +358,7 @@ cudaError_t launch_grow(const GrowArgs &a, cudaStream_t stream) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int want = (a.total + kThreads - 1) / kThreads, slot_blocks = want < kSms ? want : kSms;
-  return launch_after(grow_rows_kernel, dim3(slot_blocks + a.batch * a.c.hkv * 2), kThreads, stream, a, slot_blocks);
+  return launch_after(grow_rows_kernel, dim3(slot_blocks + a.batch * a.c.hkv * 2), kThreads, 0, stream, a, slot_blocks);
 }
 
 size_t compact_workspace_bytes(int pages) { return (4 + 3 * static_cast<size_t>(pages)) * 4; }
@@ -367,7 +367,7 @@ cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream) {
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(compact_move_kernel, dim3(kSms * 8), kThreads, stream, a);
+  return launch_after(compact_move_kernel, dim3(kSms * 8), kThreads, 0, stream, a);
 }
 
 }  // namespace bsa

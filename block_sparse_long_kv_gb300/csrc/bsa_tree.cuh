@@ -96,57 +96,77 @@ __device__ __forceinline__ int group_of(const TreeArgs &a, int b) {
   return -1;
 }
 
-// Job x of a call over shared pages: first every group's rows over its shared pages, KV head by KV head, then every
-// sequence's rows over its own pages and its drafts.
-struct SharedJob {
-  Drafts rows;     // tokens of the rows
-  int seq;         // whose table row names the pages
-  int first_page;  // the first of them
-  int keys;        // cached tokens from there on
-  int draft_keys;  // and drafted tokens behind them
+// The rows of a group over its shared pages: every token that its sequences draft.
+struct SharedRows {
+  Drafts rows;  // none where nothing is shared
+  int seq;      // whose table row names the pages: the first that drafts a token
+  int pages;
 };
-__device__ __forceinline__ SharedJob shared_job(const TreeArgs &a, int x) {
-  const int shared = a.groups * a.c.hkv;
-  SharedJob j{Drafts{0, 0}, 0, 0, 0, 0};
-  if (x < shared) {
-    const SharedGroup s = shared_group(a, x / a.c.hkv);
-    if (s.first == s.last || s.pages == 0) return j;
-    const int start = __ldg(a.cu + s.first), end = __ldg(a.cu + s.last);
-    if (start < 0 || end < start || end > a.total) {  // (its sequences report it)
-      return j;
-    }
-    j.rows = Drafts{start, end - start};
-    j.keys = s.pages << a.c.page_shift;
-    j.seq = s.first;  // the first that drafts a token
-    while (j.seq + 1 < s.last && __ldg(a.cu + j.seq + 1) == start) ++j.seq;
-    return j;
-  }
-  j.seq = (x - shared) / a.c.hkv;
-  j.rows = drafts_of(a, j.seq);
-  j.draft_keys = j.rows.len;
-  const int y = group_of(a, j.seq), n = cached_of(a, j.seq);
-  if (y >= 0) j.first_page = shared_group(a, y).pages;
-  j.keys = n - (j.first_page << a.c.page_shift);
-  if (j.keys < 0) {  // its table does not hold the group's pages
-    if (j.rows.len > 0) report_arg(a);
-    j.keys = 0;
-  }
-  return j;
+__device__ __forceinline__ SharedRows shared_rows(const TreeArgs &a, int y) {
+  const SharedGroup s = shared_group(a, y);
+  SharedRows r{Drafts{0, 0}, s.first, s.pages};
+  if (s.first == s.last || s.pages == 0) return r;
+  const int start = __ldg(a.cu + s.first), end = __ldg(a.cu + s.last);
+  if (start < 0 || end < start || end > a.total) return r;  // (its sequences report it)
+  r.rows = Drafts{start, end - start};
+  while (r.seq + 1 < s.last && __ldg(a.cu + r.seq + 1) == start) ++r.seq;
+  return r;
 }
+
+// The keys of sequence b that it does not share: its cached tokens from page `first` on.
+struct OwnKeys {
+  int first, n;
+};
+__device__ __forceinline__ OwnKeys own_keys(const TreeArgs &a, int b, int drafts) {
+  const int y = group_of(a, b), n = cached_of(a, b);
+  OwnKeys k{y >= 0 ? shared_group(a, y).pages : 0, 0};
+  k.n = n - (k.first << a.c.page_shift);
+  if (k.n < 0) {  // its table does not hold the group's pages
+    if (drafts > 0) report_arg(a);
+    k.n = 0;
+  }
+  return k;
+}
+
+// Where a call over shared pages leaves results for its combine, in fp32: O unnormalised, the maximum, the sum against
+// it.  Row buffers [3][rows]: 0 and 1 over shared pages (1 only where two softmax lanes take turns over one row tile),
+// 2 over a sequence's own keys; their statistics [3][2][rows], a row's sum in two halves over shared pages.
+struct SharedOut {
+  float *row_o;
+  float2 *row_ml;
+  size_t rows;
+  int *plan;  // first unit of every group, for the kernel that fills it
+};
+
+// How the kernel over the sequences' own keys leaves what several of its CTAs share: two parts per CTA, of `rows` rows
+// each; O of a row in order (`rows_first`), or four dimensions of all rows at a time.
+struct OwnParts {
+  int rows, ctas;
+  bool rows_first;
+};
+OwnParts own_few_parts(const CacheDims &c);
+OwnParts own_many_parts(const TreeArgs &a);
+cudaError_t launch_own_few(const TreeArgs &a, const SharedOut &so, float *part_o, float *part_ml, cudaStream_t stream);
+cudaError_t launch_own_many(const TreeArgs &a, const SharedOut &so, float *part_o, float *part_ml, float *lane_o,
+                            cudaStream_t stream);
+
+// Lets the next kernel of the stream start beside this one, if it was launched by launch_after.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A kernel launched by launch_after may start before the one ahead of it in the stream has ended; it waits
 // here, before its first read, until that one has ended and its writes are visible.
 __device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Launches a short kernel so that its launch overlaps the end of the kernel ahead of it.
+// Launches a kernel so that its launch overlaps the end of the kernel ahead of it.
 template <typename... Params, typename... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -137,7 +137,7 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const int shared = static_cast<int>(tiles < kSms - 1 ? tiles : kSms - 1);  // at most: a run boundary each
   const int most = rows < kRows * C::NTQ ? rows : kRows * C::NTQ;
   const dim3 grid(shared, D / kCombineDims, (most + kCombineRows - 1) / kCombineRows);
-  const cudaError_t e = launch_after(tree_mma_combine_kernel<D, PAIR>, grid, kCombineWarps * 32, stream, a,
+  const cudaError_t e = launch_after(tree_mma_combine_kernel<D, PAIR>, grid, kCombineWarps * 32, 0, stream, a,
                                      static_cast<const float *>(part_o), static_cast<const float *>(part_ml),
                                      static_cast<const TreeRun *>(runs));
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;

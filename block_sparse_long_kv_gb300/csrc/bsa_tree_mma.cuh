@@ -1,11 +1,9 @@
 // Attention of drafted tokens over the paged cache on tcgen05 tensor cores, for
-// the many query rows of a tree (drafted tokens x heads of a KV group), or of all
-// sequences that share pages (SHARED).
+// the many query rows of a tree (drafted tokens x heads of a KV group).
 //
 // Rows.  Query row r of a (sequence, KV head) is drafted token r / G, head r % G.
-// SHARED: the rows of a group of sequences come twice, once together over the shared
-// pages (row r is token r / G of all the group's), once by sequence over its own
-// pages and drafts; every result is left for the combine in fp32.
+// OWN: the part of a call over shared pages that sequences do not share, their keys
+// behind those pages; every result is left for that call's combine in fp32.
 // 128 rows are one MMA tile.  Keys come in units of 128: pairs of the 64-key
 // chunks of the kept pages, then the drafted tokens.  The units of all row tiles
 // are laid end to end and cut into equal runs, one per CTA (one CTA per SM); a
@@ -227,34 +225,20 @@ __device__ __forceinline__ bool wait_parked(uint32_t bar, uint32_t parity, const
   }
 }
 
-// SHARED: where whole row tiles and the plan are left for the combine.  row_o [2][total * hq][D] (over the shared
-// pages, then over a sequence's own keys) and row_ml hold O, the maximum and the sum against it.
-struct SharedOut {
-  float *row_o;
-  float2 *row_ml;
-  int *plan;  // [groups + 1] first unit
-};
-
 // Units of one row tile of group x, its row tiles, and the 64-key chunks of its kept pages.
 struct GroupPlan {
   int per, tiles, chunks;
 };
-template <int NTQ, bool SHARED>
+template <int NTQ, bool OWN>
 __device__ __forceinline__ GroupPlan plan_of(const TreeArgs &a, int x) {
-  if constexpr (SHARED) {
-    const SharedJob j = shared_job(a, x);
-    GroupPlan p;
-    p.chunks = (j.keys + kChunk - 1) / kChunk;
-    p.per = (p.chunks + 1) / 2 + (j.draft_keys + kUnit - 1) / kUnit;
-    p.tiles = (j.rows.len * a.group + kRows * NTQ - 1) / (kRows * NTQ);
-    return p;
-  }
   const int b = x / a.c.hkv;
-  const int listed = a.kv_cnt == nullptr ? 0 : __ldg(a.kv_cnt + x);  // (the loads in one round)
-  const int n = cached_of(a, b);
+  const int listed = OWN || a.kv_cnt == nullptr ? 0 : __ldg(a.kv_cnt + x);  // (the loads in one round)
+  int n = 0;
+  if constexpr (!OWN) n = cached_of(a, b);
   const Drafts dr = drafts_of(a, b);
+  if constexpr (OWN) n = own_keys(a, b, dr.len).n;
   GroupPlan p;
-  if (a.kv_cnt == nullptr) {
+  if (OWN || a.kv_cnt == nullptr) {
     p.chunks = (n + kChunk - 1) / kChunk;
   } else {
     const int pages = (n + a.c.page - 1) >> a.c.page_shift;
@@ -270,13 +254,7 @@ struct Segment {
   int grp, rt, first, units;  // group, row tile, first unit (of the whole plan) and units in this run
   int rs, re;                 // the row tile's units
 };
-// The tokens of the rows of group x.
-template <bool SHARED>
-__device__ __forceinline__ Drafts rows_of(const TreeArgs &a, int x) {
-  if constexpr (SHARED) return shared_job(a, x).rows;
-  else return drafts_of(a, x / a.c.hkv);
-}
-template <int NTQ, bool SHARED>
+template <int NTQ, bool OWN>
 __device__ __forceinline__ Segment segment_at(const TreeArgs &a, const int *pre, int groups, int x, int x1) {
   int lo = 0, hi = groups - 1;
   while (lo < hi) {  // the last group with pre <= x
@@ -284,7 +262,7 @@ __device__ __forceinline__ Segment segment_at(const TreeArgs &a, const int *pre,
     if (pre[mid] <= x) lo = mid;
     else hi = mid - 1;
   }
-  const int len = rows_of<SHARED>(a, lo).len;
+  const int len = drafts_of(a, lo / a.c.hkv).len;
   const int tiles = (len * a.group + kRows * NTQ - 1) / (kRows * NTQ);
   const int per = (pre[lo + 1] - pre[lo]) / tiles;
   Segment s;
@@ -297,7 +275,7 @@ __device__ __forceinline__ Segment segment_at(const TreeArgs &a, const int *pre,
   return s;
 }
 
-template <int D, int FMT, bool PAIR, bool SHARED>
+template <int D, int FMT, bool PAIR, bool OWN>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const TreeArgs a, float *part_o, float *part_ml, float *lane_o, TreeRun *runs, const SharedOut so) {
@@ -330,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x, G = a.group, groups = (SHARED ? a.groups + a.batch : a.batch) * a.c.hkv;
+  const int cta = blockIdx.x, G = a.group, groups = a.batch * a.c.hkv;
 
   if (tid == 0) {
     for (int x = 0; x < C::NBARS; ++x) {
@@ -361,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g0 = min(groups, tid * each), g1 = min(groups, g0 + each);
     int local = 0;
     for (int x = g0; x < g1; ++x) {
-      const GroupPlan p = plan_of<C::NTQ, SHARED>(a, x);
+      const GroupPlan p = plan_of<C::NTQ, OWN>(a, x);
       pre[x] = p.per * p.tiles;
       local += pre[x];
     }
@@ -392,12 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_all = pre[groups];
   const int W = (n_all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int x0 = min(n_all, cta * W), x1 = min(n_all, x0 + W);
-  if constexpr (SHARED) {  // the plan, for the combine
+  if constexpr (OWN) {  // the plan, for the combine
+    launch_next();      // the kernel over the shared pages takes the SMs as they fall free
     if (cta == 0)
       for (int x = tid; x <= groups; x += kThreads) so.plan[x] = pre[x];
   } else if (tid == 0) {  // the run's first row tile, for the combine
     if (x0 < x1) {
-      const Segment s = segment_at<C::NTQ, SHARED>(a, pre, groups, x0, x1);
+      const Segment s = segment_at<C::NTQ, OWN>(a, pre, groups, x0, x1);
       const Drafts dr = drafts_of(a, s.grp / a.c.hkv);
       runs[cta] = TreeRun{s.grp, s.rt, s.rs, s.re, W, dr.start, dr.len, 0};
     } else {
@@ -474,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return k == 0 || wait_parked(bar(C::B_OE + t), (k - 1) & 1, ctl);
       };
       for (int x = x0; ok && x < x1;) {
-        const Segment s = segment_at<C::NTQ, SHARED>(a, pre, groups, x, x1);
+        const Segment s = segment_at<C::NTQ, OWN>(a, pre, groups, x, x1);
         x += s.units;
         if (!(ok = wait_parked(bar(C::B_QF), n_seg & 1, ctl))) break;
         if (!PAIR && !(ok = wait_parked(bar(C::B_QF + 1), n_seg & 1, ctl))) break;
@@ -551,34 +530,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             else hi = mid - 1;
           }
           // three rounds of memory: these three together, the list's entries, the table's
-          int b = lo / a.c.hkv, n, new_keys, first_page = 0;
-          const int listed = SHARED || a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + lo);
-          if constexpr (SHARED) {
-            const SharedJob job = shared_job(a, lo);
-            b = job.seq;
-            n = job.keys;
-            new_keys = job.draft_keys;
-            first_page = job.first_page;
-          } else {
-            n = cached_of(a, b);
-            new_keys = drafts_of(a, b).len;
+          const int b = lo / a.c.hkv;
+          const int listed = OWN || a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + lo);
+          int n = 0, first_page = 0;
+          if constexpr (!OWN) n = cached_of(a, b);
+          const Drafts dr = drafts_of(a, b);
+          if constexpr (OWN) {
+            const OwnKeys own = own_keys(a, b, dr.len);
+            n = own.n;
+            first_page = own.first;
           }
           const int pages = (n + a.c.page - 1) >> a.c.page_shift;
           const int cpp = a.c.page / kChunk, kept = max(0, min(listed, pages));
           const int chunks = listed == INT32_MAX ? (n + kChunk - 1) / kChunk : kept * cpp;
-          const int cu = (chunks + 1) / 2, per = cu + (new_keys + kUnit - 1) / kUnit;
+          const int cu = (chunks + 1) / 2, per = cu + (dr.len + kUnit - 1) / kUnit;
           const int rt = (x - pre[lo]) / per, k = x - pre[lo] - rt * per;
           int page[2] = {0, 0}, w[2] = {0, 0};
           const int draft = k >= cu ? 1 : 0;
           if (draft) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[h] = max(0, min(kChunk, new_keys - (k - cu) * kUnit - h * kChunk)) | (k - cu) << 16;
+            for (int h = 0; h < 2; ++h) w[h] = max(0, min(kChunk, dr.len - (k - cu) * kUnit - h * kChunk)) | (k - cu) << 16;
           } else {
             int j[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int e = (2 * k + h) >> (a.c.page_shift - 6);
-              j[h] = e >= kept ? INT32_MAX : SHARED || a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
+              j[h] = e >= kept ? INT32_MAX : OWN || a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -829,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t dstride = static_cast<size_t>(a.c.hkv) * D;
       const int n0 = d1.y & 0xFFFF, n1 = d1.w & 0xFFFF;
       const uint16_t *drafted = kv == 0 ? a.k_new : a.v_new;
-      if (d0.z) drafted += ((static_cast<size_t>(rows_of<SHARED>(a, d0.x).start) + (d1.y >> 16) * kUnit) * a.c.hkv + g) * D;
+      if (d0.z) drafted += ((static_cast<size_t>(drafts_of(a, d0.x / a.c.hkv).start) + (d1.y >> 16) * kUnit) * a.c.hkv + g) * D;
       int ref = 0;
       if constexpr (Q16) {
         ew = ew_next & ew_mask;
@@ -928,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_q = [&](const Segment &s, uint32_t seg) {
       constexpr int LPR = D / 8, R = 32 / LPR, ROWS = PAIR ? 32 : 16;  // lanes of a row, rows of a step, of the warp
       constexpr int U = ROWS / R < 8 ? ROWS / R : 8;                   // steps in flight
-      const Drafts dr = rows_of<SHARED>(a, s.grp);
+      const Drafts dr = drafts_of(a, s.grp / a.c.hkv);
       const int q = lane % LPR, first = PAIR ? t * kRows + sub * 32 : sub * 32 + t * 16, g = s.grp % a.c.hkv;
 #pragma unroll 1
       for (int r = first; r < first + ROWS; r += R * U) {
@@ -968,13 +945,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, mine = 0, n_seg = 0, lane_segs = 0;  // units of the run, of this lane; segments
     Segment s{};
     if (x0 < x1) {
-      s = segment_at<C::NTQ, SHARED>(a, pre, groups, x0, x1);
+      s = segment_at<C::NTQ, OWN>(a, pre, groups, x0, x1);
       load_q(s, 0);
     }
     for (int x = x0; ok && x < x1; ++n_seg) {
-      if (n_seg > 0) s = segment_at<C::NTQ, SHARED>(a, pre, groups, x, x1);
+      if (n_seg > 0) s = segment_at<C::NTQ, OWN>(a, pre, groups, x, x1);
       x += s.units;
-      const Drafts dr = rows_of<SHARED>(a, s.grp);
+      const Drafts dr = drafts_of(a, s.grp / a.c.hkv);
       const int row = (s.rt * C::NTQ + (PAIR ? t : 0)) * kRows + r, tok = row / G;
       const bool live = tok < dr.len;
       float rs = a.scale_log2;
@@ -1123,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (x < x1) {  // the next segment's rows, so that its first products run beside what follows
         if (!PAIR && !(ok = wait_warp(C::B_QE, n_seg & 1))) break;
-        load_q(segment_at<C::NTQ, SHARED>(a, pre, groups, x, x1), n_seg + 1);
+        load_q(segment_at<C::NTQ, OWN>(a, pre, groups, x, x1), n_seg + 1);
       }
 
       // ---- the segment's result of this lane: rows to the output, or a part for the combine
@@ -1199,8 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mm;
         }
       }
-      const size_t row_at = SHARED && s.grp >= a.groups * a.c.hkv ? static_cast<size_t>(a.total) * a.hq : 0;
-      const float inv = SHARED || !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
+      const float inv = OWN || !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
       const size_t out = static_cast<size_t>(dr.start + tok) * a.hq + (s.grp % a.c.hkv) * G + row % G;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1222,9 +1198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (SHARED && whole) {
+        if (OWN && whole) {
           if (live) {
-            float4 *ro = reinterpret_cast<float4 *>(so.row_o + (row_at + out) * D) + c * 8;
+            float4 *ro = reinterpret_cast<float4 *>(so.row_o + (2 * so.rows + out) * D) + c * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ro[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
           }
@@ -1245,8 +1221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             po[(c * 8 + e) * kRows + r] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         }
       }
-      if (SHARED && whole) {
-        if (live) so.row_ml[row_at + out] = make_float2(m, l);
+      if (OWN && whole) {
+        if (live) so.row_ml[4 * so.rows + out] = make_float2(m, l);
       } else if (whole) {
         if (live && a.lse != nullptr) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       } else {

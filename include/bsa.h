@@ -616,8 +616,7 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
  * What is rounded: as stated at bsa_tree_fwd for more than 16 rows.
  *
  * Limits: as bsa_tree_fwd, but max_cached may be any number of pages up to
- * table_stride, and (groups + batch) * hkv <= 6144 instead of batch * hkv.  The
- * device checks what bsa_tree_fwd's does, and: of a cu_group entry that is
+ * table_stride; groups <= 4096.  The device checks what bsa_tree_fwd's does, and: of a cu_group entry that is
  * inconsistent, or a shared_pages entry below 0 or past max_cached, it sets
  * BSA_ERR_INVALID_ARG in *dev_status and the group shares no pages; a sequence of no
  * group, or of such a one, attends to all its pages by itself; one that drafts but holds fewer
