@@ -23,7 +23,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsa.so")
 SOURCES = ["bsa_api.cu", "bsa_mask.cu", "bsa_score.cu", "bsa_token_score.cu", "bsa_attn.cu", "bsa_decode.cu",
            "bsa_select_noalloc.cu", "bsa_selftest.cu", "bsa_rope.cu", "bsa_cache.cu", "bsa_tree.cu", "bsa_tree_mma.cu",
-           "bsa_cache_api.cu", "bsa_shared.cu", "bsa_own.cu", "bsa_pages.cu", "bsa_verify.cu"]
+           "bsa_cache_api.cu", "bsa_shared.cu", "bsa_pages.cu", "bsa_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I" + INCLUDE]

@@ -68,7 +68,7 @@ struct TreeArgs {
 size_t tree_mma_workspace_bytes(const CacheDims &c);
 bsa_status launch_tree_mma(const TreeArgs &a, void *workspace, cudaStream_t stream);
 // Sequences that share pages (bsa_shared.cu).
-size_t shared_workspace_bytes(const CacheDims &c, int groups, int batch, int total, int max_draft, int hq);
+size_t shared_workspace_bytes(const CacheDims &c, int groups, int batch, int total, int hq);
 bsa_status launch_shared(const TreeArgs &a, void *workspace, cudaStream_t stream);
 size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft);
 bsa_status launch_tree(const TreeArgs &a, void *workspace, cudaStream_t stream);

@@ -90,7 +90,7 @@ bsa_status check_shared(const bsa_shared_shape *s, const bsa::CacheDims &c, int 
     return BSA_ERR_UNSUPPORTED;
   // the units of a plan are counted in 32 bits: at most these, of 128 keys and 128 rows
   const long long shared_tiles = static_cast<long long>(s->total_draft) * g / 128 + s->groups;
-  const long long own_tiles = (static_cast<long long>(s->max_draft) * g + 127) / 128 * s->batch;
+  const long long own_tiles = ((static_cast<long long>(s->max_draft) * g + 127) / 128 + 1) * s->batch;
   const long long units = pages * (c.page / 64) + 4;
   if (static_cast<long long>(s->total_draft) * s->hq > INT32_MAX) return BSA_ERR_UNSUPPORTED;
   if (static_cast<double>(shared_tiles + own_tiles) * static_cast<double>(units) * c.hkv > INT32_MAX)
@@ -278,8 +278,7 @@ size_t bsa_shared_workspace_bytes(const bsa_shared_shape *shape, const bsa_cache
   bsa::CacheDims c;
   int group;
   if (check_cache(cache, &c) != BSA_OK || check_shared(shape, c, &group) != BSA_OK) return 0;
-  return bsa::shared_workspace_bytes(c, shape->groups, shape->batch, shape->total_draft, shape->max_draft,
-                                     shape->hq);
+  return bsa::shared_workspace_bytes(c, shape->groups, shape->batch, shape->total_draft, shape->hq);
 }
 
 bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *cache, const int32_t *cu_group,
@@ -299,8 +298,7 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
     return BSA_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || isinf(softmax_scale)) return BSA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 16) ||
-      workspace_bytes < bsa::shared_workspace_bytes(a.c, shape->groups, shape->batch, shape->total_draft, shape->max_draft,
-                                     shape->hq))
+      workspace_bytes < bsa::shared_workspace_bytes(a.c, shape->groups, shape->batch, shape->total_draft, shape->hq))
     return BSA_ERR_WORKSPACE;
   a.cu = cu_draft;
   a.cached = cached;

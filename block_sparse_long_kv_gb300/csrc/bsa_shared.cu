@@ -1,49 +1,276 @@
 // Attention of sequences that share the first pages of their tables, the shared pages read once for all.
 //
-// softmax over the union of two sets of keys splits: with m, l and O the maximum, the sum of 2^(x - m) and the
-// weighted values over each set, the union's are those of the sets brought to the larger maximum and added.  So the
-// rows of all sequences of a group (drafted tokens x heads of a KV group) meet the shared pages together, in
-// shared_kernel; each sequence's rows meet its own keys in the drafted-token kernels, which start first and hand over
-// the SMs as they finish; shared_combine_kernel adds the two.
+// The drafted tokens of all sequences of a group times the G heads of a KV group are the query rows; 128 are a tile of
+// tcgen05 MMAs.  The keys of a row tile come in units of 128: the group's shared pages, which all rows see; then, of
+// every sequence that has rows in the tile, the pages it does not share, which its rows alone see; then the tile's
+// drafted tokens, of which a row sees its path.  A unit that few rows see costs as much as another, but needs no
+// switch of rows, whose latencies would be several units long: a step of 32 answers over a prompt of 128K and 350
+// tokens of their own each has 1024 shared units a head, 106 own and one of drafts.
+// (Own keys in a kernel of their own, 16 rows at a time, took 23 us of that step and 36 us of trees of 5 drafts.)
 //
-// shared_kernel.  128 rows are a tile of tcgen05 MMAs, 128 keys a unit.  The units of all (group, KV head, row tile)
-// are laid end to end and cut into equal runs, one per CTA (one CTA per SM); a run crosses from one row tile into the
-// next (segments).  Two lanes of eight softmax warps share the tensor core, so that one lane's exponentials run under
-// the other's MMAs:
+// shared_plan_kernel lays the tiles out; the units of all (tile, KV head) are laid end to end and cut into equal
+// runs, one per CTA (one CTA per SM) of shared_kernel; a run crosses from one tile into the next (segments).
+// shared_combine_kernel merges what several CTAs have of a row.
+//
+// Two lanes of eight softmax warps share the tensor core, so that one lane's exponentials run under the other's MMAs:
 //   PAIR   (more than 128 rows a group)  the lanes hold two row tiles and the same keys
 //   !PAIR  the lanes hold the same rows and take alternate units; both leave their results
-// Two threads share a row, each with the 64 keys of one chunk, which is there as a whole or not at all: shared pages
-// are full.  The issuing order S_0(n), P_1 V(n-1), S_1(n), P_0 V(n) keeps one tile's products under the other's
-// softmax.  P lies over the first half of its own S columns.
-// Warps:  0      looks pages up, publishes segments, issues the copies (bf16: TMA tiles; codes: bulk copies)
+// Two threads share a row, each with the 64 keys of one page chunk.  The issuing order S_0(n), P_1 V(n-1), S_1(n),
+// P_0 V(n) keeps one tile's products under the other's softmax.  P lies over the first half of its own S columns.
+// Warps:  0      looks units up, publishes segments, issues the copies (bf16: TMA tiles; codes: bulk copies)
 //         1      TMEM owner; one thread issues the MMAs
-//         4-19   the softmax lanes
-//         20-23  (8- and 4-bit caches) Q and the codes into f16 tiles
+//         2      (PAIR) passes the arrival of V and the next K on
+//         4-19   the softmax lanes; before they release P of a unit with masked places, (bf16) they clean its V
+//         20-27  (8- and 4-bit caches) Q, then the codes and drafted rows of K (20-23) and V into f16 tiles
 //
 // An 8- or 4-bit cache is computed in f16, with the scales of the drafted-token kernel: with e the exponent of a
 // key's row and kref the largest of the unit, K' = code * 2^(e - kref + SHV) is exact down to e = kref - 21 (E4M3) or
 // kref - 18 (E2M1); 2^(kref - 127 - SHV) joins the logit scale.  V likewise against oref, the largest exponent of the
-// segment so far, O being held in units of 2^(oref - 127 - SHV - SHIFT).  P' = 2^(x - m + SHIFT) with the reference m
-// at most 2^TH below the true maximum, so P' <= 2^15.  Row sums are fp32 from unrounded values.
+// segment so far, O being held in units of 2^(oref - 127 - SHV - SHIFT).  Q rows become f16 after a power of two that
+// brings their largest element to [2^14, 2^15), drafted K and V after one per unit.  P' = 2^(x - m + SHIFT) with the
+// reference m at most 2^TH below the true maximum, so P' <= 2^15.  Row sums are fp32 from unrounded values.
 //
+// Inf and NaN of a value that some rows of the tile do not see would reach them (p = 0, and 0 times them is not 0):
+// they are taken out of the product, and the combine adds them to the rows that see them.
 // Every mbarrier wait is bounded, as in the prefill kernel.
-#include "bsa_tree_mma.cuh"
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "bsa_cache.h"
+#include "bsa_internal.h"
+#include "bsa_mma.cuh"
+#include "bsa_tree.cuh"
+#include "bsa_wait.cuh"
+#include "sm103_ptx.cuh"
 
 namespace bsa {
 namespace {
 
-constexpr int kSoftWarp = 4, kLoadWarp = 20;
+using wait::Ctl;
+using wait::drain_bar;
+using namespace mma;
+
+constexpr int kSms = 152;
+constexpr size_t kMaxSmem = 227 * 1024;  // a CTA may have
+constexpr int kRows = 128, kUnit = 128, kChunk = 64;  // rows of a tile; keys of a unit, of a page chunk
+constexpr int kSoftWarp = 4, kLoadWarp = 20, kLoadWarps = 8;
 constexpr int kSegs = 8;   // segments published ahead
 constexpr int kUnits = 8;  // units whose records are kept
+enum Kind { kShared = 0, kOwn = 1, kDraft = 2 };
+
+// ---------------------------------------------------------------- the plan
+
+// A sequence: its drafts, the keys it does not share and their first page; the place of its rows among its group's
+// tokens and the group's first tile.
+struct alignas(16) SeqRecord {
+  int start, len, keys, first_page, at, tile0, pad0, pad1;
+};
+// A row tile: its tokens, the sequences that have rows in it, its units over shared pages (and their chunks, and the
+// sequence whose table names them), the first drafted token that its rows see; the first unit (of one KV head), the
+// units and those over own keys.
+struct alignas(16) TileRecord {
+  int tok0, tokens, seq_a, seq_b, shared, chunks, table, draft0, first, units, own, pad;
+};
+// What the calls leave in the workspace.  Parts: two per CTA and lane, O as [dimension / 4][128 rows] float4, two
+// halves' (max, sum); row buffers for tiles that one CTA has whole, of lane 0 (PAIR: of both) and 1.
+struct SharedWork {
+  float *part_o, *row_o;
+  float2 *part_ml, *row_ml;
+  size_t rows;
+  SeqRecord *seqs;
+  TileRecord *tiles;
+  int *own_before;    // [batch + 1] units over own keys before a sequence's
+  int *token_start;   // [total] the first token of a token's sequence
+  int *totals;        // units of one KV head, tiles, whether a drafted value held Inf or NaN
+  uint32_t *odd;      // [batch * hkv][13] whether own values held Inf or NaN, and where: +Inf, -Inf, NaN, a bit per dimension
+  int max_tiles;
+};
+constexpr int kOdd = 13;
+
+// Places that a row tile and KV head takes in the plan beyond its units, and the places of a CTA's run.
+constexpr int kPad = 2;
+__device__ __forceinline__ int run_places(int units, int tiles) { return (units + kPad * tiles + kSms - 1) / kSms; }
+
+__device__ __forceinline__ void report_arg(const TreeArgs &a) {
+  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
+}
+
+// The sum of the values of the threads before this one; *total the whole sum.  `warps`: [33] of shared memory.
+__device__ __forceinline__ int scan_block(int value, int *warps, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = value;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  __syncthreads();  // the last sums have been read
+  if (lane == 31) warps[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = lane < (blockDim.x >> 5) ? warps[lane] : 0;
+    int run = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    warps[lane] = run - w;
+    if (lane == 31) warps[32] = run;
+  }
+  __syncthreads();
+  *total = warps[32];
+  return warps[warp] + inc - value;
+}
+
+// The last of the indexes lo .. hi - 1 whose value (ascending) is at most x; lo if none is.
+template <typename Value>
+__device__ __forceinline__ int last_at_most(int lo, int hi, int x, Value value) {
+  --hi;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (value(mid) <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// One CTA; offsets, lengths and sums stay in shared memory, so that the caller's arrays are read in one round.
+__global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, const SharedWork w, int tile_rows) {
+  extern __shared__ int sm[];
+  int *cu = sm, *own_before = cu + a.batch + 1, *cu_group = own_before + a.batch + 1;  // [batch + 1] twice, [groups + 1]
+  int *pages_of = cu_group + a.groups + 1, *tile_of = pages_of + a.groups;             // [groups], [groups + 1]
+  int4 *group = reinterpret_cast<int4 *>(tile_of + a.groups + 1 + (4 - (2 * a.batch + 3 * a.groups + 4) % 4) % 4);  // [groups]
+  __shared__ int warps[33];
+  const int threads = blockDim.x, tid = threadIdx.x, G = a.group, tile_tokens = tile_rows / G;
+  launch_next();
+  for (int b = tid; b <= a.batch; b += threads) cu[b] = __ldg(a.cu + b);
+  for (int y = tid; y <= a.groups; y += threads) cu_group[y] = __ldg(a.cu_group + y);
+  for (int y = tid; y < a.groups; y += threads) {
+    int p = __ldg(a.shared_pages + y);
+    if (p < 0 || p > a.max_cached >> a.c.page_shift) {
+      report_arg(a);
+      p = 0;
+    }
+    pages_of[y] = p;
+  }
+  int n_first = tid < a.batch ? cached_of(a, tid) : 0;  // (in the same round)
+  for (int x = tid; x < a.batch * a.c.hkv * kOdd; x += threads) w.odd[x] = 0u;
+  __syncthreads();
+  // groups that do not divide the batch up: nothing is computed
+  bool bad = false;
+  for (int y = tid; y < a.groups; y += threads)
+    bad |= cu_group[y + 1] < cu_group[y] || (y == 0 && cu_group[y] != 0) || (y == a.groups - 1 && cu_group[y + 1] != a.batch);
+  bad = __syncthreads_or(bad) != 0;
+  if (bad && tid == 0) report_arg(a);
+
+  // groups
+  int carry = 0;
+  for (int base = 0; base < a.groups; base += threads) {
+    const int y = base + tid;
+    int tiles = 0;
+    int4 rec = make_int4(0, 0, 0, 0);  // first tile, first token, tokens, the sequence whose table counts
+    if (y < a.groups && !bad) {
+      const int first = cu_group[y], last = cu_group[y + 1], start = cu[first], end = cu[last];
+      if (first < last && start >= 0 && end >= start && end <= a.total) {  // (otherwise its sequences report it)
+        int b = first;
+        while (b + 1 < last && cu[b + 1] == start) ++b;
+        rec = make_int4(0, start, end - start, b);
+        tiles = (rec.z + tile_tokens - 1) / tile_tokens;
+      }
+    }
+    int total;
+    rec.x = carry + scan_block(tiles, warps, &total);
+    if (y < a.groups) {
+      group[y] = rec;
+      tile_of[y] = rec.x;
+    }
+    carry += total;
+  }
+  const int tiles = min(carry, w.max_tiles);
+  __syncthreads();
+
+  // sequences
+  carry = 0;
+  for (int base = 0; base < a.batch; base += threads) {
+    const int b = base + tid;
+    int units = 0;
+    if (b < a.batch) {
+      SeqRecord r{0, 0, 0, 0, 0, 0, 0, 0};
+      const int n = base == 0 ? n_first : cached_of(a, b);
+      if (!bad) {
+        const int y = last_at_most(0, a.groups, b, [&](int x) { return cu_group[x]; });
+        const int4 g = group[y];
+        const Drafts dr = drafts_of(a, b);
+        r.start = dr.start;
+        r.len = dr.len;
+        r.first_page = pages_of[y];
+        r.at = r.start - g.y;
+        r.tile0 = g.x;
+        if (r.at < 0 || r.at + r.len > g.z) r.len = 0;  // (offsets that do not ascend)
+        r.keys = n - (r.first_page << a.c.page_shift);
+        if (r.keys < 0) {  // its table does not hold the group's pages
+          if (r.len > 0) report_arg(a);
+          r.keys = 0;
+        }
+        if (r.len > 0) units = ((r.keys + kChunk - 1) / kChunk + 1) / 2;
+        for (int t = 0; t < r.len; ++t) w.token_start[r.start + t] = r.start;
+      }
+      w.seqs[b] = r;
+    }
+    int total;
+    const int before = carry + scan_block(units, warps, &total);
+    if (b < a.batch) own_before[b] = w.own_before[b] = before;
+    carry += total;
+  }
+  if (tid == 0) own_before[a.batch] = w.own_before[a.batch] = carry;
+  __syncthreads();
+
+  // row tiles
+  carry = 0;
+  for (int base = 0; base < tiles; base += threads) {
+    const int e = base + tid;
+    TileRecord r{};
+    if (e < tiles) {
+      const int y = last_at_most(0, a.groups, e, [&](int x) { return tile_of[x]; });
+      const int4 g = group[y];
+      r.tok0 = g.y + (e - g.x) * tile_tokens;
+      r.tokens = max(0, min(tile_tokens, g.y + g.z - r.tok0));
+      auto start_of = [&](int b) { return cu[b]; };
+      r.seq_a = last_at_most(cu_group[y], cu_group[y + 1], r.tok0, start_of);
+      r.seq_b = last_at_most(r.seq_a, cu_group[y + 1], r.tok0 + r.tokens - 1, start_of) + 1;
+      r.chunks = pages_of[y] << (a.c.page_shift - 6);
+      r.shared = (r.chunks + 1) / 2;
+      r.table = g.w;
+      r.draft0 = max(0, min(r.tok0, cu[r.seq_a]));
+      r.own = own_before[r.seq_b] - own_before[r.seq_a];
+      r.units = r.shared + r.own + (r.tok0 + r.tokens - r.draft0 + kUnit - 1) / kUnit;
+    }
+    int total;
+    r.first = carry + scan_block(r.units, warps, &total);
+    if (e < tiles) w.tiles[e] = r;
+    carry += total;
+  }
+  if (tid == 0) {
+    w.totals[0] = carry;
+    w.totals[1] = tiles;
+    w.totals[2] = 0;
+  }
+}
+size_t plan_smem(int batch, int groups) { return (2 * static_cast<size_t>(batch) + 3 * groups + 7) * 4 + groups * sizeof(int4); }
+
+// ---------------------------------------------------------------- the attention
 
 template <int D, int FMT, bool PAIR>
 struct Shared {
   static constexpr bool Q16 = FMT != BSA_CACHE_BF16;
   static constexpr int RB = FMT == BSA_CACHE_BF16 ? 2 * D : FMT == BSA_CACHE_E4M3 ? D : D / 2;
-  static constexpr int THREADS = Q16 ? 768 : 640;
-  static constexpr int LAUNCH_REGS = Q16 ? 80 : 96;
-  static constexpr int REG_LOW = Q16 ? 40 : 56, REG_SOFT = Q16 ? 88 : 104, REG_LOAD = 88;
-  static_assert(128 * REG_LOW + 512 * REG_SOFT + (Q16 ? 128 * REG_LOAD : 0) <= THREADS * LAUNCH_REGS, "register split");
+  static constexpr int THREADS = Q16 ? 896 : 640;
+  static constexpr int LAUNCH_REGS = Q16 ? 72 : 96;
+  static constexpr int REG_LOW = 56, REG_SOFT = Q16 ? 80 : 104, REG_LOAD = 64;
+  static_assert(128 * REG_LOW + 512 * REG_SOFT + (Q16 ? 256 * REG_LOAD : 0) <= THREADS * LAUNCH_REGS, "register split");
   static constexpr int SHV = FMT == BSA_CACHE_E4M3 ? 6 : 4;  // 448 * 2^6 and 2688 * 2^4 stay below 2^16
   static constexpr int TH = Q16 ? 4 : 8;                     // log2 of how far the reference may lag the maximum
   static constexpr int SHIFT = Q16 ? 15 - TH : 0;
@@ -57,16 +284,20 @@ struct Shared {
   static constexpr uint32_t EXPS = CODES, GROUPS = EXPS + 128;    // of a stage: codes, row exponents, group scales
   static constexpr uint32_t STAGE = Q16 ? GROUPS + (FMT == BSA_CACHE_E2M1 ? 128u * (D / 16) : 0) : 0;
   static constexpr uint32_t OFF_Q = 0, OFF_T = NTQ * TILE, OFF_G = OFF_T + NS * TILE, OFF_BAR = OFF_G + NG * STAGE;
-  static constexpr int B_QF = 0, B_QE = 1, B_F = 2, B_E = B_F + NS, B_GF = B_E + NS, B_GE = B_GF + NG, B_SF = B_GE + NG,
-                       B_PR = B_SF + 2, B_OD = B_PR + 4, B_OE = B_OD + 2, B_IN = B_OE + 2, B_IK = B_IN + kUnits,
-                       B_SG = B_IK + (Q16 ? kUnits : 0), B_SE = B_SG + kSegs, B_RS = B_SE + kSegs,
+  // Q there; K, V of a unit there; V of a unit read (!PAIR); staged codes there, read; S there; P there; O done, read;
+  // unit records; K's scale, V's; segment published, done; row scales; last MMA
+  static constexpr int B_QF = 0, B_FK = 1, B_FV = B_FK + 4, B_EV = B_FV + 4, B_GF = B_EV + 4, B_GE = B_GF + NG,
+                       B_SF = B_GE + NG, B_PR = B_SF + 4, B_OD = B_PR + 2, B_OE = B_OD + 2, B_IN = B_OE + 2,
+                       B_IK = B_IN + kUnits, B_IV = B_IK + (Q16 ? kUnits : 0), B_SG = B_IV + (Q16 ? kUnits : 0), B_SE = B_SG + kSegs, B_RS = B_SE + kSegs,
                        B_FIN = B_RS + (Q16 ? 2 : 0), NBARS = B_FIN + 1;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + (NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag, run
-  static constexpr uint32_t OFF_SEG = OFF_MISC + 32;                          // [kSegs] two int4
-  static constexpr uint32_t OFF_INFO = OFF_SEG + kSegs * 32;                  // [kUnits] chunks there; K's scale; oref
-  static constexpr uint32_t OFF_RED = OFF_INFO + kUnits * 12;                 // [2][2][128] halves' maxima, bf16
+  static constexpr uint32_t OFF_MISC = OFF_BAR + (NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
+  static constexpr uint32_t OFF_SEG = OFF_MISC + 16;                          // [kSegs] two int4
+  static constexpr uint32_t OFF_INFO = OFF_SEG + kSegs * 32;                  // [kUnits] int4
+  static constexpr uint32_t OFF_SCALE = OFF_INFO + kUnits * 16;                          // [kUnits] K's scale; oref
+  static constexpr uint32_t OFF_RED = OFF_SCALE + (Q16 ? kUnits * 8 : 0);     // [2][2][128] halves' maxima, bf16
   static constexpr uint32_t OFF_ROWS = OFF_RED + 1024;                        // [2][NTQ * 128] row scales of Q
-  static constexpr uint32_t SMEM = OFF_ROWS + (Q16 ? 2 * NTQ * 128 * 4 : 0) + 1024;
+  static constexpr uint32_t OFF_FACTORS = OFF_ROWS + (Q16 ? 2 * NTQ * 128 * 4 : 0);  // [loader warps][128] f16 pairs
+  static constexpr uint32_t SMEM = OFF_FACTORS + (Q16 ? kLoadWarps * 128 * 4 : 0) + 1024;
   static_assert(SMEM <= kMaxSmem, "shared memory");
   static constexpr uint32_t F16 = Q16 ? (1u << 7) | (1u << 10) : 0;
   static constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false) & ~F16;
@@ -74,26 +305,77 @@ struct Shared {
   static constexpr int TM_O = 256;  // S_0, S_1, O_0, O_1
 };
 
-// The plan of group y over its shared pages: units of one row tile, and row tiles (of one KV head).
-struct SharedPlan {
-  int per, tiles;
-};
-__device__ __forceinline__ SharedPlan shared_plan(const TreeArgs &a, const SharedRows &r, int tile_rows) {
-  const int chunks = r.pages << (a.c.page_shift - 6);
-  return SharedPlan{(chunks + 1) / 2, (r.rows.len * a.group + tile_rows - 1) / tile_rows};
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
 
+// A run's unit, for the warps that compute: {keys of both chunks | kind << 16, own: first and one past the last of the
+// tile's rows that see it | << 16, own: the sequence, drafts: their first token, 0}.
+__device__ __forceinline__ int unit_keys(const int4 &u, int half) { return u.x >> (8 * half) & 0xFF; }
+__device__ __forceinline__ int unit_kind(const int4 &u) { return u.x >> 16; }
+
+// Takes out of a tile of bf16 values what must not reach rows that do not see it: Inf and NaN (p = 0 does for the rest,
+// whatever lies behind the last key).  Of 256 threads `thread` takes every 256th piece of 16 bytes; `odd` gets where they stood (own values), *drafts_odd
+// whether there were any (drafted ones).
+template <int D>
+__device__ __forceinline__ void clean_v(unsigned char *tile, int thread, const int4 &u, uint32_t *odd, int *drafts_odd) {
+  constexpr int N = 128 * D * 2 / 16 / 256;
+  const bool own = unit_kind(u) == kOwn;
+  uint4 *piece = reinterpret_cast<uint4 *>(tile) + thread;  // eight pieces make a row of a swizzle chunk
+  uint32_t lost = 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) finite_bf16x8(piece[256 * i], lost);
+  if (lost == 0u) return;
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) {
+    const uint4 w = piece[256 * i];
+    uint32_t bad = 0u;
+    const uint4 f = finite_bf16x8(w, bad);
+    if (bad == 0u) continue;
+    piece[256 * i] = f;
+    const int row = (thread >> 3) + 32 * (i & 3);
+    if (own && (row & 63) >= unit_keys(u, row >> 6)) continue;  // behind the last key: nobody's
+    if (!own) {
+      *drafts_odd = 1;
+      continue;
+    }
+    odd[0] = 1u;
+    const int dim = (i >> 2) * 64 + ((thread & 7) ^ (thread >> 3 & 7)) * 8;
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    for (int d = 0; d < 8; ++d) {
+      const uint32_t b16 = words[d >> 1] >> (16 * (d & 1)) & 0xFFFFu;
+      if ((b16 & 0x7F80u) != 0x7F80u) continue;
+      const int which = (b16 & 0x7Fu) != 0u ? 2 : b16 >> 15;
+      atomicOr(odd + 1 + which * 4 + (dim + d) / 32, 1u << ((dim + d) & 31));
+    }
+  }
+  ptx::fence_proxy_async_smem();
+}
+
+// The codes among four that are NaN (bit 7 of their bytes); and: marks the dimensions of those in `odd` (.. of +Inf, -Inf,
+// NaN), `each` dimensions a code from `dim` on, and takes them out.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int dim, int each, uint32_t *odd) {
+  const uint32_t bad = nan_codes(w);
+  if (bad == 0u) return w;
+  odd[0] = 1u;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c)
+    if (bad >> (8 * c + 7) & 1u)
+      atomicOr(odd + 9 + (dim + c * each) / 32, ((1u << each) - 1u) << ((dim + c * each) & 31));
+  return w & ~((bad >> 7) * 0xFFu);
+}
+
+// The maps of a bf16 call: q, cached and drafted K and V.
+struct SharedMaps {
+  CUtensorMap q, k, v, kn, vn;
+};
+
 template <int D, int FMT, bool PAIR>
 __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
-    shared_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const TreeArgs a, float *part_o, float2 *part_ml,
-                  const SharedOut so) {
+    shared_kernel(const __grid_constant__ SharedMaps maps, const TreeArgs a, const SharedWork wk) {
   using C = Shared<D, FMT, PAIR>;
   constexpr bool Q16 = C::Q16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -104,14 +386,15 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sb + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sb + C::OFF_MISC + 4);
-  int *run_of = reinterpret_cast<int *>(sb + C::OFF_MISC + 8);  // first unit of the run, the one past its last, group, its first unit
   int4 *seg_rec = reinterpret_cast<int4 *>(sb + C::OFF_SEG);
-  int *info_in = reinterpret_cast<int *>(sb + C::OFF_INFO);
-  float *info_k = reinterpret_cast<float *>(info_in + kUnits);
-  int *info_v = reinterpret_cast<int *>(info_k + kUnits);
+  int4 *unit_rec = reinterpret_cast<int4 *>(sb + C::OFF_INFO);
+  float *scale_k = reinterpret_cast<float *>(sb + C::OFF_SCALE);
+  int *ref_v = reinterpret_cast<int *>(scale_k + kUnits);
   uint16_t *red = reinterpret_cast<uint16_t *>(sb + C::OFF_RED);
   float *row_scale = reinterpret_cast<float *>(sb + C::OFF_ROWS);
+  // waits watch this CTA's own flag only: *status also carries reports about the arguments
   const Ctl ctl{abort_flag, nullptr};
+  // a whole warp waits, and goes on or gives up together
   auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait_parked(bar(i), parity, ctl)) != 0; };
   auto arrive_warp = [&](int i) {
     __syncwarp();
@@ -121,16 +404,17 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, G = a.group;
 
-  if (tid == 32) {
+  if (tid == 0) {
     for (int x = 0; x < C::NBARS; ++x) {
-      // arrivals: 1 of a commit, the producer or a copy's announcement; 4 of the loader warps; 8 of a lane's warps; 16
-      // of both lanes'
+      // arrivals: 1 of a commit, the producer or a copy's announcement; 4 of the loader warps of K or of V; 8 of all of
+      // them or a lane's warps; 16 of both lanes'; P_0 has one more for V and the next K
       uint32_t count = 1;
-      if (Q16 && (x == C::B_QF || (x >= C::B_F && x < C::B_E) || (x >= C::B_GE && x < C::B_SF) ||
-                  (x >= C::B_RS && x < C::B_FIN)))
-        count = 4;
+      if (Q16 && (x == C::B_QF || (x >= C::B_RS && x < C::B_FIN)))
+        count = kLoadWarps;
+      else if (Q16 && ((x >= C::B_FK && x < C::B_EV) || (x >= C::B_GE && x < C::B_SF)))
+        count = kLoadWarps / 2;
       else if ((x >= C::B_PR && x < C::B_OD) || (x >= C::B_OE && x < C::B_IN))
-        count = 8;
+        count = PAIR && x == C::B_PR ? 9 : 8;
       else if (x >= C::B_SE && x < C::B_RS)
         count = 16;
       ptx::mbar_init(bar(x), count);
@@ -140,173 +424,223 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
     ptx::fence_proxy_async_smem();
   }
   if (warp == 1) {
-    __syncwarp();
     ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
     ptx::tmem_relinquish();
-  }
-  if (warp == 0) {
-    // ---- the plan, a lane per group: all units, then where this CTA's run begins
-    auto units_of = [&](int y) {
-      if (y >= a.groups) return 0;
-      const SharedPlan p = shared_plan(a, shared_rows(a, y), C::NTQ * kRows);
-      return p.per * p.tiles * a.c.hkv;
-    };
-    int all = 0, mine = 0, inc = 0;
-    for (int y0 = 0; y0 < a.groups; y0 += 32) {
-      mine = units_of(y0 + lane);
-      inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
-      }
-      if (cta == 0 && y0 + lane < a.groups) so.plan[y0 + lane] = all + inc - mine;
-      all += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (cta == 0 && lane == 0) so.plan[a.groups] = all;
-    const int W = (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-    const int x0 = min(all, cta * W), x1 = min(all, x0 + W);
-    int y = 0, first = 0;
-    if (x0 < x1) {
-      int before = 0;
-      for (int y0 = 0; y0 < a.groups; y0 += 32) {
-        if (a.groups > 32) {
-          mine = units_of(y0 + lane);
-          inc = mine;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += up;
-          }
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, before + inc > x0);
-        if (over != 0) {
-          const int at = __ffs(over) - 1;
-          y = y0 + at;
-          first = before + __shfl_sync(0xffffffffu, inc - mine, at);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-      }
-    }
-    if (lane == 0) {
-      run_of[0] = x0;
-      run_of[1] = x1;
-      run_of[2] = y;
-      run_of[3] = first;
-    }
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int x0 = run_of[0], x1 = run_of[1], nu = x1 - x0;
+  after_previous_kernel();  // the plan
+  launch_next();
+  // This CTA's run.  Runs are cut where the units and kPad places behind every row tile and KV head are laid end to end:
+  // what a tile's drafts and the change of rows cost more than a unit.
+  const int units_all = wk.totals[0] * a.c.hkv, tiles_all = wk.totals[1];
+  const int places = units_all + kPad * tiles_all * a.c.hkv, W = run_places(units_all, tiles_all * a.c.hkv);
+  // the units before a place
+  auto units_before = [&](int place) {
+    if (place >= places) return units_all;
+    int e = 0, hi = tiles_all;  // the last row tile that begins at or before it, 32 looked at at a time
+    while (hi - e > 1) {
+      const int step = (hi - e + 31) / 32, at = e + lane * step;
+      const bool before = at < hi && (wk.tiles[at].first + kPad * at) * a.c.hkv <= place;
+      const int k = __popc(__ballot_sync(0xffffffffu, before));
+      hi = min(hi, e + k * step);
+      e += (k - 1) * step;
+    }
+    const int2 fu = *reinterpret_cast<const int2 *>(&wk.tiles[e].first);
+    const int off = place - (fu.x + kPad * e) * a.c.hkv, g = off / (fu.y + kPad);
+    return fu.x * a.c.hkv + g * fu.y + min(off - g * (fu.y + kPad), fu.y);
+  };
+  const int x0 = tiles_all > 0 ? units_before(cta * W) : 0, x1 = tiles_all > 0 ? units_before(cta * W + W) : 0, nu = x1 - x0;
+
+  // S of unit n (of lane t) is there.  It is also the sign that K of the unit is read, and, where both row tiles take
+  // every unit, V of the unit before: the issuing thread has few cycles for signs of their own.
+  auto s_bar = [&](int t, uint32_t n) { return C::B_SF + (PAIR ? 2 * t + static_cast<int>(n & 1) : static_cast<int>(n & 3)); };
+  auto s_parity = [&](uint32_t n) { return (PAIR ? n >> 1 : n >> 2) & 1; };
+  // The barrier and parity after which tile z may be written (z >= NS; tiles are K and V of the units in turn).
+  auto free_bar = [&](uint32_t z, uint32_t &parity) {
+    const uint32_t before = z - C::NS, m = before >> 1;
+    if (!PAIR && (before & 1) != 0) {
+      parity = (m >> 2) & 1;
+      return C::B_EV + static_cast<int>(m & 3);
+    }
+    const uint32_t n = m + (PAIR ? before & 1 : 0);
+    parity = s_parity(n);
+    return s_bar(1, n);
+  };
+  // The barrier on which tile z is announced (in phase z >> 3).
+  auto full_bar = [&](uint32_t z) { return ((z & 1) == 0 ? C::B_FK : C::B_FV) + static_cast<int>(z >> 1 & 3); };
 
   if (warp < 4) {
     ptx::setmaxnreg_dec<C::REG_LOW>();
     if (warp == 0 && nu > 0) {
       // ================================================================ producer
-      // A segment's record: {units, first token, tokens, KV head}, {row tile, 1 if the CTA has all of the row tile's
-      // units | 2 if it does not begin the run, 0, 0}.
+      // A segment's record: {units, first token, tokens, KV head}, {1 if the CTA has all of the row tile's units | 2 if
+      // it does not begin the run, 0, 0, 0}.
       bool ok = true;
-      int y = run_of[2], first = run_of[3], n = 0, seg = 0;
+      int e = 0, n = 0, seg = 0;
       uint32_t tiles_sent = 0, stages_sent = 0;
-      for (int x = x0; ok && x < x1; ++seg) {
-        SharedRows r = shared_rows(a, y);
-        SharedPlan p = shared_plan(a, r, C::NTQ * kRows);
-        while (x >= first + p.per * p.tiles * a.c.hkv) {  // (the run is not at its end: there is a next group)
-          first += p.per * p.tiles * a.c.hkv;
-          r = shared_rows(a, ++y);
-          p = shared_plan(a, r, C::NTQ * kRows);
+      const int sub_mask = (1 << (a.c.page_shift - 6)) - 1;
+      {  // the last row tile that begins at or before x0, 32 looked at at a time
+        int hi = wk.totals[1];
+        while (hi - e > 1) {
+          const int step = (hi - e + 31) / 32, at = e + lane * step;
+          const bool before = at < hi && wk.tiles[at].first * a.c.hkv <= x0;
+          const int k = __popc(__ballot_sync(0xffffffffu, before));
+          hi = min(hi, e + k * step);
+          e += (k - 1) * step;
         }
-        const int tile = (x - first) / p.per, rs = first + tile * p.per, k0 = x - rs;
-        const int g = tile / p.tiles, rt = tile - g * p.tiles, units = min(rs + p.per, x1) - x;
-        const int32_t *table = a.table + static_cast<size_t>(r.seq) * a.table_stride;
-        const int chunks = r.pages << (a.c.page_shift - 6), sub_mask = (1 << (a.c.page_shift - 6)) - 1;
-        if (seg >= kSegs) ok = wait_warp(C::B_SE + seg % kSegs, (seg / kSegs - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          seg_rec[2 * (seg % kSegs)] = make_int4(units, r.rows.start, r.rows.len, g);
-          seg_rec[2 * (seg % kSegs) + 1] =
-              make_int4(rt, (rs >= x0 && rs + p.per <= x1 ? 1 : 0) | (rs <= x0 ? 0 : 2), 0, 0);
-          ptx::mbar_arrive(bar(C::B_SG + seg % kSegs));
-        }
-        if constexpr (!Q16) {
-          if (lane == 0) {
-            if (seg > 0) ok = wait_parked(bar(C::B_QE), (seg - 1) & 1, ctl);
-            if (ok) {
-              ptx::mbar_arrive_expect_tx(bar(C::B_QF), C::NTQ * C::TILE);
-              for (int t = 0; t < C::NTQ; ++t)
-                for (int c = 0; c < C::NCH; ++c)
-                  tma_load_3d(base + C::OFF_Q + t * C::TILE + c * C::CHUNK, &tm_q, bar(C::B_QF), c * 64, g * G,
-                              r.rows.start + (rt * C::NTQ + t) * (kRows / G));
-            }
+      }
+      // the run's units, 32 at a time, one per lane and a batch ahead
+      struct Unit {
+        int p0, p1, sub, keys, rows, what;  // pages of both chunks (-1: none); the record's fields
+        int tok0, tokens, g, k, left;       // the tile's tokens; KV head; the unit's place, and how many there are from it on
+      };
+      auto look_up = [&](int i) {
+        Unit u{-1, -1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        const bool in = i < nu;
+        const int x = x0 + min(i, nu - 1);
+        const int e0 = e;
+        TileRecord tr = wk.tiles[e];
+        while (x >= (tr.first + tr.units) * a.c.hkv) tr = wk.tiles[++e];
+        const int off = x - tr.first * a.c.hkv;
+        u.g = off / tr.units;
+        u.k = off - u.g * tr.units;
+        u.left = tr.units - u.k;
+        u.tok0 = tr.tok0;
+        u.tokens = tr.tokens;
+        const int own = u.k - tr.shared, seqs = tr.seq_b - tr.seq_a, own0 = wk.own_before[tr.seq_a];
+        const bool is_own = own >= 0 && own < tr.own;
+        // the sequence of an own unit: in one tile of few sequences a lane holds each one's units before it
+        int b = tr.seq_a;
+        if (__all_sync(0xffffffffu, e == e0 && seqs <= 32)) {
+          const int before = wk.own_before[min(tr.seq_a + lane, tr.seq_b)] - own0;
+          int at = 0;
+#pragma unroll 1
+          for (int step = 16; step > 0; step >>= 1) {
+            const int there = __shfl_sync(0xffffffffu, before, min(at + step, 31));
+            if (at + step < seqs && there <= own) at += step;
           }
+          b += at;
+        } else if (is_own) {
+          b = last_at_most(tr.seq_a, tr.seq_b, own + own0, [&](int j) { return __ldg(wk.own_before + j); });
+        }
+        int seq = tr.table, c = 2 * u.k, first_page = 0;
+        if (own < 0) {
+          u.keys = kChunk | (c + 1 < tr.chunks ? kChunk << 8 : 0) | kShared << 16;
+        } else if (is_own) {
+          const SeqRecord r = wk.seqs[b];
+          seq = b;
+          first_page = r.first_page;
+          c = 2 * (own - (wk.own_before[b] - own0));
+          const int n0 = max(0, min(kChunk, r.keys - c * kChunk)), n1 = max(0, min(kChunk, r.keys - (c + 1) * kChunk));
+          u.keys = n0 | n1 << 8 | kOwn << 16;
+          const int t0 = max(r.start, tr.tok0) - tr.tok0, t1 = min(r.start + r.len, tr.tok0 + tr.tokens) - tr.tok0;
+          u.rows = max(0, t0) * G | max(0, t1) * G << 16;
+          u.what = b;
+        } else {
+          u.what = tr.draft0 + (own - tr.own) * kUnit;
+          const int left = tr.tok0 + tr.tokens - u.what;
+          u.keys = max(0, min(kChunk, left)) | max(0, min(kChunk, left - kChunk)) << 8 | kDraft << 16;
+        }
+        if (in && u.keys >> 16 != kDraft) {
+          const int32_t *entry = a.table + static_cast<size_t>(seq) * a.table_stride + first_page + (c >> (a.c.page_shift - 6));
+          u.sub = c & sub_mask;
+          u.p0 = __ldg(entry);
+          if ((u.keys >> 8 & 0xFF) != 0) u.p1 = sub_mask == 0 ? __ldg(entry + 1) : u.p0;
+        }
+        e = __shfl_sync(0xffffffffu, e, 31);
+        return u;
+      };
+      // entries that name no page: their chunk has no keys
+      auto checked = [&](Unit &u, bool in) {
+        if (u.keys >> 16 == kDraft) return;
+        const bool bad0 = (u.keys & 0xFF) != 0 && (u.p0 < 0 || u.p0 >= a.c.pages);
+        const bool bad1 = (u.keys >> 8 & 0xFF) != 0 && (u.p1 < 0 || u.p1 >= a.c.pages);
+        if (bad0) u.p0 = -1, u.keys &= ~0xFF;
+        if (bad1) u.p1 = -1, u.keys &= ~0xFF00;
+        if (in && (bad0 || bad1)) report_arg(a);
+      };
+      Unit now = look_up(lane), next{};
+      for (; ok && n < nu; ++n) {
+        if (n % 32 == 0) {
+          if (n > 0) now = next;
+          if (n + 32 < nu) next = look_up(n + 32 + lane);
+          checked(now, n + lane < nu);
+        }
+        const int from = n & 31;
+        const int g = __shfl_sync(0xffffffffu, now.g, from), k = __shfl_sync(0xffffffffu, now.k, from);
+        const bool begins = n == 0 || k == 0;  // a segment
+        const int tok0 = __shfl_sync(0xffffffffu, now.tok0, from);
+        if (begins) {
+          const int tokens = __shfl_sync(0xffffffffu, now.tokens, from);
+          const int left = __shfl_sync(0xffffffffu, now.left, from);
+          if (seg >= kSegs && !(ok = wait_warp(C::B_SE + seg % kSegs, (seg / kSegs - 1) & 1))) break;
+          if (lane == 0) {
+            seg_rec[2 * (seg % kSegs)] = make_int4(min(left, nu - n), tok0, tokens, g);
+            // (it begins the run: nothing lies before it; the CTA has all its units: nor does any of its own)
+            seg_rec[2 * (seg % kSegs) + 1] = make_int4((k == 0 && left <= nu - n ? 1 : 0) | (n == 0 ? 0 : 2), 0, 0, 0);
+            ptx::mbar_arrive(bar(C::B_SG + seg % kSegs));
+          }
+          ++seg;
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           if (!ok) break;
         }
-        // pages of the segment's units, 32 at a time, one per lane and a batch ahead; -1: none
-        auto look_up = [&](int i, int &p0, int &p1) {
-          p0 = p1 = -1;
-          if (i >= units) return;
-          const int c = 2 * (k0 + i);
-          p0 = __ldg(table + (c >> (a.c.page_shift - 6)));
-          if (c + 1 < chunks) p1 = sub_mask == 0 ? __ldg(table + c + 1) : p0;
-        };
-        auto checked = [&](int &p) {
-          if (p < -1 || p >= a.c.pages) p = -2;
-        };
-        int now0, now1, next0, next1;
-        look_up(lane, now0, now1);
-        for (int i = 0; ok && i < units; ++i, ++n) {
-          if (i % 32 == 0) {
-            if (i > 0) now0 = next0, now1 = next1;
-            look_up(i + 32 + lane, next0, next1);
-            // an entry that names no page
-            checked(now0);
-            checked(now1);
-            if (i + lane < units && (now0 < 0 || now1 < -1 || (now1 < 0 && 2 * (k0 + i + lane) + 1 < chunks))) report_arg(a);
-          }
-          const int p0 = __shfl_sync(0xffffffffu, now0, i & 31), p1 = __shfl_sync(0xffffffffu, now1, i & 31);
+        {
+          const int p0 = __shfl_sync(0xffffffffu, now.p0, from), p1 = __shfl_sync(0xffffffffu, now.p1, from);
+          const int keys = __shfl_sync(0xffffffffu, now.keys, from), rows = __shfl_sync(0xffffffffu, now.rows, from);
+          const int what = __shfl_sync(0xffffffffu, now.what, from), sub = __shfl_sync(0xffffffffu, now.sub, from);
           if (lane == 0) {
-            const int sub = (2 * (k0 + i)) & sub_mask;
-            const int there = (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0);
+            const int kind = keys >> 16;
             for (int kv = 0; kv < 2 && ok; ++kv) {
               const uint32_t z = 2u * static_cast<uint32_t>(n) + kv;
               if constexpr (!Q16) {
-                const uint32_t s = z % C::NS, round = z / C::NS;
-                if (round > 0 && !(ok = wait_parked(bar(C::B_E + s), (round - 1) & 1, ctl))) break;
+                const uint32_t s = z % C::NS;
+                uint32_t parity = 0;
+                if (z >= C::NS) {
+                  const int fb = free_bar(z, parity);
+                  if (!(ok = wait_parked(bar(fb), parity, ctl))) break;
+                }
                 if (kv == 0) {
-                  info_in[n % kUnits] = there;
+                  unit_rec[n % kUnits] = make_int4(keys, rows, what, 0);
                   ptx::mbar_arrive(bar(C::B_IN + n % kUnits));
                 }
-                const CUtensorMap *map = kv == 0 ? &tm_k : &tm_v;
-                const uint32_t dst = base + C::OFF_T + s * C::TILE, f = bar(C::B_F + s);
+                const uint32_t dst = base + C::OFF_T + s * C::TILE, f = bar(full_bar(z));
                 ptx::mbar_arrive_expect_tx(f, C::TILE);
-                // a chunk that is not there lies outside the tensor, and comes as zeros
-                const int none = a.c.pages * a.c.hkv;
-                const int row0 = p0 >= 0 ? p0 * a.c.hkv + g : none, row1 = p1 >= 0 ? p1 * a.c.hkv + g : none;
-                if (sub_mask != 0) {
-                  for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, map, f, c * 64, sub * kChunk, row0);
+                if (kind == kDraft) {
+                  const CUtensorMap *map = kv == 0 ? &maps.kn : &maps.vn;
+                  for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, map, f, c * 64, g, what);
                 } else {
+                  const CUtensorMap *map = kv == 0 ? &maps.k : &maps.v;
+                  // a chunk that is not there lies outside the tensor, and comes as zeros
+                  const int none = a.c.pages * a.c.hkv;
+                  const int row0 = p0 >= 0 ? p0 * a.c.hkv + g : none, row1 = p1 >= 0 ? p1 * a.c.hkv + g : none;
                   for (int c = 0; c < C::NCH; ++c) {
-                    tma_load_3d(dst + c * C::CHUNK, map, f, c * 64, 0, row0);
-                    tma_load_3d(dst + c * C::CHUNK + kChunk * 128, map, f, c * 64, 0, row1);
+                    tma_load_3d(dst + c * C::CHUNK, map, f, c * 64, sub * kChunk, row0);
+                    if (sub_mask == 0) tma_load_3d(dst + c * C::CHUNK + kChunk * 128, map, f, c * 64, 0, row1);
                   }
                 }
                 tiles_sent = z + 1;
+                if (kv == 0 && begins) {  // (behind K, which the segment before may wait for)
+                  if (n > 0 && !(ok = wait_parked(bar(s_bar(1, n - 1)), s_parity(n - 1), ctl))) break;  // its last S
+                  ptx::mbar_arrive_expect_tx(bar(C::B_QF), C::NTQ * C::TILE);
+                  for (int t = 0; t < C::NTQ; ++t)
+                    for (int c = 0; c < C::NCH; ++c)
+                      tma_load_3d(base + C::OFF_Q + t * C::TILE + c * C::CHUNK, &maps.q, bar(C::B_QF), c * 64, g * G,
+                                  tok0 + t * (kRows / G));
+                }
               } else {
                 const uint32_t s = z % C::NG, round = z / C::NG;
                 if (round > 0 && !(ok = wait_parked(bar(C::B_GE + s), (round - 1) & 1, ctl))) break;
                 if (kv == 0) {
-                  info_in[n % kUnits] = there;
+                  unit_rec[n % kUnits] = make_int4(keys, rows, what, 0);
                   ptx::mbar_arrive(bar(C::B_IN + n % kUnits));
                 }
                 constexpr int PER = FMT == BSA_CACHE_E4M3 ? 1 : 1 + D / 16;
                 const uint8_t *codes = kv == 0 ? a.k_codes : a.v_codes, *scales = kv == 0 ? a.k_scales : a.v_scales;
                 const uint32_t dst = base + C::OFF_G + s * C::STAGE, f = bar(C::B_GF + s);
-                const uint32_t half = C::STAGE / 2;  // of a chunk
-                ptx::mbar_arrive_expect_tx(f, ((there & 1) + (there >> 1)) * half);
+                ptx::mbar_arrive_expect_tx(f, ((p0 >= 0 ? 1u : 0u) + (p1 >= 0 ? 1u : 0u)) * (C::STAGE / 2));
                 for (int h = 0; h < 2; ++h) {
                   const int pg = h == 0 ? p0 : p1;
                   if (pg < 0) continue;
@@ -324,28 +658,35 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
           }
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
-        x += units;
       }
       if (*abort_flag && lane == 0) {
-        // let copies in flight land before the CTA's shared memory is released
+        // let copies in flight land before the CTA's shared memory is released (a barrier that lacks an arrival never
+        // completes: its wait runs out)
         if constexpr (!Q16) {
           if (seg > 0) drain_bar(bar(C::B_QF), (seg - 1) & 1);
           for (uint32_t z = tiles_sent > C::NS ? tiles_sent - C::NS : 0; z < tiles_sent; ++z)
-            drain_bar(bar(C::B_F + z % C::NS), (z / C::NS) & 1);
+            drain_bar(bar(full_bar(z)), z >> 3 & 1);
         } else {
-          for (uint32_t z = stages_sent > C::NG ? stages_sent - C::NG : 0; z < stages_sent; ++z)
-            drain_bar(bar(C::B_GF + z % (C::NG > 0 ? C::NG : 1)), (z / (C::NG > 0 ? C::NG : 1)) & 1);
+          constexpr uint32_t RING = C::NG > 0 ? C::NG : 1;
+          for (uint32_t z = stages_sent > RING ? stages_sent - RING : 0; z < stages_sent; ++z)
+            drain_bar(bar(C::B_GF + z % RING), (z / RING) & 1);
         }
       }
       __syncwarp();
     } else if (warp == 1 && lane == 0 && nu > 0) {
       // ================================================================ MMA issuer
+      // Its instructions are what the tensor core waits for (a product of 16 keys or dimensions takes 64 cycles, and every
+      // wait, commit or look costs 70 to 150 in which few products are queued), so it has one commit a row tile and
+      // unit, and one wait.
+      auto wait_for = [&](int i, uint32_t parity) { return wait_parked(bar(i), parity, ctl); };
+      // descriptors differ in the address field of the low word alone
       const uint64_t dq0 = ptx::sdesc_sw128(base + C::OFF_Q, 16, 1024);
       const uint64_t dk0 = ptx::sdesc_sw128(base + C::OFF_T, 16, 1024);
       const uint64_t dv0 = ptx::sdesc_sw128(base + C::OFF_T, C::CHUNK, 1024);
-      auto issue_s = [&](int t, uint32_t slot) {
-        const uint64_t dq = dq0 + static_cast<uint64_t>(PAIR ? t : 0) * (C::TILE >> 4);
-        const uint64_t dk = dk0 + static_cast<uint64_t>(slot) * (C::TILE >> 4);
+      constexpr uint32_t TILE16 = C::TILE >> 4;
+      auto issue_s = [&](int t, uint32_t ks, uint32_t n) {  // (ks: K's tile in the ring, in units of 16 bytes)
+        const uint64_t dq = dq0 + (PAIR && t == 1 ? TILE16 : 0);
+        const uint64_t dk = dk0 + ks;
         const uint32_t dst = tmem + t * 128;
         constexpr int NEXT = C::CHUNK >> 4;  // 16 dimensions are 32 bytes, four steps a swizzle chunk
         mma_ss_at<0, 0, true>(dst, dq, dk, C::IDESC_S);
@@ -358,85 +699,80 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
           mma_ss_at<NEXT + 4, NEXT + 4, false>(dst, dq, dk, C::IDESC_S);
           mma_ss_at<NEXT + 6, NEXT + 6, false>(dst, dq, dk, C::IDESC_S);
         }
-        ptx::mma_commit(bar(C::B_SF + t));
+        ptx::mma_commit(bar(s_bar(t, n)));
       };
       uint32_t pv_count[2] = {0, 0}, lane_segs[2] = {0, 0};  // P V products of each lane, segments in which it had a unit
-      auto issue_pv = [&](int t, uint32_t slot, bool accumulate) -> bool {
-        const uint64_t dv = dv0 + static_cast<uint64_t>(slot) * (C::TILE >> 4);
-        const uint32_t dst = tmem + C::TM_O + t * 128, src = tmem + t * 128, parity = pv_count[t]++ & 1;
-        // 32 keys of each half: P of a half lies over the first of its columns
-        if (!wait_parked(bar(C::B_PR + 2 * t), parity, ctl)) return false;
+      // `first`: the lane's first of a segment, which overwrites O: the last segment's must have been read
+      auto issue_pv = [&](int t, uint32_t vs, bool first) -> bool {
+        const uint64_t dv = dv0 + vs;
+        const uint32_t dst = tmem + C::TM_O + t * 128, src = tmem + t * 128;
+        const uint32_t count = t == 0 ? pv_count[0]++ : pv_count[1]++;
+        if (first) {
+          const uint32_t k = t == 0 ? lane_segs[0]++ : lane_segs[1]++;
+          if (k > 0 && !wait_for(C::B_OE + t, (k - 1) & 1)) return false;
+        }
+        if (!wait_for(C::B_PR + t, count & 1)) return false;
         ptx::tc_fence_after();
-        mma_ts_at<0, 0>(dst, src, dv, C::IDESC_O, accumulate ? 1u : 0u);
+        // 16 keys each: P of a half lies over the first of its columns
+        mma_ts_at<0, 0>(dst, src, dv, C::IDESC_O, first ? 0u : 1u);
         mma_ts_at<8, 128>(dst, src, dv, C::IDESC_O, 1u);
-        mma_ts_at<64, 512>(dst, src, dv, C::IDESC_O, 1u);
-        mma_ts_at<72, 640>(dst, src, dv, C::IDESC_O, 1u);
-        if (!wait_parked(bar(C::B_PR + 2 * t + 1), parity, ctl)) return false;
-        ptx::tc_fence_after();
         mma_ts_at<16, 256>(dst, src, dv, C::IDESC_O, 1u);
         mma_ts_at<24, 384>(dst, src, dv, C::IDESC_O, 1u);
+        mma_ts_at<64, 512>(dst, src, dv, C::IDESC_O, 1u);
+        mma_ts_at<72, 640>(dst, src, dv, C::IDESC_O, 1u);
         mma_ts_at<80, 768>(dst, src, dv, C::IDESC_O, 1u);
         mma_ts_at<88, 896>(dst, src, dv, C::IDESC_O, 1u);
         return true;
       };
-      // the lane's first P V of a segment overwrites O: the last segment's must have been read
-      auto o_free = [&](int t) -> bool {
-        const uint32_t k = lane_segs[t]++;
-        return k == 0 || wait_parked(bar(C::B_OE + t), (k - 1) & 1, ctl);
-      };
-      auto tile_there = [&](uint32_t z) -> bool {
-        if (!wait_parked(bar(C::B_F + z % C::NS), (z / C::NS) & 1, ctl)) return false;
-        ptx::tc_fence_after();
-        return true;
-      };
-      bool ok = true;
-      uint32_t n = 0;
-      int seg = 0;
-      for (int x = x0; ok && x < x1; ++seg) {
-        if (!(ok = wait_parked(bar(C::B_SG + seg % kSegs), (seg / kSegs) & 1, ctl))) break;
+      auto tile_there = [&](uint32_t z) { return wait_for(full_bar(z), z >> 3 & 1); };
+      constexpr uint32_t RING16 = C::NS * TILE16;
+      auto next_tile = [](uint32_t at, uint32_t by) { return at + by >= RING16 ? at + by - RING16 : at + by; };
+      uint32_t n = 0, ks = 0, vs = TILE16, v_last = 0;  // tiles of the unit's K and V, and of the last step's V
+      int seg = 0, left = nu;
+      bool ok = !PAIR || tile_there(0);
+      for (; ok && left > 0; ++seg) {
+        if (!(ok = wait_for(C::B_SG + seg % kSegs, (seg / kSegs) & 1))) break;
         const int units = seg_rec[2 * (seg % kSegs)].x;
-        x += units;
-        if (!(ok = wait_parked(bar(C::B_QF), seg & 1, ctl))) break;
+        left -= units;
+        if (!(ok = wait_for(C::B_QF, seg & 1))) break;
         ptx::tc_fence_after();
-        for (int i = 0; i < units; ++i, ++n) {
-          const uint32_t kz = 2 * n, vz = kz + 1;
-          const bool last = i == units - 1;
-          if (!(ok = tile_there(kz))) break;
-          if constexpr (PAIR) {
-            // S_0(n) overwrites what P_0 V(n - 1) reads: MMAs of one thread run in the order of issue
-            issue_s(0, kz % C::NS);
-            if (!(ok = tile_there(vz))) break;
+        // S_t(n) overwrites what P_t V(n - 1) reads: MMAs of one thread run in the order of issue
+        if constexpr (PAIR) {
+          for (int i = 0; i < units; ++i, ++n) {
+            issue_s(0, ks, n);
+            if (i > 0 && !(ok = issue_pv(1, v_last, i == 1))) break;
+            issue_s(1, ks, n);
+            // (P_0's sign says as well that V of this unit and K of the next are there)
+            if (!(ok = issue_pv(0, vs, i == 0))) break;
+            v_last = vs;
+            ks = next_tile(ks, 2 * TILE16);
+            vs = next_tile(vs, 2 * TILE16);
+          }
+          if (!ok) break;
+          ptx::mma_commit(bar(C::B_OD));
+          if (!(ok = issue_pv(1, v_last, units == 1))) break;
+          ptx::mma_commit(bar(C::B_OD + 1));
+        } else {
+#pragma unroll 1
+          for (int i = 0; i <= units; ++i) {  // S of unit i, P V of unit i - 1
+            if (i < units) {
+              if (!(ok = tile_there(2 * n))) break;
+              ptx::tc_fence_after();
+              issue_s(i & 1, ks, n);
+            }
             if (i > 0) {
-              if (i == 1 && !(ok = o_free(1))) break;
-              if (!(ok = issue_pv(1, (vz - 2) % C::NS, i > 1))) break;
-              ptx::mma_commit(bar(C::B_E + (vz - 2) % C::NS));
+              const uint32_t m = n - 1;
+              if (!(ok = tile_there(2 * m + 1))) break;
+              if (!(ok = issue_pv((i - 1) & 1, v_last, i < 3))) break;
+              ptx::mma_commit(bar(C::B_EV + static_cast<int>(m & 3)));
+              if (i >= units - 1) ptx::mma_commit(bar(C::B_OD + ((i - 1) & 1)));
             }
-            issue_s(1, kz % C::NS);
-            if (last) ptx::mma_commit(bar(C::B_QE));
-            ptx::mma_commit(bar(C::B_E + kz % C::NS));
-            if (i == 0 && !(ok = o_free(0))) break;
-            if (!(ok = issue_pv(0, vz % C::NS, i > 0))) break;
-            if (last) {
-              ptx::mma_commit(bar(C::B_OD));
-              if (i == 0 && !(ok = o_free(1))) break;
-              if (!(ok = issue_pv(1, vz % C::NS, i > 0))) break;
-              ptx::mma_commit(bar(C::B_E + vz % C::NS));
-              ptx::mma_commit(bar(C::B_OD + 1));
+            v_last = vs;
+            if (i < units) {
+              ++n;
+              ks = next_tile(ks, 2 * TILE16);
+              vs = next_tile(vs, 2 * TILE16);
             }
-          } else {
-            issue_s(i & 1, kz % C::NS);
-            ptx::mma_commit(bar(C::B_E + kz % C::NS));
-            if (last) ptx::mma_commit(bar(C::B_QE));
-            for (int j = i > 0 ? i - 1 : i; j <= i; ++j) {  // unit i - 1, and the last unit itself
-              if (j == i && !last) break;
-              const uint32_t z = vz - 2 * static_cast<uint32_t>(i - j);
-              const int t = j & 1;
-              if (j < 2 && !(ok = o_free(t))) break;
-              if (!(ok = tile_there(z) && issue_pv(t, z % C::NS, j >= 2))) break;
-              ptx::mma_commit(bar(C::B_E + z % C::NS));
-              if (j + 2 >= units) ptx::mma_commit(bar(C::B_OD + t));
-            }
-            if (!ok) break;
           }
         }
       }
@@ -444,6 +780,14 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         // every MMA issued so far must finish before TMEM is released
         ptx::mma_commit(bar(C::B_FIN));
         drain_bar(bar(C::B_FIN), 0);
+      }
+    } else if (PAIR && warp == 2 && lane == 0) {
+      // ================================================================ V and the next K, as an arrival at P_0
+      for (uint32_t z = 1; z < 2u * static_cast<uint32_t>(nu); z += 2) {
+        if (!wait_parked(bar(full_bar(z)), z >> 3 & 1, ctl)) break;
+        if (z + 1 < 2u * static_cast<uint32_t>(nu) && !wait_parked(bar(full_bar(z + 1)), (z + 1) >> 3 & 1, ctl)) break;
+        ptx::mbar_arrive(bar(C::B_PR));
+        if (!wait_parked(bar(C::B_PR), z >> 1 & 1, ctl)) break;  // (the next arrival belongs to the next phase)
       }
     }
     __syncwarp();
@@ -457,13 +801,13 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
     const uint32_t tO = tmem + lane_off + C::TM_O + t * 128 + hf * (D / 2);
     uint16_t *mine_max = red + (t * 2 + hf) * 128 + r, *other_max = red + (t * 2 + 1 - hf) * 128 + r;
     const int pair_bar = 1 + t * 4 + sub;  // the two warps that share rows
+    const int row = (PAIR ? t : 0) * kRows + r;  // of the tile (or pair of tiles)
     bool ok = true;
-    uint32_t n = 0, mine = 0, lane_segs = 0;  // units of the run, of this lane; its segments
+    uint32_t n = 0, lane_segs = 0;  // units of the run; segments in which this lane had one
     int seg = 0;
     for (int x = x0; ok && x < x1; ++seg) {
       if (!(ok = wait_warp(C::B_SG + seg % kSegs, (seg / kSegs) & 1))) break;
-      const int4 ra = seg_rec[2 * (seg % kSegs)], rb = seg_rec[2 * (seg % kSegs) + 1];
-      const int units = ra.x;
+      const int units = seg_rec[2 * (seg % kSegs)].x;
       x += units;
       float rs = a.scale_log2;
       if constexpr (Q16) {
@@ -472,42 +816,95 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
           rs *= row_scale[((seg & 1) * C::NTQ + (PAIR ? t : 0)) * 128 + r];
         }
       }
+      const int4 rt = seg_rec[2 * (seg % kSegs)];  // (.y: the tile's first token)
+      const int tok = rt.y + row / G, seq_start = row / G < rt.z ? __ldg(wk.token_start + tok) : INT32_MAX;
       float m = -INFINITY, l = 0.f;
       int oref = 0, done = 0;  // O's unit (8- and 4-bit caches); units of this lane in the segment
       for (int i = 0; i < units; ++i, ++n) {
         if (!PAIR && (i & 1) != t) continue;
         if (!(ok = wait_warp(C::B_IN + n % kUnits, (n / kUnits) & 1))) break;
-        const bool there = (info_in[n % kUnits] >> hf & 1) != 0;
+        const int4 u = unit_rec[n % kUnits];
+        // which of the thread's 64 keys the row sees
+        uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
+        bool on = true;  // it sees some
+        const bool whole_chunk = unit_keys(u, hf) == kChunk && unit_kind(u) != kDraft;
+        const bool masked = !whole_chunk;
+        if (whole_chunk) {
+          if (unit_kind(u) == kOwn) on = row >= (u.y & 0xFFFF) && row < u.y >> 16;
+        } else {
+          const int keys = unit_keys(u, hf);
+          int from = 0, to = keys;  // keys from .. to - 1
+          if (unit_kind(u) == kOwn) {
+            if (row < (u.y & 0xFFFF) || row >= u.y >> 16) to = 0;
+          } else if (unit_kind(u) == kDraft) {
+            const int first = u.z + hf * kChunk;
+            to = 0;
+            if (seq_start != INT32_MAX) {
+              if (a.parents == nullptr) {
+                from = max(0, seq_start - first);
+                to = max(0, min(keys, tok - first + 1));
+              } else {
+                see0 = see1 = 0u;
+                for (int p = tok - seq_start; p >= 0 && seq_start + p >= first; p = parent_of(a, seq_start, p)) {
+                  const int k = seq_start + p - first;
+                  if (k < 32) see0 |= 1u << k;
+                  else if (k < 64) see1 |= 1u << (k - 32);
+                }
+                to = -1;
+              }
+            }
+          }
+          if (to >= 0) {  // (bits from .. to - 1 of 64)
+            auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
+            see0 = below(to) & ~below(from);
+            see1 = below(to - 32) & ~below(from - 32);
+          }
+          on = (see0 | see1) != 0u;
+        }
+        const bool any = __any_sync(0xffffffffu, on);  // of the warp's rows
         float scl = rs;
         int oref_new = 0;
         if constexpr (Q16) {
           if (!(ok = wait_warp(C::B_IK + n % kUnits, (n / kUnits) & 1))) break;
-          // never 0, so that logits below it are 0 to any precision and not NaN
-          scl = fmaxf(scl * info_k[n % kUnits], 1e-37f);
-          oref_new = info_v[n % kUnits];
+          if (!(ok = wait_warp(C::B_IV + n % kUnits, (n / kUnits) & 1))) break;
+          // never 0, so that a masked -inf stays one (the logits below it are 0 to any precision)
+          scl = fmaxf(scl * scale_k[n % kUnits], 1e-37f);
+          oref_new = ref_v[n % kUnits];
         }
-        if (!(ok = wait_warp(C::B_SF + t, mine & 1))) break;
+        if (!(ok = wait_warp(s_bar(t, n), s_parity(n)))) break;
         ptx::tc_fence_after();
-        uint32_t sr[Q16 ? 32 : 64];
-        float pm[2];
-        if constexpr (Q16) {  // registers for half of the logits: the second half is read again
-          uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
-          ptx::tmem_ld32_max(tS + 32, s0, pm[1]);
-          ptx::tmem_wait_ld();
-          ptx::tmem_ld32_max(tS, s0, pm[0]);
-        } else {
-          ptx::tmem_ld32_max(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]), pm[0]);
-          ptx::tmem_ld32_max(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[Q16 ? 0 : 32]), pm[1]);
+        uint32_t sr[32];
+        // the row's maximum first; registers for half of the logits, the second half is read again.  (Beside the loaders
+        // of codes the loops stay loops: what 28 warps run has to fit the instruction cache.)
+        constexpr int UNROLL = Q16 ? 1 : 2;
+        float top = -INFINITY;
+        if (any) {
+#pragma unroll UNROLL
+          for (int c = 1; c >= 0; --c) {
+            float mx;
+            ptx::tmem_ld32_max(tS + c * 32, sr, mx);
+            ptx::tmem_wait_ld();
+            if (masked) {
+              const uint32_t see = c == 0 ? see0 : see1;
+              mx = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (!((see >> e) & 1u)) sr[e] = 0xFF800000u;
+                mx = fmaxf(mx, __uint_as_float(sr[e]));
+              }
+            }
+            top = fmaxf(top, mx);
+          }
+          if (!on) top = -INFINITY;
         }
-        ptx::tmem_wait_ld();
-        // the row's maximum of both halves: each half's rounded up to bf16 (any upper bound is a valid reference, and
+        // the maximum of both halves: each half's rounded up to bf16 (any upper bound is a valid reference, and
         // both halves then hold the same value).  The slot is written again only after the partner has released P,
         // which the lane's next S waits for.
-        uint32_t u = there ? __float_as_uint(fmaxf(pm[0], pm[1])) : 0xFF800000u;
-        if ((u & 0xFFFFu) != 0u && !(u >> 31)) u += 0x10000u;
-        *mine_max = static_cast<uint16_t>(u >> 16);
+        uint32_t up = __float_as_uint(top);
+        if ((up & 0xFFFFu) != 0u && !(up >> 31)) up += 0x10000u;
+        *mine_max = static_cast<uint16_t>(up >> 16);
         ptx::named_barrier(pair_bar, 64);
-        const float mx = fmaxf(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(static_cast<uint32_t>(*other_max) << 16));
+        const float mx = fmaxf(__uint_as_float(up & 0xFFFF0000u), __uint_as_float(static_cast<uint32_t>(*other_max) << 16));
         const float mt = mx == -INFINITY ? -INFINITY : mx * scl;
         // O moves to a new reference or a larger unit only when it has to
         float factor = 1.f;
@@ -523,51 +920,68 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
           }
         }
         const bool resc = done > 0 && of != 1.f;
-        const float mb = m == -INFINITY ? 0.f : m;
-        // a chunk that is not there: p = 0 whatever its columns hold
-        const float bias = there ? static_cast<float>(C::SHIFT) - mb : -INFINITY;
+        const float bias = static_cast<float>(C::SHIFT) - (m == -INFINITY ? 0.f : m);
         uint64_t acc[2] = {0ull, 0ull};
-        const uint64_t scl2 = there ? ptx::f32x2(scl, scl) : 0ull, bias2 = ptx::f32x2(bias, bias);
-#pragma unroll
+        const uint64_t scl2 = ptx::f32x2(scl, scl), bias2 = ptx::f32x2(bias, bias);
+#pragma unroll UNROLL
         for (int c = 0; c < 2; ++c) {
-          constexpr int STEP = Q16 ? 0 : 32;
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t y = ptx::fma_f32x2(
-                ptx::f32x2(__uint_as_float(sr[c * STEP + 2 * e]), __uint_as_float(sr[c * STEP + 2 * e + 1])), scl2, bias2);
-            float y0, y1;
-            ptx::f32x2_split(y, y0, y1);
-            const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
-            acc[e & 1] = ptx::add_f32x2(acc[e & 1], ptx::f32x2(p0, p1));
-            pk[e] = Q16 ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
-          }
-          ptx::tmem_st16(tS + c * 16, pk);
-          if (c == 0) {
-            if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                uint32_t ov[8];
-                ptx::tmem_ld8(tO + q * 8, ov);
-                ptx::tmem_wait_ld();
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          if (any) {
+            if (c == 1) {
+              ptx::tmem_ld32(tS + 32, sr);
+              ptx::tmem_wait_ld();
+              if (masked) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * of);
-                ptx::tmem_st8(tO + q * 8, ov);
+                for (int e = 0; e < 32; ++e)
+                  if (!((see1 >> e) & 1u)) sr[e] = 0xFF800000u;
               }
             }
-            if constexpr (Q16) ptx::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t y =
+                  ptx::fma_f32x2(ptx::f32x2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scl2, bias2);
+              float y0, y1;
+              ptx::f32x2_split(y, y0, y1);
+              const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
+              acc[e & 1] = ptx::add_f32x2(acc[e & 1], ptx::f32x2(p0, p1));
+              pk[e] = Q16 ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
+            }
+            if (!on) {  // (whatever the logits of another sequence's keys are)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            }
           }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          arrive_warp(C::B_PR + 2 * t + c);
-          if (Q16 && c == 0) ptx::tmem_wait_ld();
+          ptx::tmem_st16(tS + c * 16, pk);
+          if (c == 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t ov[8];
+              ptx::tmem_ld8(tO + q * 8, ov);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * of);
+              ptx::tmem_st8(tO + q * 8, ov);
+            }
+          }
         }
+        if constexpr (!Q16) {
+          // V of a unit with masked places: Inf and NaN become 0.  (By the first lane to use it.)
+          if (unit_kind(u) != kShared && (!PAIR || t == 0)) {
+            if (!(ok = wait_warp(full_bar(2 * n + 1), (n >> 2) & 1))) break;
+            clean_v<D>(sb + C::OFF_T + (2 * n + 1) % C::NS * C::TILE, ((warp - kSoftWarp) & 7) * 32 + lane, u,
+                       wk.odd + (static_cast<size_t>(u.z) * a.c.hkv + seg_rec[2 * (seg % kSegs)].w) * kOdd, wk.totals + 2);
+          }
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        arrive_warp(C::B_PR + t);
         float s4[4];
         ptx::f32x2_split(acc[0], s4[0], s4[1]);
         ptx::f32x2_split(acc[1], s4[2], s4[3]);
         constexpr float unshift = 1.f / (1 << C::SHIFT);
-        l = fmaf((s4[0] + s4[1]) + (s4[2] + s4[3]), unshift, l * factor);
-        ++mine;
+        l = fmaf(on ? (s4[0] + s4[1]) + (s4[2] + s4[3]) : 0.f, unshift, l * factor);
         ++done;
       }
       if (!ok) break;
@@ -579,63 +993,70 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         ++lane_segs;
       }
       m = ptx::part_max(m, l);
-      const bool whole = (rb.y & 1) != 0;
-      const int row = (rb.x * C::NTQ + (PAIR ? t : 0)) * kRows + r, tok = row / G;
-      const size_t out = static_cast<size_t>(ra.y + tok) * a.hq + ra.w * G + row % G;
-      const size_t slot = 2 * (2 * static_cast<size_t>(cta) + (rb.y >> 1)) + t;
-      const bool live = tok < ra.z;
+      const int4 ra = seg_rec[2 * (seg % kSegs)], rb = seg_rec[2 * (seg % kSegs) + 1];  // (their place is taken after B_SE)
+      const bool whole = (rb.x & 1) != 0, live = row / G < ra.z;
+      const size_t out = static_cast<size_t>(ra.y + row / G) * a.hq + ra.w * G + row % G;
+      const size_t slot = 2 * (2 * static_cast<size_t>(cta) + (rb.x >> 1)) + t;
       float unit_f = 1.f;
       if constexpr (Q16) unit_f = exp2f(static_cast<float>(oref - 127 - C::SHV - C::SHIFT));
       if (done > 0) {
-        float4 *po = reinterpret_cast<float4 *>(part_o) + (slot * (D / 4) + hf * (D / 8)) * kRows + r;
-        float4 *ro = reinterpret_cast<float4 *>(so.row_o + ((PAIR ? 0 : t) * so.rows + out) * D) + hf * (D / 8);
+        float4 *po = reinterpret_cast<float4 *>(wk.part_o) + (slot * (D / 4) + hf * (D / 8)) * kRows + r;
+        float4 *ro = reinterpret_cast<float4 *>(wk.row_o + ((PAIR ? 0 : t) * wk.rows + out) * D) + hf * (D / 8);
 #pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
-          uint32_t ov[8];
-          ptx::tmem_ld8(tO + q * 8, ov);
+        for (int q = 0; q < D / 64; ++q) {
+          uint32_t ov[32];
+          ptx::tmem_ld32(tO + q * 32, ov);
           ptx::tmem_wait_ld();
+          if (q == D / 64 - 1) {  // O may be overwritten
+            ptx::tc_fence_before();
+            arrive_warp(C::B_OE + t);
+          }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < 8; ++e) {
             const float4 v = make_float4(__uint_as_float(ov[4 * e]) * unit_f, __uint_as_float(ov[4 * e + 1]) * unit_f,
                                          __uint_as_float(ov[4 * e + 2]) * unit_f, __uint_as_float(ov[4 * e + 3]) * unit_f);
-            if (!whole) po[(2 * q + e) * kRows] = v;
-            else if (live) ro[2 * q + e] = v;
+            if (!whole) po[(8 * q + e) * kRows] = v;
+            else if (live) ro[8 * q + e] = v;
           }
         }
       }
-      if (!whole) part_ml[(slot * 2 + hf) * kRows + r] = make_float2(m, l);
-      else if (live) so.row_ml[((PAIR ? 0 : t) * 2 + hf) * so.rows + out] = make_float2(m, l);
-      ptx::tc_fence_before();
-      if (done > 0) arrive_warp(C::B_OE + t);
+      if (!whole) wk.part_ml[(slot * 2 + hf) * kRows + r] = make_float2(m, l);
+      else if (live) wk.row_ml[((PAIR ? 0 : t) * 2 + hf) * wk.rows + out] = make_float2(m, l);
       arrive_warp(C::B_SE + seg % kSegs);
     }
   } else if constexpr (Q16) {
     // ================================================================ loaders
-    ptx::setmaxnreg_inc<C::REG_LOAD>();
+    ptx::setmaxnreg_dec<C::REG_LOAD>();
     const int lt = tid - kLoadWarp * 32;
-    constexpr int PP = C::RB / 16, STEP = 128 / PP;  // pieces of a code row; a thread's rows are STEP apart
-    const int p = lt % PP, r0 = lt / PP;
+    // four warps for K, four for V; a thread takes pieces of 16 bytes of rows STEP apart
+    constexpr int PP = C::RB / 16, ST = kLoadWarps * 16, STEP = ST / PP, LT = 2 * ST;
+    const int kv = lt / ST, st = lt % ST;
+    // Eight lanes read and write eight different banks: with eight pieces a row they take four of one row and the other
+    // four of the next (whose units stand in the other order).
+    const int p = PP == 8 ? (st & 3) | ((st >> 2 ^ st >> 3) & 1) << 2 : st % PP;
+    const int r0 = PP == 8 ? st >> 4 << 1 | (st >> 2 & 1) : st / PP;
+    uint32_t *factors = reinterpret_cast<uint32_t *>(sb + C::OFF_FACTORS) + (warp - kLoadWarp) * 128;  // of the tile's rows
     bool ok = true;
     uint32_t n = 0;
     int seg = 0;
     for (int x = x0; ok && x < x1; ++seg) {
       if (!(ok = wait_warp(C::B_SG + seg % kSegs, (seg / kSegs) & 1))) break;
-      const int4 ra = seg_rec[2 * (seg % kSegs)], rb = seg_rec[2 * (seg % kSegs) + 1];
-      const int units = ra.x;
+      const int4 ra = seg_rec[2 * (seg % kSegs)];
+      const int units = ra.x, g = ra.w;
       x += units;
       // ---- Q: rows as f16, the largest element of each brought to [2^14, 2^15)
-      if (seg > 0 && !(ok = wait_warp(C::B_QE, (seg - 1) & 1))) break;
-      constexpr int LPR = D / 8, RS = 128 / LPR, U = 4;  // threads of a row, rows of a step, steps in flight
+      if (n > 0 && !(ok = wait_warp(s_bar(1, n - 1), s_parity(n - 1)))) break;  // (the last S of the segment before)
+      constexpr int LPR = D / 8, RS = LT / LPR, U = 4;  // threads of a row, rows of a step, steps in flight
 #pragma unroll 1
       for (int q0 = 0; q0 < C::NTQ * kRows; q0 += RS * U) {
         uint4 v[U];
 #pragma unroll
         for (int e = 0; e < U; ++e) {
-          const int row = rb.x * C::NTQ * kRows + q0 + e * RS + lt / LPR, tok = row / G;
+          const int row = q0 + e * RS + lt / LPR, tok = row / G;
           v[e] = make_uint4(0u, 0u, 0u, 0u);
           if (tok < ra.z)
             v[e] = __ldg(reinterpret_cast<const uint4 *>(
-                a.q + (static_cast<size_t>(ra.y + tok) * a.hq + ra.w * G + row % G) * D + lt % LPR * 8));
+                a.q + (static_cast<size_t>(ra.y + tok) * a.hq + g * G + row % G) * D + lt % LPR * 8));
         }
 #pragma unroll
         for (int e = 0; e < U; ++e) {
@@ -662,70 +1083,118 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
       for (int i = 0; ok && i < units; ++i, ++n) {
         // ---- the unit's scales, K's and V's
         if (!(ok = wait_warp(C::B_IN + n % kUnits, (n / kUnits) & 1))) break;
-        const int there = info_in[n % kUnits];
-        int ref[2];
+        const int4 u = unit_rec[n % kUnits];
+        const int n0 = unit_keys(u, 0), n1 = unit_keys(u, 1), kind = unit_kind(u);
+        const size_t dstride = static_cast<size_t>(a.c.hkv) * D;
+        const uint32_t z = 2 * n + kv, s = z % C::NS;
+        if (!(ok = wait_warp(C::B_GF + z % C::NG, (z / C::NG) & 1))) break;
+        const uint16_t *drafted = (kv == 0 ? a.k_new : a.v_new) + (static_cast<size_t>(kind == kDraft ? u.z : 0) * a.c.hkv + g) * D;
+        int top;
+        uint32_t exps = 0u;  // of the lane's four rows
+        if (kind == kDraft) {  // the largest finite element lands in [2^14, 2^15); every warp looks at all rows
+          float am = 0.f;
+          uint32_t lost = 0u;
+#pragma unroll 4
+          for (int c = lane; c < (n0 + n1) * LPR; c += 32)
+            am = fmaxf(am, amax8(finite_bf16x8(
+                               __ldg(reinterpret_cast<const uint4 *>(drafted + (c / LPR) * dstride + c % LPR * 8)), lost)));
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t z = 2 * n + kv;
-          if (!(ok = wait_warp(C::B_GF + z % C::NG, (z / C::NG) & 1))) break;
+          for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+          top = max(8, (__float_as_int(am) >> 23) + C::SHV - 14);
+        } else {
           const uint32_t w = *reinterpret_cast<const uint32_t *>(sb + C::OFF_G + (z % C::NG) * C::STAGE + C::EXPS + lane * 4);
-          const uint32_t m = (there >> (lane >> 4) & 1) != 0 ? __vmaxu4(w, w >> 16) : 0u;
-          ref[kv] = static_cast<int>(__reduce_max_sync(0xffffffffu, max(m & 0xFFu, (m >> 8) & 0xFFu)));
+          const int live = (lane < 16 ? n0 : n1) - 4 * (lane & 15);  // of the lane's four rows
+          exps = live >= 4 ? w : live <= 0 ? 0u : w & ((1u << (8 * live)) - 1u);
+          const uint32_t m = __vmaxu4(exps, exps >> 16);
+          top = static_cast<int>(__reduce_max_sync(0xffffffffu, max(m & 0xFFu, (m >> 8) & 0xFFu)));
         }
-        if (!ok) break;
-        ref[1] = oref = max(oref, ref[1]);
-        if (lt == 0) {
-          info_k[n % kUnits] = exp2f(static_cast<float>(ref[0] - C::SHV - 127));
-          info_v[n % kUnits] = oref;
-          ptx::mbar_arrive(bar(C::B_IK + n % kUnits));
+        if (kv == 1) top = oref = max(oref, top);
+        if (st == 0) {
+          if (kv == 0) scale_k[n % kUnits] = exp2f(static_cast<float>(top - C::SHV - 127));
+          else ref_v[n % kUnits] = top;
+          ptx::mbar_arrive(bar((kv == 0 ? C::B_IK : C::B_IV) + n % kUnits));
         }
-        // ---- both tiles
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t z = 2 * n + kv, s = z % C::NS, round = z / C::NS;
-          if (round > 0 && !(ok = wait_warp(C::B_E + s, (round - 1) & 1))) break;
+        // ---- the tile
+        {
+          uint32_t parity = 0;
+          if (z >= C::NS) {
+            const int fb = free_bar(z, parity);
+            if (!(ok = wait_warp(fb, parity))) break;
+          }
           const unsigned char *stage = sb + C::OFF_G + (z % C::NG) * C::STAGE;
           const uint32_t dst = C::OFF_T + s * C::TILE;
-          const int top = kv == 0 ? ref[0] : ref[1];
-#pragma unroll 4
-          for (int e = 0; e < PP; ++e) {
-            const int row = r0 + e * STEP;
-            const bool live = (there >> (row >> 6) & 1) != 0;
-            const uint4 cw = live ? *reinterpret_cast<const uint4 *>(stage + row * C::RB + p * 16) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t f = live ? pow2_f16x2(static_cast<int>(stage[C::EXPS + row]) - top + C::SHV) : 0u;
-            const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
-            const uint32_t at = dst + static_cast<uint32_t>(row) * 128;
-            auto put = [&](int c, int u, uint4 v) {  // unit u of swizzle chunk c
-              *reinterpret_cast<uint4 *>(sb + at + static_cast<uint32_t>(c) * C::CHUNK +
-                                         static_cast<uint32_t>((u ^ (row & 7)) * 16)) = v;
-            };
-            if constexpr (FMT == BSA_CACHE_E4M3) {
-              uint32_t h[8];
+          if (kind == kDraft) {
+            const float f = pow2_biased(254 + C::SHV - top);
+            uint32_t lost = 0u;
+#pragma unroll 2
+            for (int c = st; c < 128 * LPR; c += ST) {
+              const int row = c / LPR, q = c % LPR;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (row < n0 + n1) v = __ldg(reinterpret_cast<const uint4 *>(drafted + row * dstride + q * 8));
+              if (kv == 1) v = finite_bf16x8(v, lost);
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                h[2 * c] = mul_f16x2(e4m3x2_f16(w[c]), f);
-                h[2 * c + 1] = mul_f16x2(e4m3x2_f16(w[c] >> 16), f);
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+              *reinterpret_cast<uint4 *>(sb + swizzled(dst, q >> 3, row, q & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (__any_sync(0xffffffffu, lost != 0u) && lane == 0) wk.totals[2] = 1;
+          } else {
+            const bool check = kv == 1 && kind == kOwn;
+            __syncwarp();  // the last tile's factors have been read
+            {
+              auto factor = [&](int x) { return pow2_f16x2(static_cast<int>(exps >> (8 * x) & 0xFFu) - top + C::SHV); };
+              reinterpret_cast<uint4 *>(factors)[lane] = make_uint4(factor(0), factor(1), factor(2), factor(3));
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int e = 0; e < 128 / STEP; ++e) {
+              const int row = r0 + e * STEP;
+              const bool live = (row & 63) < (row >= 64 ? n1 : n0);
+              uint4 cw = live ? *reinterpret_cast<const uint4 *>(stage + row * C::RB + p * 16) : make_uint4(0u, 0u, 0u, 0u);
+              uint32_t scale2 = 0u;  // group scales of the piece
+              if constexpr (FMT == BSA_CACHE_E2M1)
+                scale2 = live ? *reinterpret_cast<const uint16_t *>(stage + C::GROUPS + row * (D / 16) + 2 * p) : 0u;
+              if (check) {  // a NaN in a masked place goes by way of the combine
+                uint32_t *odd = wk.odd + (static_cast<size_t>(u.z) * a.c.hkv + g) * kOdd;
+                if constexpr (FMT == BSA_CACHE_E2M1) {
+                  scale2 = without_nan(scale2, p * 32, 16, odd);
+                } else if ((nan_codes(cw.x) | nan_codes(cw.y) | nan_codes(cw.z) | nan_codes(cw.w)) != 0u) {
+                  cw = make_uint4(without_nan(cw.x, p * 16, 1, odd), without_nan(cw.y, p * 16 + 4, 1, odd),
+                                  without_nan(cw.z, p * 16 + 8, 1, odd), without_nan(cw.w, p * 16 + 12, 1, odd));
+                }
               }
-              const uint4 s0 = make_uint4(h[0], h[1], h[2], h[3]), s1 = make_uint4(h[4], h[5], h[6], h[7]);
-              // the upper pieces store their halves in the other order: no two lanes meet in a bank
-              const int u = 2 * (p & 3), sw = (p >> 2) & 1;
-              put(p >> 2, u + sw, sw ? s1 : s0);
-              put(p >> 2, u + 1 - sw, sw ? s0 : s1);
-            } else {
-              const uint32_t g2 = mul_f16x2(
-                  e4m3x2_f16(live ? *reinterpret_cast<const uint16_t *>(stage + C::GROUPS + row * (D / 16) + 2 * p) : 0u), f);
-              const uint32_t ga = __byte_perm(g2, g2, 0x1010), gb = __byte_perm(g2, g2, 0x3232);
+              const uint32_t f = factors[row];
+              const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+              const uint32_t at = dst + static_cast<uint32_t>(row) * 128;
+              auto put = [&](int c, int q, uint4 v) {  // eight values into unit q of swizzle chunk c
+                *reinterpret_cast<uint4 *>(sb + at + static_cast<uint32_t>(c) * C::CHUNK +
+                                           static_cast<uint32_t>((q ^ (row & 7)) * 16)) = v;
+              };
+              if constexpr (FMT == BSA_CACHE_E4M3) {
+                uint32_t h[8];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t gs = c < 2 ? ga : gb;
-                put(p >> 1, 4 * (p & 1) + c,
-                    make_uint4(mul_f16x2(e2m1x2_f16(w[c]), gs), mul_f16x2(e2m1x2_f16(w[c] >> 8), gs),
-                               mul_f16x2(e2m1x2_f16(w[c] >> 16), gs), mul_f16x2(e2m1x2_f16(w[c] >> 24), gs)));
+                for (int c = 0; c < 4; ++c) {
+                  h[2 * c] = mul_f16x2(e4m3x2_f16(w[c]), f);
+                  h[2 * c + 1] = mul_f16x2(e4m3x2_f16(w[c] >> 16), f);
+                }
+                put(p >> 2, 2 * (p & 3), make_uint4(h[0], h[1], h[2], h[3]));
+                put(p >> 2, 2 * (p & 3) + 1, make_uint4(h[4], h[5], h[6], h[7]));
+              } else {
+                const uint32_t g2 = mul_f16x2(e4m3x2_f16(scale2), f);
+                const uint32_t ga = __byte_perm(g2, g2, 0x1010), gb = __byte_perm(g2, g2, 0x3232);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t gs = c < 2 ? ga : gb;
+                  put(p >> 1, 4 * (p & 1) + c,
+                      make_uint4(mul_f16x2(e2m1x2_f16(w[c]), gs), mul_f16x2(e2m1x2_f16(w[c] >> 8), gs),
+                                 mul_f16x2(e2m1x2_f16(w[c] >> 16), gs), mul_f16x2(e2m1x2_f16(w[c] >> 24), gs)));
+                }
               }
             }
           }
           ptx::fence_proxy_async_smem();
-          arrive_warp(C::B_F + s);
+          arrive_warp(full_bar(z));
           arrive_warp(C::B_GE + z % C::NG);
         }
       }
@@ -740,66 +1209,35 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
-  // The kernel over the sequences' own keys may still run beside this one; the combine waits for this one alone.
-  after_previous_kernel();
 }
 
-// The combine.  A block is up to kItems (row, four dimensions) of one token and KV head; its kSplit teams take parts
-// i, i + kSplit, ..: the parts of the token's rows over the shared pages, then those over its own keys.  Sums are
-// added in a fixed order.
-constexpr int kItems = 64, kSplit = 8;
+// ---------------------------------------------------------------- the combine
 
-// Where the parts of a token's rows in one row tile are.
-struct Parts {
-  int count;  // 0: no keys
-  bool whole;  // one part, left row by row
-  int first_cta, tile_first, run, tile, row;
-};
-__device__ __forceinline__ Parts parts_of(int tile_first, int per, int row, int tile_rows, int run) {
-  Parts p;
-  p.tile_first = tile_first;
-  p.first_cta = tile_first / run;
-  p.count = (tile_first + per - 1) / run - p.first_cta + 1;
-  p.whole = p.count == 1;
-  p.run = run;
-  p.tile = row % tile_rows / kRows;
-  p.row = row % kRows;
-  return p;
-}
+// A block is kItems (row, four dimensions) of one token and KV head; its teams take the parts i, i + teams, .. of the
+// token's rows, and the sums are added in a fixed order.
+constexpr int kCombineThreads = 512;
 
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(kItems * kSplit)
-    shared_combine_kernel(const TreeArgs a, const float *part_o, const float2 *part_ml, const float *own_o,
-                          const float2 *own_ml, const SharedOut so, const int *own_plan, const OwnParts op) {
-  constexpr int LANES = PAIR ? 1 : 2;  // results of a row and part over shared pages
+template <int D, bool PAIR, int kItems>
+__global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const TreeArgs a, const SharedWork wk) {
+  constexpr int kSplit = kCombineThreads / kItems;
+  constexpr int LANES = PAIR ? 1 : 2;  // results of a row and part
+  constexpr int TILE_ROWS = PAIR ? 2 * kRows : kRows;
   after_previous_kernel();
   __shared__ float red_m[kSplit][kItems], red_l[kSplit][kItems];
   __shared__ float4 red_o[kSplit][kItems];
   const int G = a.group, items = G * (D / 4), slices = (items + kItems - 1) / kItems;
   const int i = blockIdx.x / slices, g = blockIdx.y, b = blockIdx.z;
-  const Drafts dr = drafts_of(a, b);
+  const SeqRecord dr = wk.seqs[b];
+  const int all = wk.totals[0] * a.c.hkv, tiles = wk.totals[1], drafts_odd = wk.totals[2];
+  const uint32_t *mark = wk.odd + static_cast<size_t>(b * a.c.hkv + g) * kOdd;
+  const uint32_t own_odd = mark[0];
   if (i >= dr.len) return;
-  const int y = group_of(a, b);
-  Parts ps{}, po{};
-  if (y >= 0) {
-    constexpr int TILE_ROWS = PAIR ? 2 * kRows : kRows;
-    const SharedRows all = shared_rows(a, y);
-    const SharedPlan plan = shared_plan(a, all, TILE_ROWS);
-    const int at = dr.start + i - all.rows.start, units = so.plan[a.groups];
-    if (at >= 0 && at < all.rows.len && plan.per > 0)
-      ps = parts_of(so.plan[y] + (g * plan.tiles + at * G / TILE_ROWS) * plan.per, plan.per, at * G, TILE_ROWS,
-                    (units + kSms - 1) / kSms);
-  }
-  const int shared = ps.count * LANES;
-  {
-    const int x = b * a.c.hkv + g, u0 = own_plan[x], units = own_plan[x + 1] - u0, all = own_plan[a.batch * a.c.hkv];
-    const int tiles = (dr.len * G + op.rows - 1) / op.rows, per = units / tiles;
-    if (op.rows_first) {  // one row tile, whatever its rows
-      po = parts_of(u0, units, i * G, kRows, (all + op.ctas - 1) / op.ctas);
-    } else {
-      po = parts_of(u0 + i * G / op.rows * per, per, i * G, op.rows, (all + op.ctas - 1) / op.ctas);
-    }
-  }
+  const int row0 = (dr.at + i) * G, e = dr.tile0 + row0 / TILE_ROWS;
+  if (e >= tiles) return;
+  const int2 fu = *reinterpret_cast<const int2 *>(&wk.tiles[e].first);
+  const int run = run_places(all, tiles * a.c.hkv);
+  const int first = (fu.x + kPad * e) * a.c.hkv + g * (fu.y + kPad), cta0 = first / run, count = (first + fu.y - 1) / run - cta0 + 1;
+  const int tile = row0 % TILE_ROWS / kRows, rr = row0 % kRows;
 
   const int item = threadIdx.x % kItems, team = threadIdx.x / kItems;
   const int it = blockIdx.x % slices * kItems + item, h = it % G, q = it / G;
@@ -807,45 +1245,27 @@ __global__ void __launch_bounds__(kItems * kSplit)
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (it < items) {
-    const int n = shared + po.count;
-    constexpr int U = 2;  // parts in flight
+    const int n = count * LANES;
+    constexpr int U = 4;  // parts in flight
     for (int base = team; base < n; base += U * kSplit) {
       float2 ml[U], ml2[U];
       float4 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int x = base + u * kSplit;
+        const int x = base + u * kSplit, lane = PAIR ? 0 : x & 1;
         ml[u] = ml2[u] = make_float2(-INFINITY, 0.f);
         v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x < shared) {
-          const int lane = PAIR ? 0 : x & 1;
-          if (ps.whole) {
-            ml[u] = so.row_ml[2 * lane * so.rows + out];
-            ml2[u] = so.row_ml[(2 * lane + 1) * so.rows + out];
-            v[u] = reinterpret_cast<const float4 *>(so.row_o)[(lane * so.rows + out) * (D / 4) + q];
-          } else {
-            const int cta = ps.first_cta + x / LANES;
-            const size_t slot = 2 * (2 * static_cast<size_t>(cta) + (ps.tile_first <= cta * ps.run ? 0 : 1)) + (PAIR ? ps.tile : lane);
-            ml[u] = part_ml[slot * 2 * kRows + ps.row + h];
-            ml2[u] = part_ml[(slot * 2 + 1) * kRows + ps.row + h];
-            v[u] = reinterpret_cast<const float4 *>(part_o)[(slot * (D / 4) + q) * kRows + ps.row + h];
-          }
-        } else if (x < n) {
-          if (po.whole) {
-            ml[u] = so.row_ml[4 * so.rows + out];
-            v[u] = reinterpret_cast<const float4 *>(so.row_o)[(2 * so.rows + out) * (D / 4) + q];
-          } else {
-            const int cta = po.first_cta + x - shared;
-            const size_t slot = 2 * static_cast<size_t>(cta) + (po.tile_first <= cta * po.run ? 0 : 1);
-            if (op.rows_first) {
-              ml[u] = own_ml[slot * op.rows + po.row + h];
-              v[u] = reinterpret_cast<const float4 *>(own_o)[(slot * op.rows + po.row + h) * (D / 4) + q];
-            } else {
-              const size_t tile = slot * (op.rows / kRows) + po.tile;
-              ml[u] = own_ml[tile * kRows + po.row + h];
-              v[u] = reinterpret_cast<const float4 *>(own_o)[(tile * (D / 4) + q) * kRows + po.row + h];
-            }
-          }
+        if (x >= n) continue;
+        if (count == 1) {
+          ml[u] = wk.row_ml[2 * lane * wk.rows + out];
+          ml2[u] = wk.row_ml[(2 * lane + 1) * wk.rows + out];
+          v[u] = reinterpret_cast<const float4 *>(wk.row_o)[(lane * wk.rows + out) * (D / 4) + q];
+        } else {
+          const int cta = cta0 + x / LANES;
+          const size_t slot = 2 * (2 * static_cast<size_t>(cta) + (first - kPad <= cta * run ? 0 : 1)) + (PAIR ? tile : lane);
+          ml[u] = wk.part_ml[slot * 2 * kRows + rr + h];
+          ml2[u] = wk.part_ml[(slot * 2 + 1) * kRows + rr + h];
+          v[u] = reinterpret_cast<const float4 *>(wk.part_o)[(slot * (D / 4) + q) * kRows + rr + h];
         }
       }
 #pragma unroll
@@ -884,42 +1304,70 @@ __global__ void __launch_bounds__(kItems * kSplit)
     s.z = fmaf(v.z, f, s.z);
     s.w = fmaf(v.w, f, s.w);
   }
+  float o[4] = {s.x, s.y, s.z, s.w};
+  if (own_odd != 0u) {  // Inf and NaN of own values, which every row of the sequence sees
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int dim = 4 * q + d;
+      auto marked = [&](int which) { return (mark[1 + which * 4 + dim / 32] >> (dim & 31) & 1u) != 0u; };
+      if (marked(0)) o[d] += INFINITY;
+      if (marked(1)) o[d] -= INFINITY;
+      if (marked(2)) o[d] = __int_as_float(0x7FC00000);
+    }
+  }
+  if (drafts_odd != 0) {  // and of the drafted values on its path
+    const uint16_t *vn = a.v_new + (static_cast<size_t>(dr.start) * a.c.hkv + g) * D + 4 * q;
+    for (int p = i; p >= 0; p = parent_of(a, dr.start, p)) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(vn + static_cast<size_t>(p) * a.c.hkv * D));
+      o[0] += not_finite(w.x & 0xFFFFu);
+      o[1] += not_finite(w.x >> 16);
+      o[2] += not_finite(w.y & 0xFFFFu);
+      o[3] += not_finite(w.y >> 16);
+    }
+  }
   const float inv = ls == 0.f ? 0.f : 1.f / ls;
   *reinterpret_cast<uint2 *>(a.o + out * D + 4 * q) =
-      make_uint2(ptx::pack_bf16x2(s.x * inv, s.y * inv), ptx::pack_bf16x2(s.z * inv, s.w * inv));
+      make_uint2(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv));
   if (a.lse != nullptr && q == 0) a.lse[out] = ls == 0.f ? -INFINITY : (mm + log2f(ls)) * 0.69314718055994531f;
 }
 
-struct Workspace {
-  size_t part_o, part_ml, own_o, own_ml, lane_o, row_o, row_ml, plan, own_plan, total;
-};
-Workspace workspace_layout(const CacheDims &c, int groups, int batch, size_t rows) {
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t d = c.d, parts = 4ull * kSms * kRows;  // two parts per CTA, up to two row tiles or lanes each
-  const OwnParts few = own_few_parts(c);
-  const size_t own = 2ull * few.ctas * few.rows > parts ? 2ull * few.ctas * few.rows : parts;
-  Workspace w;
-  w.part_o = 0;
-  w.part_ml = up(parts * d * 4);
-  w.own_o = w.part_ml + up(2 * parts * 8);
-  w.own_ml = w.own_o + up(own * d * 4);
-  w.lane_o = w.own_ml + up(own * 8);
-  w.row_o = w.lane_o + up(static_cast<size_t>(kSms) * kRows * (d + 4) * 4);
-  w.row_ml = w.row_o + up(3 * rows * d * 4);
-  w.plan = w.row_ml + up(6 * rows * 8);
-  w.own_plan = w.plan + up((static_cast<size_t>(groups) + 1) * 4);
-  w.total = w.own_plan + up((static_cast<size_t>(batch) * c.hkv + 1) * 4);
+// ---------------------------------------------------------------- host side
+
+// Lays the workspace out from `base` (null: sizes only); *bytes gets what it takes.
+SharedWork work_layout(const CacheDims &c, int groups, int batch, int total, int hq, char *base, size_t *bytes) {
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    char *p = base + at;
+    at += (n + 255) / 256 * 256;
+    return p;
+  };
+  const size_t d = c.d, parts = 4ull * kSms * kRows;  // two parts per CTA, two row tiles or lanes each
+  SharedWork w;
+  w.rows = static_cast<size_t>(total) * hq;
+  w.max_tiles = static_cast<int>(static_cast<long long>(total) * (hq / c.hkv) / kRows) + groups;
+  w.part_o = reinterpret_cast<float *>(take(parts * d * 4));
+  w.part_ml = reinterpret_cast<float2 *>(take(2 * parts * 8));
+  w.row_o = reinterpret_cast<float *>(take(2 * w.rows * d * 4));
+  w.row_ml = reinterpret_cast<float2 *>(take(4 * w.rows * 8));
+  w.seqs = reinterpret_cast<SeqRecord *>(take(static_cast<size_t>(batch) * sizeof(SeqRecord)));
+  w.tiles = reinterpret_cast<TileRecord *>(take(static_cast<size_t>(w.max_tiles) * sizeof(TileRecord)));
+  w.own_before = reinterpret_cast<int *>(take((static_cast<size_t>(batch) + 1) * 4));
+  w.token_start = reinterpret_cast<int *>(take(static_cast<size_t>(total) * 4));
+  w.totals = reinterpret_cast<int *>(take(16));
+  w.odd = reinterpret_cast<uint32_t *>(take(static_cast<size_t>(batch) * c.hkv * kOdd * 4));
+  *bytes = at;
   return w;
 }
 
-// Rows of q [total, hq, d]: box of 64 dimensions, the G heads of a KV group and 128 / G tokens; 128-byte swizzle.
-bool query_map(EncodeTiledFn fn, CUtensorMap *map, const TreeArgs &a) {
-  const cuuint64_t d = static_cast<cuuint64_t>(a.c.d);
-  const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(a.hq), static_cast<cuuint64_t>(a.total)};
-  const cuuint64_t strides[2] = {d * 2, d * 2 * static_cast<cuuint64_t>(a.hq)};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(kRows / a.group)};
+// Rows of q, or of drafted k or v [total, heads, d]: box of 64 dimensions, `box_heads` heads and 128 / box_heads tokens;
+// 128-byte swizzle.
+bool token_map(EncodeTiledFn fn, CUtensorMap *map, const uint16_t *ptr, int d, int heads, int total, int box_heads) {
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(total)};
+  const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(heads)};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(kRows / box_heads)};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(a.q), dims, strides, box, estr,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -927,40 +1375,36 @@ bool query_map(EncodeTiledFn fn, CUtensorMap *map, const TreeArgs &a) {
 template <int D, int FMT, bool PAIR>
 bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   using C = Shared<D, FMT, PAIR>;
-  CUtensorMap mq{}, mk{}, mv{};
+  SharedMaps maps{};
   if (!C::Q16) {
     cudaError_t e = cudaSuccess;
     EncodeTiledFn fn = tensor_map_encoder(&e);
-    if (fn == nullptr || e != cudaSuccess || !query_map(fn, &mq, a) || !chunk_map(fn, &mk, a.k_codes, a.c) ||
-        !chunk_map(fn, &mv, a.v_codes, a.c))
+    if (fn == nullptr || e != cudaSuccess || !token_map(fn, &maps.q, a.q, D, a.hq, a.total, a.group) ||
+        !token_map(fn, &maps.kn, a.k_new, D, a.c.hkv, a.total, 1) || !token_map(fn, &maps.vn, a.v_new, D, a.c.hkv, a.total, 1) ||
+        !chunk_map(fn, &maps.k, a.k_codes, a.c) || !chunk_map(fn, &maps.v, a.v_codes, a.c))
       return BSA_ERR_CUDA;
   }
-  const size_t rows = static_cast<size_t>(a.total) * a.hq;
-  const Workspace ws = workspace_layout(a.c, a.groups, a.batch, rows);
-  char *base = static_cast<char *>(workspace);
-  auto f32 = [&](size_t at) { return reinterpret_cast<float *>(base + at); };
-  auto f32x2 = [&](size_t at) { return reinterpret_cast<float2 *>(base + at); };
-  SharedOut so{f32(ws.row_o), f32x2(ws.row_ml), rows, reinterpret_cast<int *>(base + ws.own_plan)};
-  int *own_plan = so.plan;
+  size_t bytes = 0;
+  const SharedWork w = work_layout(a.c, a.groups, a.batch, a.total, a.hq, static_cast<char *>(workspace), &bytes);
   auto kern = shared_kernel<D, FMT, PAIR>;
   // setmaxnreg.inc waits until the registers it asks for are free: the split is only safe if the
   // kernel really launches with that many registers per thread
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_up(kern, C::SMEM, C::LAUNCH_REGS, done);
   if (e != cudaSuccess) return e == cudaErrorNotSupported ? BSA_ERR_UNSUPPORTED : BSA_ERR_CUDA;
-  const bool few = a.max_draft * a.group <= own_few_parts(a.c).rows;
-  const OwnParts op = few ? own_few_parts(a.c) : own_many_parts(a);
-  e = few ? launch_own_few(a, so, f32(ws.own_o), f32(ws.own_ml), stream)
-          : launch_own_many(a, so, f32(ws.own_o), f32(ws.own_ml), f32(ws.lane_o), stream);
-  if (e != cudaSuccess) return e == cudaErrorNotSupported ? BSA_ERR_UNSUPPORTED : BSA_ERR_CUDA;
-  so.plan = reinterpret_cast<int *>(base + ws.plan);
-  e = launch_after(kern, dim3(kSms), C::THREADS, C::SMEM, stream, mq, mk, mv, a, f32(ws.part_o), f32x2(ws.part_ml), so);
+  static std::atomic<uint64_t> plan_done{0};
+  e = set_up(shared_plan_kernel, plan_smem(kMaxDecodeRows, kMaxDecodeRows), 0, plan_done);
   if (e != cudaSuccess) return BSA_ERR_CUDA;
-  const int slices = (a.group * (D / 4) + kItems - 1) / kItems;
-  e = launch_after(shared_combine_kernel<D, PAIR>, dim3(a.max_draft * slices, a.c.hkv, a.batch), kItems * kSplit, 0, stream, a,
-                   static_cast<const float *>(f32(ws.part_o)), static_cast<const float2 *>(f32x2(ws.part_ml)),
-                   static_cast<const float *>(f32(ws.own_o)), static_cast<const float2 *>(f32x2(ws.own_ml)), so,
-                   static_cast<const int *>(own_plan), op);
+  const int plan_threads = a.batch <= 128 ? 128 : a.batch <= 512 ? 512 : 1024;
+  shared_plan_kernel<<<1, plan_threads, plan_smem(a.batch, a.groups), stream>>>(a, w, C::NTQ * kRows);
+  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  e = launch_after(kern, dim3(kSms), C::THREADS, C::SMEM, stream, maps, a, w);
+  if (e != cudaSuccess) return BSA_ERR_CUDA;
+  // few rows: small blocks, so that many teams share a row's parts; many rows: a block is a whole token's
+  const bool small = static_cast<long long>(a.total) * a.c.hkv <= 2 * kSms;
+  auto combine = small ? shared_combine_kernel<D, PAIR, 64> : shared_combine_kernel<D, PAIR, 256>;
+  const int items = small ? 64 : 256, slices = (a.group * (D / 4) + items - 1) / items;
+  e = launch_after(combine, dim3(a.max_draft * slices, a.c.hkv, a.batch), kCombineThreads, 0, stream, a, w);
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -973,8 +1417,10 @@ bsa_status launch_fmt(const TreeArgs &a, void *workspace, cudaStream_t stream) {
 
 }  // namespace
 
-size_t shared_workspace_bytes(const CacheDims &c, int groups, int batch, int total, int, int hq) {
-  return workspace_layout(c, groups, batch, static_cast<size_t>(total) * hq).total;
+size_t shared_workspace_bytes(const CacheDims &c, int groups, int batch, int total, int hq) {
+  size_t bytes = 0;
+  work_layout(c, groups, batch, total, hq, nullptr, &bytes);
+  return bytes;
 }
 
 bsa_status launch_shared(const TreeArgs &a, void *workspace, cudaStream_t stream) {

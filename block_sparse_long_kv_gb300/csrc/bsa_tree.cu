@@ -43,9 +43,6 @@
 // Groups that one CTA holds whole are written by it; of the others every CTA
 // leaves an unnormalised part (O, max, sum), which tree_combine_kernel merges in
 // a fixed order, so the result does not depend on timing.
-//
-// OWN: the part of a call over shared pages that sequences do not share, their keys
-// behind those pages; every result is left for that call's combine in fp32.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -162,9 +159,9 @@ __device__ __forceinline__ int cta_scan(int c, int *total, int *wsum) {
 
 // A unit: .x the group (b * hkv + g), .y the cache tile (page * hkv + g; -1: drafted tokens, or nothing), .z its
 // keys, .w its 64-key chunk of the page.
-template <int D, int FMT, bool OWN>
+template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(const TreeArgs a, float *part_o, float *part_ml,
-                                                                        TreeRun *runs, const SharedOut so) {
+                                                                        TreeRun *runs) {
   using C = Cfg<D, FMT>;
   constexpr bool Q16 = FMT != BSA_CACHE_BF16;  // f16 fragments
   extern __shared__ __align__(16) unsigned char smem[];
@@ -191,15 +188,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     int local = 0;
     for (int x = g0; x < g1; ++x) {
       const int b = x / a.c.hkv;
-      const int listed = OWN || a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + x);  // (the loads in one round)
-      int n = 0;
-      if constexpr (!OWN) n = cached_of(a, b);
+      const int listed = a.kv_cnt == nullptr ? INT32_MAX : __ldg(a.kv_cnt + x);  // (the loads in one round)
+      const int n = cached_of(a, b);
       const Drafts dr = drafts_of(a, b);
-      if constexpr (OWN) n = own_keys(a, b, dr.len).n;
       const int pages = (n + a.c.page - 1) >> a.c.page_shift;
       const int kept = max(0, min(listed, pages));
       // without a list the chunks past the last token are not units at all
-      const int ku = OWN || a.kv_cnt == nullptr ? (n + kKeys - 1) / kKeys : kept * cpp;
+      const int ku = a.kv_cnt == nullptr ? (n + kKeys - 1) / kKeys : kept * cpp;
       pre[x] = dr.len > 0 ? ku + 1 : 0;
       local += pre[x];
     }
@@ -216,16 +211,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
     }
     __syncthreads();
   }
-  if constexpr (OWN) {
-    launch_next();  // the kernel over the shared pages takes the SMs as they fall free
-    if (cta == 0)
-      for (int x = tid; x <= groups; x += kThreads) so.plan[x] = pre[x];
-  }
   const int n_all = pre[groups];
   const int W = (n_all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int x0 = min(n_all, cta * W), x1 = min(n_all, x0 + W);
   if (x0 >= x1) {  // CTA-uniform
-    if (!OWN && tid == 0) runs[cta].group = -1;
+    if (tid == 0) runs[cta].group = -1;
     return;
   }
   const int nu = x1 - x0;
@@ -241,16 +231,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
       else hi = mid - 1;
     }
     const int b = lo / a.c.hkv, k = x - pre[lo];
-    const OwnKeys own = OWN ? own_keys(a, b, 0) : OwnKeys{0, cached_of(a, b)};
-    const int n = own.n;
+    const int n = cached_of(a, b);
     int4 d = make_int4(lo, -1, 0, 0);
     if (k == pre[lo + 1] - pre[lo] - 1) {
       d.z = drafts_of(a, b).len;
     } else {
       const int e = k >> (a.c.page_shift - 6), sub = k & (cpp - 1);
-      const int j = OWN || a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
+      const int j = a.kv_idx == nullptr ? e : __ldg(a.kv_idx + static_cast<size_t>(lo) * a.table_stride + e);
       if (j >= 0 && j < (n + a.c.page - 1) >> a.c.page_shift) {
-        const int pg = __ldg(a.table + static_cast<size_t>(b) * a.table_stride + own.first + j);
+        const int pg = __ldg(a.table + static_cast<size_t>(b) * a.table_stride + j);
         if (pg >= 0 && pg < a.c.pages) {
           d.y = pg * a.c.hkv + (lo - b * a.c.hkv);
           d.z = max(0, min(kKeys, n - j * a.c.page - sub * kKeys));
@@ -447,11 +436,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
           v.w += not_finite(u.y >> 16);
         }
       }
-      if (OWN && whole) {
-        const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + r % G;
-        *reinterpret_cast<float4 *>(so.row_o + (2 * so.rows + at) * D + d4) = v;
-        if (d4 == 0) so.row_ml[4 * so.rows + at] = make_float2(m, l);
-      } else if (whole) {
+      if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (NaN where the sum is)
         const size_t at = static_cast<size_t>(adr.start + t) * a.hq + (arow_g % a.c.hkv) * G + r % G;
         *reinterpret_cast<uint2 *>(a.o + at * D + d4) =
@@ -754,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT>::CTAS) tree_attn_kernel(
 
   resolve(0);
   __syncthreads();
-  if (!OWN && tid == 0) {  // the run's first group, for the combine
+  if (tid == 0) {  // the run's first group, for the combine
     const int grp = unit[0].x;
     const Drafts dr = drafts_of(a, grp / a.c.hkv);
     runs[cta] = TreeRun{grp, 0, pre[grp], pre[grp + 1], W, dr.start, dr.len, 0};
@@ -889,12 +874,12 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   char *base = static_cast<char *>(workspace);
   float *part_o = reinterpret_cast<float *>(base + ws.part_o), *part_ml = reinterpret_cast<float *>(base + ws.part_ml);
   TreeRun *runs = reinterpret_cast<TreeRun *>(base + ws.runs);
-  auto kern = tree_attn_kernel<D, FMT, false>;
+  auto kern = tree_attn_kernel<D, FMT>;
   const size_t smem = C::smem(a.batch * a.c.hkv);
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_up(kern, C::smem(kMaxDecodeRows), 0, done);
   if (e != cudaSuccess) return e;
-  kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, runs, SharedOut{});
+  kern<<<kSms * C::CTAS, kThreads, smem, stream>>>(a, part_o, part_ml, runs);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int ctas = kSms * C::CTAS, groups = a.batch * a.c.hkv;
@@ -904,37 +889,7 @@ cudaError_t launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
                       static_cast<const TreeRun *>(runs), ctas);
 }
 
-template <int D, int FMT>
-cudaError_t launch_own_t(const TreeArgs &a, const SharedOut &so, float *part_o, float *part_ml, cudaStream_t stream) {
-  using C = Cfg<D, FMT>;
-  auto kern = tree_attn_kernel<D, FMT, true>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = set_up(kern, C::smem(kMaxDecodeRows), 0, done);
-  if (e != cudaSuccess) return e;
-  kern<<<kSms * C::CTAS, kThreads, C::smem(a.batch * a.c.hkv), stream>>>(a, part_o, part_ml, nullptr, so);
-  return cudaGetLastError();
-}
-
 }  // namespace
-
-OwnParts own_few_parts(const CacheDims &c) {
-  return OwnParts{kRows, kSms * (c.format == BSA_CACHE_BF16 && c.d == 128 ? 2 : 3), true};
-}
-
-cudaError_t launch_own_few(const TreeArgs &a, const SharedOut &so, float *part_o, float *part_ml, cudaStream_t stream) {
-  const bool wide = a.c.d == 128;
-  switch (a.c.format) {
-    case BSA_CACHE_E4M3:
-      return wide ? launch_own_t<128, BSA_CACHE_E4M3>(a, so, part_o, part_ml, stream)
-                  : launch_own_t<64, BSA_CACHE_E4M3>(a, so, part_o, part_ml, stream);
-    case BSA_CACHE_E2M1:
-      return wide ? launch_own_t<128, BSA_CACHE_E2M1>(a, so, part_o, part_ml, stream)
-                  : launch_own_t<64, BSA_CACHE_E2M1>(a, so, part_o, part_ml, stream);
-    default:
-      return wide ? launch_own_t<128, BSA_CACHE_BF16>(a, so, part_o, part_ml, stream)
-                  : launch_own_t<64, BSA_CACHE_BF16>(a, so, part_o, part_ml, stream);
-  }
-}
 
 size_t tree_workspace_bytes(const CacheDims &c, int batch, int hq, int max_draft) {
   return max_draft * (hq / c.hkv) > kRows ? tree_mma_workspace_bytes(c) : workspace_layout(c.d).total;

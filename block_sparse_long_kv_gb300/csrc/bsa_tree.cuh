@@ -62,94 +62,6 @@ __device__ __forceinline__ int parent_of(const TreeArgs &a, int start, int i) {
   return -1;
 }
 
-// Sequences that share pages: group y is the sequences cu_group[y] .. cu_group[y + 1] - 1, whose tables begin with the
-// same shared_pages[y] pages.  What is not as documented sets *status; a group then shares none, and a sequence of no
-// group is on its own.
-__device__ __forceinline__ void report_arg(const TreeArgs &a) {
-  if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
-}
-struct SharedGroup {
-  int first, last, pages;  // its sequences first .. last - 1
-};
-__device__ __forceinline__ SharedGroup shared_group(const TreeArgs &a, int y) {
-  SharedGroup s{__ldg(a.cu_group + y), __ldg(a.cu_group + y + 1), __ldg(a.shared_pages + y)};
-  if (s.first < 0 || s.last < s.first || s.last > a.batch) {
-    report_arg(a);
-    s.first = s.last = 0;
-  }
-  if (s.pages < 0 || s.pages > a.max_cached >> a.c.page_shift) {
-    report_arg(a);
-    s.pages = 0;
-  }
-  return s;
-}
-// The group of sequence b; -1 for none.
-__device__ __forceinline__ int group_of(const TreeArgs &a, int b) {
-  int lo = 0, hi = a.groups - 1;
-  while (lo < hi) {  // the last group that begins at or before b
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.cu_group + mid) <= b) lo = mid;
-    else hi = mid - 1;
-  }
-  if (__ldg(a.cu_group + lo) <= b && b < __ldg(a.cu_group + lo + 1)) return lo;
-  report_arg(a);
-  return -1;
-}
-
-// The rows of a group over its shared pages: every token that its sequences draft.
-struct SharedRows {
-  Drafts rows;  // none where nothing is shared
-  int seq;      // whose table row names the pages: the first that drafts a token
-  int pages;
-};
-__device__ __forceinline__ SharedRows shared_rows(const TreeArgs &a, int y) {
-  const SharedGroup s = shared_group(a, y);
-  SharedRows r{Drafts{0, 0}, s.first, s.pages};
-  if (s.first == s.last || s.pages == 0) return r;
-  const int start = __ldg(a.cu + s.first), end = __ldg(a.cu + s.last);
-  if (start < 0 || end < start || end > a.total) return r;  // (its sequences report it)
-  r.rows = Drafts{start, end - start};
-  while (r.seq + 1 < s.last && __ldg(a.cu + r.seq + 1) == start) ++r.seq;
-  return r;
-}
-
-// The keys of sequence b that it does not share: its cached tokens from page `first` on.
-struct OwnKeys {
-  int first, n;
-};
-__device__ __forceinline__ OwnKeys own_keys(const TreeArgs &a, int b, int drafts) {
-  const int y = group_of(a, b), n = cached_of(a, b);
-  OwnKeys k{y >= 0 ? shared_group(a, y).pages : 0, 0};
-  k.n = n - (k.first << a.c.page_shift);
-  if (k.n < 0) {  // its table does not hold the group's pages
-    if (drafts > 0) report_arg(a);
-    k.n = 0;
-  }
-  return k;
-}
-
-// Where a call over shared pages leaves results for its combine, in fp32: O unnormalised, the maximum, the sum against
-// it.  Row buffers [3][rows]: 0 and 1 over shared pages (1 only where two softmax lanes take turns over one row tile),
-// 2 over a sequence's own keys; their statistics [3][2][rows], a row's sum in two halves over shared pages.
-struct SharedOut {
-  float *row_o;
-  float2 *row_ml;
-  size_t rows;
-  int *plan;  // first unit of every group, for the kernel that fills it
-};
-
-// How the kernel over the sequences' own keys leaves what several of its CTAs share: two parts per CTA, of `rows` rows
-// each; O of a row in order (`rows_first`), or four dimensions of all rows at a time.
-struct OwnParts {
-  int rows, ctas;
-  bool rows_first;
-};
-OwnParts own_few_parts(const CacheDims &c);
-OwnParts own_many_parts(const TreeArgs &a);
-cudaError_t launch_own_few(const TreeArgs &a, const SharedOut &so, float *part_o, float *part_ml, cudaStream_t stream);
-cudaError_t launch_own_many(const TreeArgs &a, const SharedOut &so, float *part_o, float *part_ml, float *lane_o,
-                            cudaStream_t stream);
-
 // Lets the next kernel of the stream start beside this one, if it was launched by launch_after.
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
