@@ -354,6 +354,12 @@ __device__ __forceinline__ void clean_v(unsigned char *tile, int thread, const i
   ptx::fence_proxy_async_smem();
 }
 
+// TMEM columns to and from registers.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { ptx::tmem_ld32(at, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[16]) { ptx::tmem_ld16(at, r); }
+__device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t (&r)[16]) { ptx::tmem_st16(at, r); }
+__device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t (&r)[8]) { ptx::tmem_st8(at, r); }
+
 // The codes among four that are NaN (bit 7 of their bytes); and: marks the dimensions of those in `odd` (.. of +Inf, -Inf,
 // NaN), `each` dimensions a code from `dim` on, and takes them out.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
@@ -873,29 +879,53 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         }
         if (!(ok = wait_warp(s_bar(t, n), s_parity(n)))) break;
         ptx::tc_fence_after();
-        uint32_t sr[32];
-        // the row's maximum first; registers for half of the logits, the second half is read again.  (Beside the loaders
-        // of codes the loops stay loops: what 28 warps run has to fit the instruction cache.)
-        constexpr int UNROLL = Q16 ? 1 : 2;
+        // The row's maximum first, then the logits again, 32 at a time (the first half stays in registers).  Beside the
+        // loaders of codes 16 at a time and loops stay loops: what all the warps of a scheduler run has to fit its
+        // instruction cache.
+        uint32_t sr[Q16 ? 16 : 32];
+        auto seen = [&](int c) { return (c < 2 ? see0 : see1) >> (16 * (c & 1)); };  // of columns 16 c ..
         float top = -INFINITY;
-        if (any) {
-#pragma unroll UNROLL
-          for (int c = 1; c >= 0; --c) {
-            float mx;
-            ptx::tmem_ld32_max(tS + c * 32, sr, mx);
-            ptx::tmem_wait_ld();
-            if (masked) {
-              const uint32_t see = c == 0 ? see0 : see1;
-              mx = -INFINITY;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if (!((see >> e) & 1u)) sr[e] = 0xFF800000u;
-                mx = fmaxf(mx, __uint_as_float(sr[e]));
-              }
+        if constexpr (Q16) {
+          if (any && !masked) {
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t unused[32];
+              float mx;
+              ptx::tmem_ld32_max(tS + c, unused, mx);
+              ptx::tmem_wait_ld();
+              top = fmaxf(top, mx);
             }
-            top = fmaxf(top, mx);
+            if (!on) top = -INFINITY;
+          } else if (any) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              ptx::tmem_ld16(tS + c * 16, sr);
+              ptx::tmem_wait_ld();
+              const uint32_t see = seen(c);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, (see >> e) & 1u ? __uint_as_float(sr[e]) : -INFINITY);
+            }
           }
-          if (!on) top = -INFINITY;
+        } else {
+          if (any) {
+#pragma unroll
+            for (int c = 1; c >= 0; --c) {
+              float mx;
+              ptx::tmem_ld32_max(tS + c * 32, sr, mx);
+              ptx::tmem_wait_ld();
+              if (masked) {
+                const uint32_t see = c == 0 ? see0 : see1;
+                mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  if (!((see >> e) & 1u)) sr[e] = 0xFF800000u;
+                  mx = fmaxf(mx, __uint_as_float(sr[e]));
+                }
+              }
+              top = fmaxf(top, mx);
+            }
+            if (!on) top = -INFINITY;
+          }
         }
         // the maximum of both halves: each half's rounded up to bf16 (any upper bound is a valid reference, and
         // both halves then hold the same value).  The slot is written again only after the partner has released P,
@@ -923,23 +953,25 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         const float bias = static_cast<float>(C::SHIFT) - (m == -INFINITY ? 0.f : m);
         uint64_t acc[2] = {0ull, 0ull};
         const uint64_t scl2 = ptx::f32x2(scl, scl), bias2 = ptx::f32x2(bias, bias);
+        constexpr int W = Q16 ? 16 : 32, UNROLL = Q16 ? 1 : 2;
 #pragma unroll UNROLL
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+        for (int c = 0; c < 64 / W; ++c) {
+          uint32_t pk[W / 2];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          for (int e = 0; e < W / 2; ++e) pk[e] = 0u;
           if (any) {
-            if (c == 1) {
-              ptx::tmem_ld32(tS + 32, sr);
+            if (Q16 || c == 1) {
+              tmem_ld_cols(tS + c * W, sr);
               ptx::tmem_wait_ld();
               if (masked) {
+                const uint32_t see = Q16 ? seen(c) : see1;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((see1 >> e) & 1u)) sr[e] = 0xFF800000u;
+                for (int e = 0; e < W; ++e)
+                  if (!((see >> e) & 1u)) sr[e] = 0xFF800000u;
               }
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < W / 2; ++e) {
               const uint64_t y =
                   ptx::fma_f32x2(ptx::f32x2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scl2, bias2);
               float y0, y1;
@@ -950,10 +982,10 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
             }
             if (!on) {  // (whatever the logits of another sequence's keys are)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+              for (int e = 0; e < W / 2; ++e) pk[e] = 0u;
             }
           }
-          ptx::tmem_st16(tS + c * 16, pk);
+          tmem_st_cols(tS + c * (W / 2), pk);
           if (c == 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
