@@ -69,9 +69,9 @@ struct alignas(16) SeqRecord {
 };
 // A row tile: its tokens, the sequences that have rows in it, its units over shared pages (and their chunks, and the
 // sequence whose table names them), the first drafted token that its rows see; the first unit (of one KV head), the
-// units and those over own keys.
+// units and those over own keys, the first place.
 struct alignas(16) TileRecord {
-  int tok0, tokens, seq_a, seq_b, shared, chunks, table, draft0, first, units, own, pad;
+  int tok0, tokens, seq_a, seq_b, shared, chunks, table, draft0, first, units, own, place;
 };
 // What the calls leave in the workspace.  Parts: two per CTA and lane, O as [dimension / 4][128 rows] float4, two
 // halves' (max, sum); row buffers for tiles that one CTA has whole, of lane 0 (PAIR: of both) and 1.
@@ -83,15 +83,23 @@ struct SharedWork {
   TileRecord *tiles;
   int *own_before;    // [batch + 1] units over own keys before a sequence's
   int *token_start;   // [total] the first token of a token's sequence
-  int *totals;        // units of one KV head, tiles, whether a drafted value held Inf or NaN
+  int *totals;        // units of one KV head, tiles, whether a drafted value held Inf or NaN, places of one KV head
   uint32_t *odd;      // [batch * hkv][13] whether own values held Inf or NaN, and where: +Inf, -Inf, NaN, a bit per dimension
   int max_tiles;
 };
 constexpr int kOdd = 13;
 
-// Places that a row tile and KV head takes in the plan beyond its units, and the places of a CTA's run.
+// Runs are cut where the units of all tiles and KV heads are laid end to end at places: a unit that few rows see takes
+// 7/6 of one over shared pages (its V is cleaned, its keys come from anywhere), and a tile's drafts with the change of
+// rows behind them kPad more.  32 answers over 128K, own keys on four CTAs a head: these take 63 us of the run's units
+// where the others take 53 without that, 55 with it.
 constexpr int kPad = 2;
-__device__ __forceinline__ int run_places(int units, int tiles) { return (units + kPad * tiles + kSms - 1) / kSms; }
+__device__ __forceinline__ int place_of(int k, int shared) { return k + max(0, k - shared) / 6; }
+__device__ __forceinline__ int unit_at(int place, int shared, int units) {  // the units before a place
+  const int r = max(0, place - shared);
+  return min(place - r / 7, units);
+}
+__device__ __forceinline__ int span_of(int shared, int units) { return place_of(units, shared) + kPad; }
 
 __device__ __forceinline__ void report_arg(const TreeArgs &a) {
   if (a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(BSA_ERR_INVALID_ARG));
@@ -230,6 +238,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
 
   // row tiles
   carry = 0;
+  int places = 0;
   for (int base = 0; base < tiles; base += threads) {
     const int e = base + tid;
     TileRecord r{};
@@ -250,13 +259,16 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
     }
     int total;
     r.first = carry + scan_block(r.units, warps, &total);
-    if (e < tiles) w.tiles[e] = r;
     carry += total;
+    r.place = places + scan_block(e < tiles ? span_of(r.shared, r.units) : 0, warps, &total);
+    places += total;
+    if (e < tiles) w.tiles[e] = r;
   }
   if (tid == 0) {
     w.totals[0] = carry;
     w.totals[1] = tiles;
     w.totals[2] = 0;
+    w.totals[3] = places;
   }
 }
 size_t plan_smem(int batch, int groups) { return (2 * static_cast<size_t>(batch) + 3 * groups + 7) * 4 + groups * sizeof(int4); }
@@ -433,30 +445,34 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
     ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
+  if (!Q16 && tid == 64) {
+    ptx::tma_prefetch_desc(&maps.q);
+    ptx::tma_prefetch_desc(&maps.k);
+    ptx::tma_prefetch_desc(&maps.v);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   after_previous_kernel();  // the plan
   launch_next();
-  // This CTA's run.  Runs are cut where the units and kPad places behind every row tile and KV head are laid end to end:
-  // what a tile's drafts and the change of rows cost more than a unit.
-  const int units_all = wk.totals[0] * a.c.hkv, tiles_all = wk.totals[1];
-  const int places = units_all + kPad * tiles_all * a.c.hkv, W = run_places(units_all, tiles_all * a.c.hkv);
+  // This CTA's run
+  const int units_all = wk.totals[0] * a.c.hkv, tiles_all = wk.totals[1], places = wk.totals[3] * a.c.hkv;
+  const int W = (places + kSms - 1) / kSms;
   // the units before a place
   auto units_before = [&](int place) {
     if (place >= places) return units_all;
     int e = 0, hi = tiles_all;  // the last row tile that begins at or before it, 32 looked at at a time
     while (hi - e > 1) {
       const int step = (hi - e + 31) / 32, at = e + lane * step;
-      const bool before = at < hi && (wk.tiles[at].first + kPad * at) * a.c.hkv <= place;
+      const bool before = at < hi && wk.tiles[at].place * a.c.hkv <= place;
       const int k = __popc(__ballot_sync(0xffffffffu, before));
       hi = min(hi, e + k * step);
       e += (k - 1) * step;
     }
-    const int2 fu = *reinterpret_cast<const int2 *>(&wk.tiles[e].first);
-    const int off = place - (fu.x + kPad * e) * a.c.hkv, g = off / (fu.y + kPad);
-    return fu.x * a.c.hkv + g * fu.y + min(off - g * (fu.y + kPad), fu.y);
+    const TileRecord t = wk.tiles[e];
+    const int span = span_of(t.shared, t.units), off = place - t.place * a.c.hkv, g = off / span;
+    return t.first * a.c.hkv + g * t.units + unit_at(off - g * span, t.shared, t.units);
   };
   const int x0 = tiles_all > 0 ? units_before(cta * W) : 0, x1 = tiles_all > 0 ? units_before(cta * W + W) : 0, nu = x1 - x0;
 
@@ -1245,97 +1261,121 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
 
 // ---------------------------------------------------------------- the combine
 
-// A block is kItems (row, four dimensions) of one token and KV head; its teams take the parts i, i + teams, .. of the
-// token's rows, and the sums are added in a fixed order.
-constexpr int kCombineThreads = 512;
+// A block is kItems (row, four dimensions) of one token and KV head.  The weights of all parts of the token's rows come
+// first, a warp a row; then its teams take the parts i, i + teams, .., and the teams' sums are added in a fixed order.
+constexpr int kCombineThreads = 512, kMaxParts = 2 * (kSms + 1);
 
 template <int D, bool PAIR, int kItems>
 __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const TreeArgs a, const SharedWork wk) {
   constexpr int kSplit = kCombineThreads / kItems;
   constexpr int LANES = PAIR ? 1 : 2;  // results of a row and part
   constexpr int TILE_ROWS = PAIR ? 2 * kRows : kRows;
-  after_previous_kernel();
-  __shared__ float red_m[kSplit][kItems], red_l[kSplit][kItems];
+  extern __shared__ float2 part[];  // [parts][G] maximum (later: weight) and sum
   __shared__ float4 red_o[kSplit][kItems];
+  __shared__ float2 row_ml[16];  // maximum and sum of the rows
   const int G = a.group, items = G * (D / 4), slices = (items + kItems - 1) / kItems;
   const int i = blockIdx.x / slices, g = blockIdx.y, b = blockIdx.z;
+  // (the plan was there before the kernel ahead could let this one start)
   const SeqRecord dr = wk.seqs[b];
-  const int all = wk.totals[0] * a.c.hkv, tiles = wk.totals[1], drafts_odd = wk.totals[2];
-  const uint32_t *mark = wk.odd + static_cast<size_t>(b * a.c.hkv + g) * kOdd;
-  const uint32_t own_odd = mark[0];
+  const int tiles = wk.totals[1], places = wk.totals[3] * a.c.hkv;
   if (i >= dr.len) return;
   const int row0 = (dr.at + i) * G, e = dr.tile0 + row0 / TILE_ROWS;
   if (e >= tiles) return;
-  const int2 fu = *reinterpret_cast<const int2 *>(&wk.tiles[e].first);
-  const int run = run_places(all, tiles * a.c.hkv);
-  const int first = (fu.x + kPad * e) * a.c.hkv + g * (fu.y + kPad), cta0 = first / run, count = (first + fu.y - 1) / run - cta0 + 1;
-  const int tile = row0 % TILE_ROWS / kRows, rr = row0 % kRows;
-
+  const TileRecord tr = wk.tiles[e], prev = wk.tiles[max(e - 1, 0)];
+  const int run = (places + kSms - 1) / kSms, span = span_of(tr.shared, tr.units);
+  const int first = tr.place * a.c.hkv + g * span, cta0 = first / run;
+  const int count = (first + place_of(tr.units - 1, tr.shared)) / run - cta0 + 1;
+  const int tile = row0 % TILE_ROWS / kRows, rr = row0 % kRows, n = count * LANES;
   const int item = threadIdx.x % kItems, team = threadIdx.x / kItems;
   const int it = blockIdx.x % slices * kItems + item, h = it % G, q = it / G;
-  const size_t out = static_cast<size_t>(dr.start + i) * a.hq + g * G + h;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (it < items) {
-    const int n = count * LANES;
-    constexpr int U = 4;  // parts in flight
-    for (int base = team; base < n; base += U * kSplit) {
-      float2 ml[U], ml2[U];
-      float4 v[U];
+  const size_t out0 = static_cast<size_t>(dr.start + i) * a.hq + g * G, out = out0 + h;
+  // a CTA's run begins with this tile if no unit lies between: in the places behind the last unit of the one before too
+  const TileRecord &ahead = g > 0 ? tr : prev;
+  const int before = g > 0 || e > 0 ? first - (span_of(ahead.shared, ahead.units) - place_of(ahead.units - 1, ahead.shared) - 1) : 0;
+  auto slot_of = [&](int x) {
+    const int cta = cta0 + x / LANES;
+    return 2 * (2 * static_cast<size_t>(cta) + (before <= cta * run ? 0 : 1)) + (PAIR ? tile : x & 1);
+  };
+  after_previous_kernel();
+
+  const uint32_t *mark = wk.odd + static_cast<size_t>(b * a.c.hkv + g) * kOdd;
+  const uint32_t own_odd = mark[0];
+  const int drafts_odd = wk.totals[2];
+  constexpr int U = 5;  // parts in flight
+  float4 v[U];
+  auto fetch = [&](int base) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = base + u * kSplit, lane = PAIR ? 0 : x & 1;
-        ml[u] = ml2[u] = make_float2(-INFINITY, 0.f);
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x >= n) continue;
-        if (count == 1) {
-          ml[u] = wk.row_ml[2 * lane * wk.rows + out];
-          ml2[u] = wk.row_ml[(2 * lane + 1) * wk.rows + out];
-          v[u] = reinterpret_cast<const float4 *>(wk.row_o)[(lane * wk.rows + out) * (D / 4) + q];
-        } else {
-          const int cta = cta0 + x / LANES;
-          const size_t slot = 2 * (2 * static_cast<size_t>(cta) + (first - kPad <= cta * run ? 0 : 1)) + (PAIR ? tile : lane);
-          ml[u] = wk.part_ml[slot * 2 * kRows + rr + h];
-          ml2[u] = wk.part_ml[(slot * 2 + 1) * kRows + rr + h];
-          v[u] = reinterpret_cast<const float4 *>(wk.part_o)[(slot * (D / 4) + q) * kRows + rr + h];
-        }
-      }
+    for (int u = 0; u < U; ++u) {
+      const int x = base + u * kSplit;
+      if (x >= n || it >= items) continue;
+      v[u] = count == 1 ? reinterpret_cast<const float4 *>(wk.row_o)[((PAIR ? 0 : x & 1) * wk.rows + out) * (D / 4) + q]
+                        : reinterpret_cast<const float4 *>(wk.part_o)[(slot_of(x) * (D / 4) + q) * kRows + rr + h];
+    }
+  };
+  fetch(team);
+  for (int x = threadIdx.x; x < n * G; x += kCombineThreads) {
+    const int p = x / G, r = x - p * G, lane = PAIR ? 0 : p & 1;
+    float2 ml = make_float2(-INFINITY, 0.f), ml2 = ml;
+    const int from = max(0, (cta0 + p / LANES) * run - first), to = (cta0 + p / LANES + 1) * run - first;
+    if (unit_at(from, tr.shared, tr.units) == unit_at(to, tr.shared, tr.units)) {
+      // (a short run may fall on a place without a unit)
+    } else if (count == 1) {
+      ml = wk.row_ml[2 * lane * wk.rows + out0 + r];
+      ml2 = wk.row_ml[(2 * lane + 1) * wk.rows + out0 + r];
+    } else {
+      const size_t slot = slot_of(p);
+      ml = wk.part_ml[slot * 2 * kRows + rr + r];
+      ml2 = wk.part_ml[(slot * 2 + 1) * kRows + rr + r];
+    }
+    part[x] = make_float2(ptx::max_nan(ml.x, ml2.x), ml.y + ml2.y);  // (the halves differ where one holds NaN alone)
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < G) {
+    float m = -INFINITY, l = 0.f;
+    for (int p = lane; p < n; p += 32) m = ptx::max_nan(m, part[p * G + warp].x);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float pm = ptx::max_nan(ml[u].x, ml2[u].x);  // (the halves differ where one holds NaN alone)
-        if (pm == -INFINITY) continue;
-        const float mn = ptx::max_nan(m, pm);
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(pm - mn);
-        m = mn;
-        l = fmaf(ml[u].y + ml2[u].y, w, l * f);
-        acc.x = fmaf(v[u].x, w, acc.x * f);
-        acc.y = fmaf(v[u].y, w, acc.y * f);
-        acc.z = fmaf(v[u].z, w, acc.z * f);
-        acc.w = fmaf(v[u].w, w, acc.w * f);
-      }
+    for (int o = 16; o > 0; o >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int p = lane; p < n; p += 32) {
+      const float2 ml = part[p * G + warp];
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      l = ml.x == -INFINITY ? l : fmaf(ml.y, w, l);
+      part[p * G + warp].x = w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) row_ml[warp] = make_float2(m, l);
+  }
+  __syncthreads();
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = team; base < n; base += U * kSplit) {
+    if (base != team) fetch(base);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = base + u * kSplit;
+      const float w = x < n && it < items ? part[x * G + h].x : 0.f;
+      if (w == 0.f) continue;  // (a part without a key may hold anything)
+      s.x = fmaf(v[u].x, w, s.x);
+      s.y = fmaf(v[u].y, w, s.y);
+      s.z = fmaf(v[u].z, w, s.z);
+      s.w = fmaf(v[u].w, w, s.w);
     }
   }
-  red_m[team][item] = m;
-  red_l[team][item] = l;
-  red_o[team][item] = acc;
-  __syncthreads();
-  if (team != 0 || it >= items) return;
-  float mm = -INFINITY;
+  if (kSplit > 1) {
+    red_o[team][item] = s;
+    __syncthreads();
+    if (team != 0) return;
 #pragma unroll
-  for (int w = 0; w < kSplit; ++w) mm = ptx::max_nan(mm, red_m[w][item]);
-  float ls = 0.f;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kSplit; ++w) {
-    if (red_m[w][item] == -INFINITY) continue;
-    const float f = exp2f(red_m[w][item] - mm);
-    ls = fmaf(red_l[w][item], f, ls);
-    const float4 v = red_o[w][item];
-    s.x = fmaf(v.x, f, s.x);
-    s.y = fmaf(v.y, f, s.y);
-    s.z = fmaf(v.z, f, s.z);
-    s.w = fmaf(v.w, f, s.w);
+    for (int w = 1; w < kSplit; ++w) {
+      const float4 x = red_o[w][item];
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
   }
+  if (it >= items) return;
+  const float mm = row_ml[h].x, ls = row_ml[h].y;
   float o[4] = {s.x, s.y, s.z, s.w};
   if (own_odd != 0u) {  // Inf and NaN of own values, which every row of the sequence sees
 #pragma unroll
@@ -1436,7 +1476,8 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   const bool small = static_cast<long long>(a.total) * a.c.hkv <= 2 * kSms;
   auto combine = small ? shared_combine_kernel<D, PAIR, 64> : shared_combine_kernel<D, PAIR, 256>;
   const int items = small ? 64 : 256, slices = (a.group * (D / 4) + items - 1) / items;
-  e = launch_after(combine, dim3(a.max_draft * slices, a.c.hkv, a.batch), kCombineThreads, 0, stream, a, w);
+  e = launch_after(combine, dim3(a.max_draft * slices, a.c.hkv, a.batch), kCombineThreads,
+                   static_cast<size_t>(kMaxParts) * a.group * sizeof(float2), stream, a, w);
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
