@@ -5,6 +5,8 @@
 // of rows (growth) and pages (compaction), which HBM bounds.
 #include <stdint.h>
 
+#include <atomic>
+
 #include "bsa_pages.h"
 #include "bsa_tree.cuh"
 
@@ -14,6 +16,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kSms = 152;
+constexpr int kHeld = 4;  // neighbouring pages of a planning thread, of which the first round's counts stay in registers
+
+// Threads of a planning CTA: a round takes all pages, and all sequences, up to kPlanThreads (fewer threads meet sooner).
+int plan_threads(int pages, int batch) {
+  const int want = (pages + kHeld - 1) / kHeld > batch ? (pages + kHeld - 1) / kHeld : batch;
+  return want >= kPlanThreads ? kPlanThreads : want <= 128 ? 128 : (want + 31) / 32 * 32;
+}
 
 __device__ __forceinline__ void report(int32_t *status, bsa_status what) {
   if (status != nullptr) atomicCAS(status, 0, static_cast<int32_t>(what));
@@ -83,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(const TrimArgs a) {
   if (threadIdx.x == 0) a.cached[b] = keep;
 }
 
-// ---------------------------------------------------------------- sums over a block of kPlanThreads
+// ---------------------------------------------------------------- sums over a planning block
 
 // The sum of the values of the threads before this one; *total the whole sum.  `warps`: [33] of shared memory.
 __device__ __forceinline__ int scan_block(int value, int *warps, int *total) {
@@ -98,7 +107,8 @@ __device__ __forceinline__ int scan_block(int value, int *warps, int *total) {
   if (lane == 31) warps[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int w = warps[lane], run = w;
+    const int w = lane < blockDim.x >> 5 ? warps[lane] : 0;
+    int run = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, run, o);
@@ -114,60 +124,81 @@ __device__ __forceinline__ int scan_block(int value, int *warps, int *total) {
 
 // ---------------------------------------------------------------- growth
 
+// The counts of this thread's pages of a round, INT_MIN behind the pool's end.
+struct Held {
+  int refs[kHeld];
+};
+__device__ __forceinline__ Held held_pages(const int32_t *refs, int pages, int round) {
+  Held h;
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) {
+    const int p = (round * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kHeld + e;
+    h.refs[e] = p < pages ? refs[p] : INT32_MIN;
+  }
+  return h;
+}
+__device__ __forceinline__ int rounds_of(int pages) { return (pages + blockDim.x * kHeld - 1) / (blockDim.x * kHeld); }
+
 // One CTA plans: who needs how many pages (a copy of a shared last page among them, unless this is the last sequence
 // that holds it), whether there are enough, and which; sequences and pages in ascending order, so that the outcome is
 // that of one sequence after the other.
 __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs a) {
   extern __shared__ int sm[];
-  int *last = sm, *first = sm + a.batch;  // [batch] partial last page that gets tokens or -1, [batch + 1] first new page
+  // [batch] the partial last page that gets tokens or -1; [batch] where the first new page goes, times 2, and whether
+  // that is a copy; [batch + 1] the first new page
+  int *last = sm, *goes = sm + a.batch, *first = goes + a.batch;
   __shared__ int warps[33];
   __shared__ int carry;
-  const int tid = threadIdx.x, shift = a.c.page_shift, mask = a.c.page - 1;
-  auto wanted = [&](int b, int n) -> int {  // tokens sequence b grows by
+  const int tid = threadIdx.x, threads = blockDim.x, shift = a.c.page_shift, mask = a.c.page - 1;
+  launch_next();
+  struct Seq {
+    int n, g, page, refs;  // tokens, those it grows by, its partial last page (-1: none) and the count of that
+  };
+  auto read = [&](int b) -> Seq {
+    Seq s{held(a.cached, b, shift, a.stride, a.status), 0, -1, 0};
     const int t0 = a.cu[b], t1 = a.cu[b + 1];
     if (t0 < 0 || t1 < t0 || t1 > a.total) {
       report(a.status, BSA_ERR_INVALID_ARG);
-      return 0;
+      return s;
     }
-    const int g = a.grow == nullptr ? t1 - t0 : a.grow[b];
-    if (g < 0 || g > t1 - t0 || n > INT32_MAX - g || pages_of(n + g, shift) > a.stride) {
+    s.g = a.grow == nullptr ? t1 - t0 : a.grow[b];
+    if (s.g < 0 || s.g > t1 - t0 || s.n > INT32_MAX - s.g || pages_of(s.n + s.g, shift) > a.stride) {
       report(a.status, BSA_ERR_INVALID_ARG);
-      return 0;
+      s.g = 0;
     }
-    return g;
-  };
-  for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const int n = held(a.cached, b, shift, a.stride, a.status), g = wanted(b, n);
-    int page = -1;
-    if (g > 0 && (n & mask) != 0) {
-      page = a.table[static_cast<size_t>(b) * a.stride + (n >> shift)];
-      if (page < 0 || page >= a.c.pages) {
+    if (s.g > 0 && (s.n & mask) != 0) {
+      s.page = a.table[static_cast<size_t>(b) * a.stride + (s.n >> shift)];
+      if (s.page < 0 || s.page >= a.c.pages) {
         report(a.status, BSA_ERR_INVALID_ARG);
-        page = -1;
+        s.page = -1;
+        s.g = 0;
+      } else {
+        s.refs = a.refs[s.page];
       }
     }
-    last[b] = page;
+    return s;
+  };
+  const Held round0 = held_pages(a.refs, a.c.pages, 0);
+  Seq seq0{0, 0, -1, 0};  // the first round's stays in registers
+  for (int b = tid; b < a.batch; b += threads) {
+    const Seq s = read(b);
+    if (b == tid) seq0 = s;
+    last[b] = s.page;
   }
   if (tid == 0) carry = 0;
   __syncthreads();
-  for (int base = 0; base < a.batch; base += kPlanThreads) {
+  for (int base = 0; base < a.batch; base += threads) {
     const int b = base + tid;
     int need = 0;
     if (b < a.batch) {
-      const int n = held(a.cached, b, shift, a.stride, nullptr), page = last[b];
-      int g = wanted(b, n);
-      const bool lost = g > 0 && (n & mask) != 0 && page < 0;  // its last page is not in the cache
-      if (lost) g = 0;
-      bool copy = false;
-      if (page >= 0) {
-        const int refs = a.refs[page];
-        int earlier = 0;
-        if (refs > 1)
-          for (int x = 0; x < b; ++x) earlier += last[x] == page ? 1 : 0;
-        copy = refs - earlier > 1;
-      }
-      need = g == 0 ? 0 : pages_of(n + g, shift) - pages_of(n, shift) + (copy ? 1 : 0);
-      a.jobs[b] = GrowJob{g > 0 ? n : -1, copy ? page : -1, -1, copy ? n & mask : 0};
+      const Seq s = base == 0 ? seq0 : read(b);
+      int earlier = 0;
+      if (s.refs > 1)
+        for (int x = 0; x < b; ++x) earlier += last[x] == s.page ? 1 : 0;
+      const bool copy = s.refs - earlier > 1;
+      need = s.g == 0 ? 0 : pages_of(s.n + s.g, shift) - pages_of(s.n, shift) + (copy ? 1 : 0);
+      goes[b] = 2 * (pages_of(s.n, shift) - (copy ? 1 : 0)) + (copy ? 1 : 0);
+      a.jobs[b] = GrowJob{s.g > 0 ? s.n : -1, copy ? s.page : -1, -1, copy ? s.n & mask : 0};
     }
     int total;
     const int before = scan_block(need, warps, &total);
@@ -179,42 +210,66 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
   const int total = carry;
   if (tid == 0) first[a.batch] = total;
   __syncthreads();
-  // the free pages, lowest first: counted until there are enough, then given out
-  for (int pass = 0; pass < 2 && total > 0; ++pass) {
-    int found = 0;
-    for (int base = 0; base < a.c.pages && found < total; base += kPlanThreads) {
-      const int p = base + tid;
-      const bool is_free = p < a.c.pages && a.refs[p] == 0;
-      int n;
-      const int k = found + scan_block(is_free ? 1 : 0, warps, &n);
-      if (pass == 1 && is_free && k < total) {
+
+  // the free pages, lowest first
+  auto free_of = [&](const Held &h) {
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) n += h.refs[e] == 0 ? 1 : 0;
+    return n;
+  };
+  auto give = [&](const Held &h, int round, int k) {  // k: the free pages before this thread's
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      if (h.refs[e] != 0) continue;
+      const int p = (round * threads + tid) * kHeld + e;
+      if (k < total) {
         int lo = 0, hi = a.batch - 1;
         while (lo < hi) {  // the last sequence whose first new page is at or before k: the one that gets it
           const int mid = (lo + hi + 1) >> 1;
           if (first[mid] <= k) lo = mid;
           else hi = mid - 1;
         }
-        GrowJob &job = a.jobs[lo];
-        const int copies = job.from >= 0 ? 1 : 0;
-        const int at = pages_of(job.start, shift) - copies + k - first[lo];
-        if (copies && k == first[lo]) job.to = p;
-        a.table[static_cast<size_t>(lo) * a.stride + at] = p;
+        const int to = goes[lo];
+        if ((to & 1) != 0 && k == first[lo]) a.jobs[lo].to = p;
+        a.table[static_cast<size_t>(lo) * a.stride + (to >> 1) + k - first[lo]] = p;
         a.refs[p] = 1;
       }
-      found += n;
+      ++k;
     }
-    __syncthreads();
+  };
+  if (total > 0) {
+    int n;
+    const int k0 = scan_block(free_of(round0), warps, &n);
+    const int rounds = rounds_of(a.c.pages);
+    int found = n;
+    for (int r = 1; r < rounds && found < total; ++r) {
+      int more;
+      scan_block(free_of(held_pages(a.refs, a.c.pages, r)), warps, &more);
+      found += more;
+    }
     if (found < total) {  // not enough: nobody grows
       if (tid == 0) report(a.status, BSA_ERR_WORKSPACE);
-      for (int b = tid; b < a.batch; b += kPlanThreads) a.jobs[b] = GrowJob{-1, -1, -1, 0};
+      for (int b = tid; b < a.batch; b += threads) a.jobs[b] = GrowJob{-1, -1, -1, 0};
       return;
     }
+    give(round0, 0, k0);
+    for (int r = 1; n < total; ++r) {
+      const Held h = held_pages(a.refs, a.c.pages, r);
+      int more;
+      const int k = n + scan_block(free_of(h), warps, &more);
+      give(h, r, k);
+      n += more;
+    }
   }
-  for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const GrowJob job = a.jobs[b];
-    if (job.start < 0) continue;
-    if (job.from >= 0) atomicSub(a.refs + job.from, 1);
-    a.cached[b] = job.start + wanted(b, job.start);
+  for (int base = 0; base < a.batch; base += threads) {
+    const int b = base + tid;
+    if (b >= a.batch) break;
+    const int from = (goes[b] & 1) != 0 ? last[b] : -1;
+    if (from >= 0) atomicSub(a.refs + from, 1);
+    const int n = base == 0 ? seq0.n : held(a.cached, b, shift, a.stride, nullptr);
+    const int g = base == 0 ? seq0.g : a.jobs[b].start < 0 ? 0 : a.grow == nullptr ? a.cu[b + 1] - a.cu[b] : a.grow[b];
+    if (g > 0) a.cached[b] = n + g;
   }
 }
 
@@ -275,25 +330,44 @@ __global__ void __launch_bounds__(kThreads) grow_rows_kernel(const GrowArgs a, i
 // One CTA: with L pages in use, the pages in use from L on go, in order, to the free ones below L.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
   __shared__ int warps[33];
-  const int tid = threadIdx.x, pages = a.c.pages;
+  const int tid = threadIdx.x, threads = blockDim.x, pages = a.c.pages, rounds = rounds_of(pages);
   int *holes = a.work + 4, *moved = holes + pages, *to = moved + pages;
+  launch_next();
+  const Held round0 = held_pages(a.refs, pages, 0);
   int live = 0;
-  for (int base = 0; base < pages; base += kPlanThreads) live += __syncthreads_count(base + tid < pages && a.refs[base + tid] > 0);
+  for (int r = 0; r < rounds; ++r) {
+    const Held h = r == 0 ? round0 : held_pages(a.refs, pages, r);
+    int used = 0, n;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) used += h.refs[e] > 0 ? 1 : 0;
+    scan_block(used, warps, &n);
+    live += n;
+  }
   int nh = 0, nm = 0;
-  for (int base = 0; base < pages; base += kPlanThreads) {
-    const int p = base + tid;
-    const bool used = p < pages && a.refs[p] > 0;
-    const bool hole = p < live && !used, mover = p >= live && used;
-    int n;
-    const int k = scan_block((hole ? 1 : 0) + (mover ? 0x10000 : 0), warps, &n);  // (at most 1024 of each a round)
-    if (hole) holes[nh + (k & 0xFFFF)] = p;
-    if (mover) moved[nm + (k >> 16)] = p;
-    if (p >= live && p < pages && !used) to[p] = -1;  // (no entry should name it)
+  for (int r = 0; r < rounds; ++r) {
+    const Held h = r == 0 ? round0 : held_pages(a.refs, pages, r);
+    const int p0 = (r * threads + tid) * kHeld;
+    int mine = 0, n;  // holes, and times 2^16 pages that move (at most 4096 of each a round)
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int p = p0 + e;
+      mine += p < live && h.refs[e] <= 0 ? 1 : p >= live && h.refs[e] > 0 ? 0x10000 : 0;
+    }
+    const int k = scan_block(mine, warps, &n);
+    int hole = nh + (k & 0xFFFF), move = nm + (k >> 16);
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int p = p0 + e;
+      if (p >= pages) break;
+      if (p < live && h.refs[e] <= 0) holes[hole++] = p;
+      if (p >= live && h.refs[e] > 0) moved[move++] = p;
+      if (p >= live && h.refs[e] <= 0) to[p] = -1;  // (no entry should name it)
+    }
     nh += n & 0xFFFF;
     nm += n >> 16;
   }
   __syncthreads();
-  for (int i = tid; i < nm; i += kPlanThreads) {
+  for (int i = tid; i < nm; i += threads) {
     const int src = moved[i], dst = holes[i];
     to[src] = dst;
     a.refs[dst] = a.refs[src];
@@ -354,9 +428,12 @@ cudaError_t launch_trim(const TrimArgs &a, cudaStream_t stream) {
 size_t grow_workspace_bytes(int batch) { return static_cast<size_t>(batch) * sizeof(GrowJob); }
 
 cudaError_t launch_grow(const GrowArgs &a, cudaStream_t stream) {
-  grow_plan_kernel<<<1, kPlanThreads, (2 * a.batch + 1) * sizeof(int), stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  auto smem_of = [](int batch) { return (3 * static_cast<size_t>(batch) + 1) * sizeof(int); };
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_up(grow_plan_kernel, smem_of(kMaxDecodeRows), 0, done);
   if (e != cudaSuccess) return e;
+  grow_plan_kernel<<<1, plan_threads(a.c.pages, a.batch), smem_of(a.batch), stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int want = (a.total + kThreads - 1) / kThreads, slot_blocks = want < kSms ? want : kSms;
   return launch_after(grow_rows_kernel, dim3(slot_blocks + a.batch * a.c.hkv * 2), kThreads, 0, stream, a, slot_blocks);
 }
@@ -364,7 +441,7 @@ cudaError_t launch_grow(const GrowArgs &a, cudaStream_t stream) {
 size_t compact_workspace_bytes(int pages) { return (4 + 3 * static_cast<size_t>(pages)) * 4; }
 
 cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream) {
-  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  compact_plan_kernel<<<1, plan_threads(a.c.pages, 1), 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(compact_move_kernel, dim3(kSms * 8), kThreads, 0, stream, a);
