@@ -395,20 +395,28 @@ __global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArg
     if (q < 0) report(a.status, BSA_ERR_INVALID_ARG);
     else if (q != p) a.table[e] = q;
   }
-  const size_t tile[2] = {static_cast<size_t>(a.c.hkv) * a.c.page * a.c.row,
-                          static_cast<size_t>(a.c.hkv) * a.c.page * a.c.per_row};
-  const int planes = a.c.per_row == 0 ? 2 : 4;
-  for (int plane = 0; plane < planes; ++plane) {
-    const size_t bytes = tile[plane >> 1];  // a page's, a multiple of 64
-    const size_t n16 = bytes / 16;
-    const long long all = static_cast<long long>(n16) * moves;
-    uint4 *at = reinterpret_cast<uint4 *>(a.planes[plane]);
-    for (long long e = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; e < all;
-         e += static_cast<long long>(gridDim.x) * kThreads) {
-      const int i = static_cast<int>(e / static_cast<long long>(n16));
-      const size_t o = static_cast<size_t>(e - static_cast<long long>(i) * static_cast<long long>(n16));
-      at[static_cast<size_t>(holes[i]) * n16 + o] = at[static_cast<size_t>(moved[i]) * n16 + o];
-    }
+  // a block takes pieces of a page's part of an array, codes first; four loads of a thread under way
+  constexpr int kPiece = 4 * kThreads;  // times 16 bytes
+  const int n16[2] = {static_cast<int>(static_cast<size_t>(a.c.hkv) * a.c.page * a.c.row / 16),
+                      static_cast<int>(static_cast<size_t>(a.c.hkv) * a.c.page * a.c.per_row / 16)};
+  const int codes = (n16[0] + kPiece - 1) / kPiece, scales = (n16[1] + kPiece - 1) / kPiece, pieces = 2 * (codes + scales);
+  for (long long e = blockIdx.x; e < static_cast<long long>(moves) * pieces; e += gridDim.x) {
+    const int i = static_cast<int>(e / pieces);
+    int x = static_cast<int>(e - static_cast<long long>(i) * pieces);
+    const int kind = x < 2 * codes ? 0 : 1, each = kind == 0 ? codes : scales, n = n16[kind];
+    x -= kind == 0 ? 0 : 2 * codes;
+    const int kv = x >= each ? 1 : 0;
+    uint4 *plane = reinterpret_cast<uint4 *>(a.planes[2 * kind + kv]);
+    const uint4 *from = plane + static_cast<size_t>(moved[i]) * n;
+    uint4 *to_page = plane + static_cast<size_t>(holes[i]) * n;
+    const int at = (x - kv * each) * kPiece + threadIdx.x;
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (at + u * kThreads < n) v[u] = __ldcs(from + at + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (at + u * kThreads < n) __stcs(to_page + at + u * kThreads, v[u]);
   }
 }
 
