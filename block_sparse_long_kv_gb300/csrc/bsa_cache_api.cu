@@ -344,6 +344,7 @@ bsa_status bsa_cache_fork(const bsa_cache_shape *shape, int32_t batch, int32_t b
     if (overlap(cached_out, 4ull * batch_out, from[i], in[i]) ||
         overlap(table_out, 4ull * batch_out * table_stride, from[i], in[i]))
       return BSA_ERR_INVALID_ARG;
+  if (overlap(cached_out, 4ull * batch_out, table_out, 4ull * batch_out * table_stride)) return BSA_ERR_INVALID_ARG;
   const bsa::ForkArgs a{source, cached, block_table, refs, cached_out, table_out, dev_status, c.pages, c.page_shift,
                         batch, batch_out, table_stride};
   return bsa::launch_fork(a, cu_stream(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;

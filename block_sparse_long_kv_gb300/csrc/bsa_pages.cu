@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
   };
   auto read = [&](int b) -> Seq {
     Seq s{held(a.cached, b, shift, a.stride, a.status), 0, -1, 0};
+    if (a.cached[b] != s.n) return s;  // (reported)
     const int t0 = a.cu[b], t1 = a.cu[b + 1];
     if (t0 < 0 || t1 < t0 || t1 > a.total) {
       report(a.status, BSA_ERR_INVALID_ARG);

@@ -613,14 +613,22 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
  * pages are read from the table of the group's first sequence that drafts a
  * token; a sequence without drafts takes no part and needs no pages.
  *
- * What is rounded: as stated at bsa_tree_fwd for more than 16 rows.
+ * Inf and NaN in q, k_new, v_new and in a sequence's own cached keys and values
+ * (those behind the shared pages) go into the rows that attend to them, of values
+ * into those dimensions, and into no other row.
+ *
+ * What is rounded: as stated at bsa_tree_fwd for more than 16 rows, but over an 8-
+ * or 4-bit cache rows of a group's sequences are computed together, so the largest
+ * |v| is that of the cached and drafted tokens of all of them.
  *
  * Limits: as bsa_tree_fwd, but max_cached may be any number of pages up to
- * table_stride; groups <= 4096.  The device checks what bsa_tree_fwd's does, and: of a cu_group entry that is
- * inconsistent, or a shared_pages entry below 0 or past max_cached, it sets
- * BSA_ERR_INVALID_ARG in *dev_status and the group shares no pages; a sequence of no
- * group, or of such a one, attends to all its pages by itself; one that drafts but holds fewer
- * tokens than the group's pages sets it and attends to the group's pages.
+ * table_stride; groups <= 4096; total_draft * hq < 2^31.  The device checks what
+ * bsa_tree_fwd's does, and sets BSA_ERR_INVALID_ARG in *dev_status too
+ *   - where cu_group does not ascend from 0 to batch: nothing is computed, o and
+ *     lse stay as they were;
+ *   - for a shared_pages entry below 0 or past max_cached: the group shares none;
+ *   - for a sequence that drafts but holds fewer tokens than the group's pages:
+ *     it attends to the group's pages and its drafts.
  * workspace: bsa_shared_workspace_bytes bytes, 16-byte aligned, the caller's
  * alone while the call runs (two graphs that may replay at the same time need one each).
  * ------------------------------------------------------------------------ */
@@ -643,8 +651,8 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * sequence's cached[b] tokens, ceil(cached[b] / page) of them; entries behind
  * those are -1 or left as they were.  refs (int32 [pages]) counts the entries
  * that name a page: 0 is a free page, and all zeros an empty pool.  These calls keep
- * both in step; they run on the device alone, so a step that forks, grows and
- * trims can be captured.  Free pages are given out lowest first, to sequences in ascending order.
+ * both in step.  They run on the device alone, so a step that forks, grows and
+ * trims can be captured; calls over one pool follow one another on a stream.  Free pages are given out lowest first, to sequences in ascending order.
  *
  * bsa_cache_fork: the rows of table_out [batch_out, table_stride] and
  * cached_out [batch_out] take the place of those of block_table: row j is a
@@ -658,7 +666,8 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * that others share is replaced by a copy of its rows (the last sequence that
  * still holds it keeps it).  slots[t] (int32 [total_new], for bsa_cache_write)
  * is the place of token t: the position cached[b] + rank[t] (rank nullable: t -
- * cu_new[b]), or -1 where rank[t] is not in [0, grow[b]).  cached, block_table
+ * cu_new[b]), or -1 where rank[t] is not in [0, grow[b]); the ranks of a sequence
+ * are distinct, as the slots of bsa_cache_write must be.  cached, block_table
  * and refs are updated in place, and rows of the cache are copied in all its
  * arrays.  When the pool lacks pages nothing changes: *dev_status is set to
  * BSA_ERR_WORKSPACE and every slot is -1.  A sequence whose row cannot hold the
@@ -672,8 +681,8 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  *
  * bsa_cache_compact: with L pages in use, the pages in use from L on move, in
  * ascending order, to the free ones below L, in ascending order; the tables and
- * refs follow, and *live = L (int32).  Pages from L on are free afterwards.  block_table must hold every
- * entry that refs counts.
+ * refs follow, and *live = L (int32).  Pages from L on are free afterwards.
+ * block_table must hold every entry that refs counts.
  *
  * Entries and counts that do not fit together set BSA_ERR_INVALID_ARG and are
  * left out.  All int32 arrays 4-byte aligned, workspaces 16-byte.
@@ -716,9 +725,11 @@ bsa_status bsa_cache_compact(const bsa_cache_shape *shape, int32_t batch, int32_
  *   rank[t]    token t's place in the path, 0 for the first, -1 if not taken; with
  *              count what bsa_cache_grow takes as rank and grow
  * p, q: fp32 or bf16 (`type`), probabilities in [0, 1] that add up to about 1 in
- * every row; what is negative or NaN counts as 0, what is larger as 1.  u_accept
+ * every row (the token drawn from a row whose sum reaches 16 is any); what is
+ * negative or NaN counts as 0, what is larger as 1.  u_accept
  * [total_draft] and u_sample [batch] in [0, 1), fp32 (of u_sample, 1 and more or NaN takes the
- * last token that has anything left).  Sums are exact in units of 2^-60.  Another root, a
+ * last token that has anything left).  Sums and what is left are integers in units of
+ * 2^-60: what is smaller counts as nothing.  A row with nothing gives token 0.  Another root, a
  * parent that is not smaller than its token or an id outside the vocabulary (the last two set
  * BSA_ERR_INVALID_ARG in *dev_status) is not reached.  rank past cu_draft[batch] is left as it was.  Limits: max_draft <= 256
  * and <= total_draft, vocab <= 2^22, batch <= 65535, strides in elements, at least vocab and at most 2^30; p and q
