@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         next = v0 + found * kTile + first * kLane + __shfl_sync(0xffffffffu, e, first);
       }
     }
-    if (lane == 0) a.next[b] = next;
+    if (lane == 0) a.next[b] = max(next, 0);  // (-1: the sum has wrapped)
   }
   if (me == 0) {
     if (tid == 0) {
