@@ -154,17 +154,20 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
   __shared__ int warps[33];
   const int threads = blockDim.x, tid = threadIdx.x, G = a.group, tile_tokens = tile_rows / G;
   launch_next();
-  for (int b = tid; b <= a.batch; b += threads) cu[b] = __ldg(a.cu + b);
-  for (int y = tid; y <= a.groups; y += threads) cu_group[y] = __ldg(a.cu_group + y);
+  // (one round of reads for what `threads` hold: a read behind a store of another's result would wait for that)
+  const int c0 = tid <= a.batch ? __ldg(a.cu + tid) : 0, g0 = tid <= a.groups ? __ldg(a.cu_group + tid) : 0;
+  const int p0 = tid < a.groups ? __ldg(a.shared_pages + tid) : 0;
+  const int n_first = tid < a.batch ? cached_of(a, tid) : 0;
+  for (int b = tid; b <= a.batch; b += threads) cu[b] = b == tid ? c0 : __ldg(a.cu + b);
+  for (int y = tid; y <= a.groups; y += threads) cu_group[y] = y == tid ? g0 : __ldg(a.cu_group + y);
   for (int y = tid; y < a.groups; y += threads) {
-    int p = __ldg(a.shared_pages + y);
+    int p = y == tid ? p0 : __ldg(a.shared_pages + y);
     if (p < 0 || p > a.max_cached >> a.c.page_shift) {
       report_arg(a);
       p = 0;
     }
     pages_of[y] = p;
   }
-  int n_first = tid < a.batch ? cached_of(a, tid) : 0;  // (in the same round)
   for (int x = tid; x < a.batch * a.c.hkv * kOdd; x += threads) w.odd[x] = 0u;
   __syncthreads();
   // groups that do not divide the batch up: nothing is computed
@@ -1263,7 +1266,7 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
 
 // A block is kItems (row, four dimensions) of one token and KV head.  The weights of all parts of the token's rows come
 // first, a warp a row; then its teams take the parts i, i + teams, .., and the teams' sums are added in a fixed order.
-constexpr int kCombineThreads = 512, kMaxParts = 2 * (kSms + 1);
+constexpr int kCombineThreads = 256, kMaxParts = 2 * (kSms + 1);
 
 template <int D, bool PAIR, int kItems>
 __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const TreeArgs a, const SharedWork wk) {
@@ -1330,8 +1333,8 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const T
     part[x] = make_float2(ptx::max_nan(ml.x, ml2.x), ml.y + ml2.y);  // (the halves differ where one holds NaN alone)
   }
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < G) {
+  const int lane = threadIdx.x & 31;
+  for (int warp = threadIdx.x >> 5; warp < G; warp += kCombineThreads / 32) {  // a warp a row
     float m = -INFINITY, l = 0.f;
     for (int p = lane; p < n; p += 32) m = ptx::max_nan(m, part[p * G + warp].x);
 #pragma unroll
@@ -1472,10 +1475,17 @@ bsa_status launch_t(const TreeArgs &a, void *workspace, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   e = launch_after(kern, dim3(kSms), C::THREADS, C::SMEM, stream, maps, a, w);
   if (e != cudaSuccess) return BSA_ERR_CUDA;
-  // few rows: small blocks, so that many teams share a row's parts; many rows: a block is a whole token's
-  const bool small = static_cast<long long>(a.total) * a.c.hkv <= 2 * kSms;
-  auto combine = small ? shared_combine_kernel<D, PAIR, 64> : shared_combine_kernel<D, PAIR, 256>;
-  const int items = small ? 64 : 256, slices = (a.group * (D / 4) + items - 1) / items;
+  // Teams to a row's parts: as many as let all blocks run at once (1024 threads an SM).  A step of 32 answers over 128K (4 KV
+  // heads, 38 parts a row) with 2, 4, 8, 16 teams: 81, 77, 79, 86 us; of 8 answers (76 parts) with 8, 16: 87, 85.
+  const long long threads = static_cast<long long>(a.total) * a.c.hkv * a.group * (D / 4);
+  int items = kCombineThreads;
+  while (items > 16 && threads * (2 * kCombineThreads / items) <= 1024ll * kSms) items /= 2;
+  auto combine = items == 16    ? shared_combine_kernel<D, PAIR, 16>
+                 : items == 32  ? shared_combine_kernel<D, PAIR, 32>
+                 : items == 64  ? shared_combine_kernel<D, PAIR, 64>
+                 : items == 128 ? shared_combine_kernel<D, PAIR, 128>
+                                : shared_combine_kernel<D, PAIR, 256>;
+  const int slices = (a.group * (D / 4) + items - 1) / items;
   e = launch_after(combine, dim3(a.max_draft * slices, a.c.hkv, a.batch), kCombineThreads,
                    static_cast<size_t>(kMaxParts) * a.group * sizeof(float2), stream, a, w);
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
