@@ -33,6 +33,12 @@
 // Inf and NaN of a value that some rows of the tile do not see would reach them (p = 0, and 0 times them is not 0):
 // they are taken out of the product, and the combine adds them to the rows that see them.
 // Every mbarrier wait is bounded, as in the prefill kernel.
+//
+// Measured (32 / 4 heads of 128): 32 answers over 128K in bf16 78 us (295 MB, 3.8 TB/s, 0.88 PFLOP/s), 8 answers 67 (bf16),
+// 78 (e4m3), 75 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 9 pass before the first product
+// (plan, look-ups, first tile) and 9 after the last (parts through the L2, combine).  bf16: 3300 cycles a unit and pair of
+// row tiles, 2150 of them products; the thread that issues them sets the pace (P released in halves: 90 us, waits that
+// spin: 82).  Codes: issue slots and instruction supply; unrolled loops are slower.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -9,8 +9,11 @@
 // where a child was refused and a sibling follows, and once for the token that is drawn.  A cluster of CTAs shares a
 // row.  M and the running sums are integers in units of 2^-60 (a probability's 24 bits shifted, products truncated
 // there), so that no order of summation moves a border; a border in 64-bit floating point is off by as much.
-// Bound by the two rows (p, and q where a token was refused) of every sequence, and by the latency of a walk of
-// dependent decisions.
+// What is left of a row stays in shared memory from refusal to refusal, so that each reads one more row of q; 8 bytes an
+// element, as far as a second CTA still fits beside this one.
+// Bound by the latency of a walk of dependent decisions, not by its bytes: 32 trees of 32 tokens over 131072 ids (34 MB,
+// 5 us of them) take 44 us, as long as the sequence with most refusals (104 with rows read anew each time); 19 chains of
+// 8 over 50021 ids 9.6; one chain of 4 over 32768 ids 7.
 #include <stdint.h>
 
 #include <atomic>
