@@ -88,12 +88,12 @@ bsa_status check_shared(const bsa_shared_shape *s, const bsa::CacheDims &c, int 
   if (s->max_draft > 256) return BSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(s->batch) * c.hkv > bsa::kMaxDecodeRows || s->groups > bsa::kMaxDecodeRows)
     return BSA_ERR_UNSUPPORTED;
-  // the units of a plan are counted in 32 bits: at most these, of 128 keys and 128 rows
+  // the units of a plan and their places are counted in 32 bits: at most these, of 128 keys and 128 rows
   const long long shared_tiles = static_cast<long long>(s->total_draft) * g / 128 + s->groups;
   const long long own_tiles = ((static_cast<long long>(s->max_draft) * g + 127) / 128 + 1) * s->batch;
-  const long long units = pages * (c.page / 64) + 4;
+  const long long units = pages * (c.page / 64) + 8;
   if (static_cast<long long>(s->total_draft) * s->hq > INT32_MAX) return BSA_ERR_UNSUPPORTED;
-  if (static_cast<double>(shared_tiles + own_tiles) * static_cast<double>(units) * c.hkv > INT32_MAX)
+  if (static_cast<double>(shared_tiles + own_tiles) * static_cast<double>(units) * c.hkv > INT32_MAX / 2)
     return BSA_ERR_UNSUPPORTED;
   *group = g;
   return BSA_OK;

@@ -176,8 +176,10 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
   }
   for (int x = tid; x < a.batch * a.c.hkv * kOdd; x += threads) w.odd[x] = 0u;
   __syncthreads();
-  // groups that do not divide the batch up: nothing is computed
+  // groups that do not divide the batch up, or sequences whose tokens do not follow one another: nothing is computed (the
+  // host's bounds on the numbers of tiles and units hold for those that do)
   bool bad = false;
+  for (int b = tid; b < a.batch; b += threads) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > a.total;
   for (int y = tid; y < a.groups; y += threads)
     bad |= cu_group[y + 1] < cu_group[y] || (y == 0 && cu_group[y] != 0) || (y == a.groups - 1 && cu_group[y + 1] != a.batch);
   bad = __syncthreads_or(bad) != 0;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
     int4 rec = make_int4(0, 0, 0, 0);  // first tile, first token, tokens, the sequence whose table counts
     if (y < a.groups && !bad) {
       const int first = cu_group[y], last = cu_group[y + 1], start = cu[first], end = cu[last];
-      if (first < last && start >= 0 && end >= start && end <= a.total) {  // (otherwise its sequences report it)
+      if (first < last) {
         int b = first;
         while (b + 1 < last && cu[b + 1] == start) ++b;
         rec = make_int4(0, start, end - start, b);
@@ -226,7 +228,6 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
         r.first_page = pages_of[y];
         r.at = r.start - g.y;
         r.tile0 = g.x;
-        if (r.at < 0 || r.at + r.len > g.z) r.len = 0;  // (offsets that do not ascend)
         r.keys = n - (r.first_page << a.c.page_shift);
         if (r.keys < 0) {  // its table does not hold the group's pages
           if (r.len > 0) report_arg(a);
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const TreeArgs a, con
       r.chunks = pages_of[y] << (a.c.page_shift - 6);
       r.shared = (r.chunks + 1) / 2;
       r.table = g.w;
-      r.draft0 = max(0, min(r.tok0, cu[r.seq_a]));
+      r.draft0 = max(cu[r.seq_a], r.tok0 - a.max_draft + 1);  // (a longer sequence reads as none)
       r.own = own_before[r.seq_b] - own_before[r.seq_a];
       r.units = r.shared + r.own + (r.tok0 + r.tokens - r.draft0 + kUnit - 1) / kUnit;
     }

@@ -624,8 +624,8 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
  * Limits: as bsa_tree_fwd, but max_cached may be any number of pages up to
  * table_stride; groups <= 4096; total_draft * hq < 2^31.  The device checks what
  * bsa_tree_fwd's does, and sets BSA_ERR_INVALID_ARG in *dev_status too
- *   - where cu_group does not ascend from 0 to batch: nothing is computed, o and
- *     lse stay as they were;
+ *   - where cu_group does not ascend from 0 to batch, or cu_draft within 0 and
+ *     total_draft: nothing is computed, o and lse stay as they were;
  *   - for a shared_pages entry below 0 or past max_cached: the group shares none;
  *   - for a sequence that drafts but holds fewer tokens than the group's pages:
  *     it attends to the group's pages and its drafts.

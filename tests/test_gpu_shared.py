@@ -295,9 +295,27 @@ def test_bad_lengths_and_offsets():
     # a length past max_cached reads as an empty cache, which lacks those pages
     o, lse = c.run(want_status=1, cached=i32([c.lengths[0], 1 << 30, c.lengths[2]]))
     c.check(o, lse, drop=lambda b: np.arange(c.lengths[b]) < (64 if b == 1 else 1 << 30))
-    # a drafted range that is none: that sequence reads as without drafts (5 is past its 3, 7 past the total)
-    for cu in ([0, 2, 1, 6], [0, 2, 7, 6], [0, -1, 5, 6], [0, 2, 1 << 30, 6]):
-        c.run(want_status=1, cu_draft=i32(cu))
+    # offsets that do not follow one another: nothing is computed
+    for cu in ([0, 2, 1, 6], [0, 2, 7, 6], [0, -1, 5, 6], [0, 2, 1 << 30, 6], [0, 2, 5, 7], [-(1 << 31), 2, 5, 6]):
+        o, lse = c.run(want_status=1, cu_draft=i32(cu))
+        assert torch.isnan(o).all() and torch.isnan(lse).all(), cu
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group", [1, 16])
+def test_a_sequence_with_more_drafts_than_the_shape_allows(fmt, group):
+    """It reads as without drafts, and its tokens' rows stay as they were; those before and behind it are computed."""
+    c = Case(fmt, [(1, [3, 70, 10], [2, 300, 3])], group, 1, 64, 64, seed=17)
+    shape, a = c.args()
+    shape = c.bsa.make_shared_shape(1, 3, 305, 3, max(c.lengths), group, c.stride)
+    o = torch.full((305, group, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st = i32([0])
+    ws = torch.full((c.bsa.shared_workspace_bytes(shape, c.cs),), 0xFF, dtype=torch.uint8, device="cuda")
+    c.bsa.shared_fwd(shape, c.cs, a["cu_group"], a["shared_pages"], a["cu_draft"], a["cached"], a["block_table"], a["parents"],
+                     a["q"], a["k_new"], a["v_new"], c.cache, 0.125, o, None, ws, st)
+    torch.cuda.synchronize()
+    assert st.item() == 1 and torch.isnan(o[2:302]).all()
+    c.check(o, None, only=[0, 2])
 
 
 def test_a_parent_that_is_none():
