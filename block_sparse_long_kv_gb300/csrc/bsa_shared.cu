@@ -910,7 +910,6 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         // loaders of codes 16 at a time and loops stay loops: what all the warps of a scheduler run has to fit its
         // instruction cache.
         uint32_t sr[Q16 ? 16 : 32];
-        auto seen = [&](int c) { return (c < 2 ? see0 : see1) >> (16 * (c & 1)); };  // of columns 16 c ..
         float top = -INFINITY;
         if constexpr (Q16) {
           if (any && !masked) {
@@ -923,15 +922,20 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
               top = fmaxf(top, mx);
             }
             if (!on) top = -INFINITY;
-          } else if (any) {
+          } else if (any) {  // (written back masked, so that the loop below knows no masks)
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               ptx::tmem_ld16(tS + c * 16, sr);
               ptx::tmem_wait_ld();
-              const uint32_t see = seen(c);
+              const uint32_t see = (c < 2 ? see0 : see1) >> (16 * (c & 1));
 #pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, (see >> e) & 1u ? __uint_as_float(sr[e]) : -INFINITY);
+              for (int e = 0; e < 16; ++e) {
+                if (!((see >> e) & 1u)) sr[e] = 0xFF800000u;
+                top = fmaxf(top, __uint_as_float(sr[e]));
+              }
+              tmem_st_cols(tS + c * 16, sr);
             }
+            ptx::tmem_wait_st();
           }
         } else {
           if (any) {
@@ -990,11 +994,10 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
             if (Q16 || c == 1) {
               tmem_ld_cols(tS + c * W, sr);
               ptx::tmem_wait_ld();
-              if (masked) {
-                const uint32_t see = Q16 ? seen(c) : see1;
+              if (!Q16 && masked) {
 #pragma unroll
                 for (int e = 0; e < W; ++e)
-                  if (!((see >> e) & 1u)) sr[e] = 0xFF800000u;
+                  if (!((see1 >> e) & 1u)) sr[e] = 0xFF800000u;
               }
             }
 #pragma unroll
@@ -1180,7 +1183,7 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
             const int fb = free_bar(z, parity);
             if (!(ok = wait_warp(fb, parity))) break;
           }
-          const unsigned char *stage = sb + C::OFF_G + (z % C::NG) * C::STAGE;
+          unsigned char *stage = sb + C::OFF_G + (z % C::NG) * C::STAGE;
           const uint32_t dst = C::OFF_T + s * C::TILE;
           if (kind == kDraft) {
             const float f = pow2_biased(254 + C::SHV - top);
@@ -1199,30 +1202,39 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
             }
             if (__any_sync(0xffffffffu, lost != 0u) && lane == 0) wk.totals[2] = 1;
           } else {
-            const bool check = kv == 1 && kind == kOwn;
             __syncwarp();  // the last tile's factors have been read
             {
               auto factor = [&](int x) { return pow2_f16x2(static_cast<int>(exps >> (8 * x) & 0xFFu) - top + C::SHV); };
               reinterpret_cast<uint4 *>(factors)[lane] = make_uint4(factor(0), factor(1), factor(2), factor(3));
             }
             __syncwarp();
-#pragma unroll 2
-            for (int e = 0; e < 128 / STEP; ++e) {
-              const int row = r0 + e * STEP;
-              const bool live = (row & 63) < (row >= 64 ? n1 : n0);
-              uint4 cw = live ? *reinterpret_cast<const uint4 *>(stage + row * C::RB + p * 16) : make_uint4(0u, 0u, 0u, 0u);
-              uint32_t scale2 = 0u;  // group scales of the piece
-              if constexpr (FMT == BSA_CACHE_E2M1)
-                scale2 = live ? *reinterpret_cast<const uint16_t *>(stage + C::GROUPS + row * (D / 16) + 2 * p) : 0u;
-              if (check) {  // a NaN in a masked place goes by way of the combine
-                uint32_t *odd = wk.odd + (static_cast<size_t>(u.z) * a.c.hkv + g) * kOdd;
-                if constexpr (FMT == BSA_CACHE_E2M1) {
-                  scale2 = without_nan(scale2, p * 32, 16, odd);
-                } else if ((nan_codes(cw.x) | nan_codes(cw.y) | nan_codes(cw.z) | nan_codes(cw.w)) != 0u) {
-                  cw = make_uint4(without_nan(cw.x, p * 16, 1, odd), without_nan(cw.y, p * 16 + 4, 1, odd),
-                                  without_nan(cw.z, p * 16 + 8, 1, odd), without_nan(cw.w, p * 16 + 12, 1, odd));
+            // Of V, rows behind the last key become 0 and a NaN that some rows do not see goes by way of the combine (of K
+            // neither matters: those logits are masked).  Apart, because what the loop below takes in instructions counts.
+            if (kv == 1 && (kind == kOwn || n0 + n1 < kUnit)) {
+              uint32_t *odd = wk.odd + (static_cast<size_t>(u.z) * a.c.hkv + g) * kOdd;
+#pragma unroll 1
+              for (int e = 0; e < 128 / STEP; ++e) {
+                const int row = r0 + e * STEP;
+                const bool live = (row & 63) < (row >= 64 ? n1 : n0);
+                if constexpr (FMT == BSA_CACHE_E4M3) {
+                  uint4 *piece = reinterpret_cast<uint4 *>(stage + row * C::RB + p * 16);
+                  const uint4 c = *piece;
+                  if (!live)
+                    *piece = make_uint4(0u, 0u, 0u, 0u);
+                  else if (kind == kOwn && (nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w)) != 0u)
+                    *piece = make_uint4(without_nan(c.x, p * 16, 1, odd), without_nan(c.y, p * 16 + 4, 1, odd),
+                                        without_nan(c.z, p * 16 + 8, 1, odd), without_nan(c.w, p * 16 + 12, 1, odd));
+                } else {
+                  uint16_t *scale = reinterpret_cast<uint16_t *>(stage + C::GROUPS + row * (D / 16) + 2 * p);
+                  if (!live) *scale = 0;
+                  else if (kind == kOwn) *scale = static_cast<uint16_t>(without_nan(*scale, p * 32, 16, odd));
                 }
               }
+            }
+#pragma unroll 4
+            for (int e = 0; e < 128 / STEP; ++e) {
+              const int row = r0 + e * STEP;
+              const uint4 cw = *reinterpret_cast<const uint4 *>(stage + row * C::RB + p * 16);
               const uint32_t f = factors[row];
               const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
               const uint32_t at = dst + static_cast<uint32_t>(row) * 128;
@@ -1240,6 +1252,7 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
                 put(p >> 2, 2 * (p & 3), make_uint4(h[0], h[1], h[2], h[3]));
                 put(p >> 2, 2 * (p & 3) + 1, make_uint4(h[4], h[5], h[6], h[7]));
               } else {
+                const uint32_t scale2 = *reinterpret_cast<const uint16_t *>(stage + C::GROUPS + row * (D / 16) + 2 * p);
                 const uint32_t g2 = mul_f16x2(e4m3x2_f16(scale2), f);
                 const uint32_t ga = __byte_perm(g2, g2, 0x1010), gb = __byte_perm(g2, g2, 0x3232);
 #pragma unroll
