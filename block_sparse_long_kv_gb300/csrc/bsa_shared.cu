@@ -34,11 +34,11 @@
 // they are taken out of the product, and the combine adds them to the rows that see them.
 // Every mbarrier wait is bounded, as in the prefill kernel.
 //
-// Measured (32 / 4 heads of 128): 32 answers over 128K in bf16 78 us (295 MB, 3.8 TB/s, 0.88 PFLOP/s), 8 answers 67 (bf16),
-// 78 (e4m3), 75 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 9 pass before the first product
+// Measured (32 / 4 heads of 128): 32 answers over 128K in bf16 78 us (295 MB, 3.8 TB/s, 0.88 PFLOP/s), 8 answers 68 (bf16),
+// 76 (e4m3), 77 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 9 pass before the first product
 // (plan, look-ups, first tile) and 9 after the last (parts through the L2, combine).  bf16: 3300 cycles a unit and pair of
 // row tiles, 2150 of them products; the thread that issues them sets the pace (P released in halves: 90 us, waits that
-// spin: 82).  Codes: issue slots and instruction supply; unrolled loops are slower.
+// spin: 82).  Codes: a loader warp's chain, 3700 cycles a unit (2300 of conversion), and instruction supply.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1143,13 +1143,12 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
 
       int oref = 0;
       for (int i = 0; ok && i < units; ++i, ++n) {
-        // ---- the unit's scales, K's and V's
-        if (!(ok = wait_warp(C::B_IN + n % kUnits, (n / kUnits) & 1))) break;
+        // ---- the unit's scales, K's and V's (its record was written before the copies were announced)
+        const uint32_t z = 2 * n + kv, s = z % C::NS;
+        if (!(ok = wait_warp(C::B_GF + z % C::NG, (z / C::NG) & 1))) break;
         const int4 u = unit_rec[n % kUnits];
         const int n0 = unit_keys(u, 0), n1 = unit_keys(u, 1), kind = unit_kind(u);
         const size_t dstride = static_cast<size_t>(a.c.hkv) * D;
-        const uint32_t z = 2 * n + kv, s = z % C::NS;
-        if (!(ok = wait_warp(C::B_GF + z % C::NG, (z / C::NG) & 1))) break;
         const uint16_t *drafted = (kv == 0 ? a.k_new : a.v_new) + (static_cast<size_t>(kind == kDraft ? u.z : 0) * a.c.hkv + g) * D;
         int top;
         uint32_t exps = 0u;  // of the lane's four rows
