@@ -34,11 +34,11 @@
 // they are taken out of the product, and the combine adds them to the rows that see them.
 // Every mbarrier wait is bounded, as in the prefill kernel.
 //
-// Measured (32 / 4 heads of 128): 32 answers over 128K in bf16 78 us (295 MB, 3.8 TB/s, 0.88 PFLOP/s), 8 answers 68 (bf16),
-// 76 (e4m3), 77 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 9 pass before the first product
+// Measured (32 / 4 heads of 128): 32 answers over 128K in bf16 78 us (295 MB, 3.8 TB/s, 0.88 PFLOP/s), 8 answers 67 (bf16),
+// 74 (e4m3), 74 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 9 pass before the first product
 // (plan, look-ups, first tile) and 9 after the last (parts through the L2, combine).  bf16: 3300 cycles a unit and pair of
 // row tiles, 2150 of them products; the thread that issues them sets the pace (P released in halves: 90 us, waits that
-// spin: 82).  Codes: a loader warp's chain, 3700 cycles a unit (2300 of conversion), and instruction supply.
+// spin: 82).  Codes: a loader warp's chain (of 3700 cycles a unit 2300 converted) and instruction supply.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -311,7 +311,7 @@ struct Shared {
   // unit records; K's scale, V's; segment published, done; row scales; last MMA
   static constexpr int B_QF = 0, B_FK = 1, B_FV = B_FK + 4, B_EV = B_FV + 4, B_GF = B_EV + 4, B_GE = B_GF + NG,
                        B_SF = B_GE + NG, B_PR = B_SF + 4, B_OD = B_PR + 2, B_OE = B_OD + 2, B_IN = B_OE + 2,
-                       B_IK = B_IN + kUnits, B_IV = B_IK + (Q16 ? kUnits : 0), B_SG = B_IV + (Q16 ? kUnits : 0), B_SE = B_SG + kSegs, B_RS = B_SE + kSegs,
+                       B_IK = B_IN + (Q16 ? 0 : kUnits), B_IV = B_IK + (Q16 ? kUnits : 0), B_SG = B_IV + (Q16 ? kUnits : 0), B_SE = B_SG + kSegs, B_RS = B_SE + kSegs,
                        B_FIN = B_RS + (Q16 ? 2 : 0), NBARS = B_FIN + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + (NBARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
   static constexpr uint32_t OFF_SEG = OFF_MISC + 16;                          // [kSegs] two int4
@@ -666,10 +666,7 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
               } else {
                 const uint32_t s = z % C::NG, round = z / C::NG;
                 if (round > 0 && !(ok = wait_parked(bar(C::B_GE + s), (round - 1) & 1, ctl))) break;
-                if (kv == 0) {
-                  unit_rec[n % kUnits] = make_int4(keys, rows, what, 0);
-                  ptx::mbar_arrive(bar(C::B_IN + n % kUnits));
-                }
+                if (kv == 0) unit_rec[n % kUnits] = make_int4(keys, rows, what, 0);
                 constexpr int PER = FMT == BSA_CACHE_E4M3 ? 1 : 1 + D / 16;
                 const uint8_t *codes = kv == 0 ? a.k_codes : a.v_codes, *scales = kv == 0 ? a.k_scales : a.v_scales;
                 const uint32_t dst = base + C::OFF_G + s * C::STAGE, f = bar(C::B_GF + s);
@@ -855,7 +852,8 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
       int oref = 0, done = 0;  // O's unit (8- and 4-bit caches); units of this lane in the segment
       for (int i = 0; i < units; ++i, ++n) {
         if (!PAIR && (i & 1) != t) continue;
-        if (!(ok = wait_warp(C::B_IN + n % kUnits, (n / kUnits) & 1))) break;
+        // (over codes K's scale comes after the copies, and they after the record)
+        if (!(ok = wait_warp((Q16 ? C::B_IK : C::B_IN) + n % kUnits, (n / kUnits) & 1))) break;
         const int4 u = unit_rec[n % kUnits];
         // which of the thread's 64 keys the row sees
         uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
@@ -898,7 +896,6 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         float scl = rs;
         int oref_new = 0;
         if constexpr (Q16) {
-          if (!(ok = wait_warp(C::B_IK + n % kUnits, (n / kUnits) & 1))) break;
           if (!(ok = wait_warp(C::B_IV + n % kUnits, (n / kUnits) & 1))) break;
           // never 0, so that a masked -inf stays one (the logits below it are 0 to any precision)
           scl = fmaxf(scl * scale_k[n % kUnits], 1e-37f);
