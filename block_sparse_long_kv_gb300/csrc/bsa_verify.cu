@@ -81,6 +81,12 @@ __device__ __forceinline__ float at(const void *row, int64_t i) {
   if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t *>(row) + i)) << 16);
   else return __ldg(static_cast<const float *>(row) + i);
 }
+// The same as a probability: what is none counts as `scaled` says.
+template <bool BF16>
+__device__ __forceinline__ float prob_at(const void *row, int64_t i) {
+  const float x = at<BF16>(row, i);
+  return x > 0.f ? fminf(x, 1.f) : 0.f;
+}
 template <bool BF16>
 __device__ __forceinline__ const void *row_of(const void *base, int64_t row, int64_t stride) {
   return static_cast<const char *>(base) + row * stride * (BF16 ? 2 : 4);
@@ -121,7 +127,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int per) {
   extern __shared__ uint64_t dyn[];               // [tiles of a slice] their sums, [kept elements] what is left of them
   __shared__ int parent[kMaxDraft], token[kMaxDraft], rank[kMaxDraft];
-  __shared__ float u_of[kMaxDraft], p_at[kMaxDraft], q_at[kMaxDraft];
+  __shared__ float u_of[kMaxDraft], q_at[kMaxDraft];
   __shared__ double left[kMaxDraft];              // what is left of the node's row at its children's tokens
   __shared__ int turned[kMaxDraft];               // refused children of the node
   __shared__ uint64_t mass[kMaxDraft];            // M after as many refusals
@@ -158,9 +164,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     token[i] = x;
     rank[i] = i == 0 ? 0 : -1;
     u_of[i] = __ldg(a.u_accept + t);
-    p_at[i] = up < 0 ? 0.f : at<BF16>(row_of<BF16>(a.p, sp.start + up, a.p_stride), x);
-    left[i] = p_at[i];
-    q_at[i] = up < 0 || a.q == nullptr ? 1.f : at<BF16>(row_of<BF16>(a.q, t, a.q_stride), x);
+    left[i] = up < 0 ? 0.f : prob_at<BF16>(row_of<BF16>(a.p, sp.start + up, a.p_stride), x);
+    q_at[i] = up < 0 || a.q == nullptr ? 1.f : prob_at<BF16>(row_of<BF16>(a.q, t, a.q_stride), x);
   }
 
   const int v0 = min(a.vocab, me * per), v1 = min(a.vocab, v0 + per), tiles = (v1 - v0 + kTile - 1) / kTile;
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     for (int i = tid; i < sp.len; i += kThreads) {
       if (i <= t || parent[i] != node) continue;
       const float q = a.q == nullptr ? (token[t] == token[i] ? 1.f : 0.f)
-                                     : at<BF16>(row_of<BF16>(a.q, sp.start + t, a.q_stride), token[i]);
+                                     : prob_at<BF16>(row_of<BF16>(a.q, sp.start + t, a.q_stride), token[i]);
       left[i] = fmax(left[i] - static_cast<double>(mass[k - 1]) * 0x1p-60 * static_cast<double>(q), 0.);
     }
     const uint64_t m = sum_left(row_of<BF16>(a.p, sp.start + node, a.p_stride), k, have);

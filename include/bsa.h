@@ -658,7 +658,8 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * cached_out [batch_out] take the place of those of block_table: row j is a
  * copy of row source[j] (int32; -1: an empty row).  A row named several times is
  * shared from then on, one that is not named gives up its pages.  refs is
- * updated in place; the outputs overlap no input.
+ * updated in place; the outputs overlap no input and one another.  batch +
+ * batch_out <= 65535.
  *
  * bsa_cache_grow: sequence b gets the tokens cu_new[b] .. cu_new[b+1]-1 of
  * total_new, or with `grow` (int32 [batch], nullable) the first grow[b] of as many

@@ -27,8 +27,8 @@ def clean(row):
     return np.clip(row, 0.0, 1.0)
 
 
-def reference(p, q, tokens, parents, u, us, exact=()):
-    """One sequence: rows p [n, vocab], q (or None); (path ranks, count, next).  exact: decisions that may be ties."""
+def reference(p, q, tokens, parents, u, us):
+    """One sequence: rows p [n, vocab], q (or None); (path ranks, count, next, how far each decision was from a tie)."""
     n, vocab = p.shape
     rank, node, depth = [-1] * n, 0, 1
     rank[0] = 0
@@ -228,6 +228,24 @@ def test_values_that_are_no_probabilities():
     b.q[2, 11] = float("inf")
     b.q[:, 12::50] = -float("inf")
     b.check()
+
+
+@pytest.mark.parametrize("value", [float("nan"), -0.5, 3.0, float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["p", "q", "sibling"])
+def test_a_drafted_token_without_a_probability(value, where):
+    """At the drafted ids themselves: 0 for NaN and below, 1 above."""
+    for seed in range(6):
+        b = Batch([4, 5], 60, seed=40 + seed, parents="star")
+        x = int(b.tokens[2])
+        b.tokens[3] = x
+        if where == "p":
+            b.p[0, x] = value
+        elif where == "q":
+            b.q[2, x] = value
+        else:
+            b.q[1, x] = value                                 # of the child tried before
+            b.u[1] = 1.0
+        b.check(ties=True)
 
 
 def test_subnormal_and_tiny_probabilities():
