@@ -1298,9 +1298,13 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const T
   // (the plan was there before the kernel ahead could let this one start)
   const SeqRecord dr = wk.seqs[b];
   const int tiles = wk.totals[1], places = wk.totals[3] * a.c.hkv;
-  if (i >= dr.len) return;
   const int row0 = (dr.at + i) * G, e = dr.tile0 + row0 / TILE_ROWS;
-  if (e >= tiles) return;
+  if (i >= dr.len || e >= tiles) {
+    // One block without rows waits all the same: where none has any (a step without drafts), this kernel would else end
+    // before the one ahead, and what follows in the stream could use its workspace.
+    if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) after_previous_kernel();
+    return;
+  }
   const TileRecord tr = wk.tiles[e], prev = wk.tiles[max(e - 1, 0)];
   const int run = (places + kSms - 1) / kSms, span = span_of(tr.shared, tr.units);
   const int first = tr.place * a.c.hkv + g * span, cta0 = first / run;

@@ -396,6 +396,43 @@ def test_captured_lengths_change():
         c.drafts = keep
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("what", ["no drafts", "too many drafts", "bad groups"])
+def test_steps_that_write_no_row_between_others_in_one_workspace(fmt, what):
+    """Queued one behind the other: a step in which no sequence has rows, then a whole one, in the same workspace."""
+    c = Case(fmt, [(70, [900, 5, 0], [3, 1, 2]), (33, [129, 640], [1, 1])], 8, 2, 128, 64, seed=18)
+    shape, a = c.args()
+    bsa, t = c.bsa, sum(c.drafts)
+    ws = torch.full((bsa.shared_workspace_bytes(shape, c.cs),), 0xFF, dtype=torch.uint8, device="cuda")
+    empty = dict(a)
+    if what == "no drafts":
+        empty["cu_draft"] = i32([0] * 6)
+    elif what == "too many drafts":
+        empty["cu_draft"] = i32([0, 4, 4, 8, 8, 8])             # of 3
+    else:
+        empty["cu_group"] = i32([0, 6, 5])
+
+    def call(x, o, lse, st):
+        bsa.shared_fwd(shape, c.cs, x["cu_group"], x["shared_pages"], x["cu_draft"], x["cached"], x["block_table"],
+                       x["parents"], x["q"], x["k_new"], x["v_new"], c.cache, 1 / math.sqrt(c.d), o, lse, ws, st)
+
+    def outs(n):
+        return ([torch.full((t, c.hq, c.d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(n)],
+                [torch.full((t, c.hq), float("nan"), device="cuda") for _ in range(n)])
+    n = 20
+    (o, lse), (none, no_lse), st, st_none = outs(n), outs(n), i32([0]), i32([0])
+    torch.cuda.synchronize()
+    for i in range(n):
+        call(empty, none[i], no_lse[i], st_none)
+        call(a, o[i], lse[i], st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and st_none.item() == (0 if what == "no drafts" else 1)
+    c.check(o[0], lse[0])
+    for i in range(n):
+        assert torch.isnan(none[i]).all() and torch.isnan(no_lse[i]).all()
+        assert torch.equal(o[i].view(torch.int16), o[0].view(torch.int16)) and torch.equal(lse[i], lse[0]), i
+
+
 def test_refusals_of_the_binding():
     c = Case(C.BF16, ONE, 4, 2, 64, 64)
     for over, kind in ((dict(cu_group=i32([0])), ValueError), (dict(shared_pages=torch.zeros(1, device="cuda")), TypeError),
