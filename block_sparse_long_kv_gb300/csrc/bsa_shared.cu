@@ -595,6 +595,23 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
         if (bad1) u.p1 = -1, u.keys &= ~0xFF00;
         if (in && (bad0 || bad1)) report_arg(a);
       };
+      // With two row tiles and an odd ring, tiles of K and V of a unit j take the places of V(j - 3) and K(j - 2), which one
+      // sign frees: S_1(j - 2).  V does not wait for it again: S_1(j), which needs K(j) alone, may by then have completed
+      // that barrier once more, and the parity would be that of another phase.  V((NS - 1) / 2) is the first that needs a
+      // place, and its K none: it takes S_1(0), or S_1(1) where that barrier has gone on (its own does so with the product
+      // that needs this V).
+      static_assert(Q16 || !PAIR || C::NS % 2 == 1, "V's place becomes free with K's");
+      auto first_place = [&]() -> bool {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        for (;;) {
+          if (try_wait_parked(bar(s_bar(1, 0)), 0) || is_complete(bar(s_bar(1, 1)), 0)) return true;
+          if (*ctl.abort_flag) return false;
+          if (ptx::globaltimer_ns() - t0 > wait::kWaitTimeoutNs) {
+            wait::report(ctl, BSA_ERR_DEVICE_TIMEOUT);
+            return false;
+          }
+        }
+      };
       Unit now = look_up(lane), next{};
       for (; ok && n < nu; ++n) {
         if (n % 32 == 0) {
@@ -631,7 +648,9 @@ __global__ void __launch_bounds__(Shared<D, FMT, PAIR>::THREADS, 1)
               if constexpr (!Q16) {
                 const uint32_t s = z % C::NS;
                 uint32_t parity = 0;
-                if (z >= C::NS) {
+                if (PAIR && kv == 1) {  // (K has waited for the sign of both, but the first V to need a place)
+                  if (z == C::NS && !(ok = first_place())) break;
+                } else if (z >= C::NS) {
                   const int fb = free_bar(z, parity);
                   if (!(ok = wait_parked(bar(fb), parity, ctl))) break;
                 }

@@ -433,6 +433,19 @@ def test_steps_that_write_no_row_between_others_in_one_workspace(fmt, what):
         assert torch.equal(o[i].view(torch.int16), o[0].view(torch.int16)) and torch.equal(lse[i], lse[0]), i
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("groups", [[(456, [70, 0, 130], [4, 3, 3])], [(150, [3, 70], [5, 4]), (140, [1], [9]), (160, [64, 0], [6, 3])]],
+                         ids=["one run", "segments"])
+def test_a_dozen_units_a_run_in_two_row_tiles(fmt, groups):
+    """Every place of the rings of tiles, codes, records and signs is used several times, each in its turn."""
+    c = Case(fmt, groups, 128, 8, 64, 64, seed=19)
+    o, lse = c.run()
+    c.check(o, lse)
+    for _ in range(3):
+        again, lse2 = c.run()
+        assert torch.equal(o.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
 def test_refusals_of_the_binding():
     c = Case(C.BF16, ONE, 4, 2, 64, 64)
     for over, kind in ((dict(cu_group=i32([0])), ValueError), (dict(shared_pages=torch.zeros(1, device="cuda")), TypeError),
