@@ -503,9 +503,14 @@ __global__ void __launch_bounds__(Cfg<D, BLK, NT, F8>::THREADS, 1)
       // full normaliser = the two halves' shares, added in a fixed order; the Q tiles'
       // shared memory is free once every MMA has completed
       float *lsh = reinterpret_cast<float *>(sb + C::OFF_Q) + (t * C::CH) * 128;
-      lsh[hf * 128 + r] = l;
-      ptx::named_barrier(pair_bar, 64);
-      l = lsh[r] + lsh[128 + r];
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        lsh[hf * 128 + r] = l;
+        ptx::named_barrier(pair_bar, 64);
+        l = lsh[r] + lsh[128 + r];
+      } else {
+        wait::leave_pair(pair_bar);
+      }
     }
     const float inv = (ok && l > 0.f) ? p.v_scale / l : 0.f;
     const bool row_valid = qtok < sp.len;  // a partial last block's tile rows past the sequence end

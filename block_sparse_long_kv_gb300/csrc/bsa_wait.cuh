@@ -2,7 +2,8 @@
 // wait self-test.  A wait that runs out records BSA_ERR_DEVICE_TIMEOUT in the
 // caller's status word and in the CTA's abort flag and returns false; a CTA
 // that sees another CTA's nonzero status stops at its next check.  No wait
-// traps or spins without a limit.
+// traps or spins without a limit; a warp that gives up lets its partner at a
+// named barrier go (leave_pair).
 #pragma once
 
 #include <stdint.h>
@@ -54,6 +55,13 @@ __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
   while (!ptx::mbar_try_wait(bar, parity)) {
     if (ptx::globaltimer_ns() - t0 > kDrainTimeoutNs) return;
   }
+}
+
+// Two warps that meet on named barrier `id` in every turn: there no limit holds.  One that gives up a bounded wait
+// calls this, once, as it leaves, so that a partner that still saw its own wait end is let through.  That one comes no
+// further than its next wait, which needs what the warp that left did not do.  Every thread of the warp.
+__device__ __forceinline__ void leave_pair(int id) {
+  ptx::named_arrive(id, 64);
 }
 
 }  // namespace wait

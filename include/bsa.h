@@ -752,7 +752,8 @@ bsa_status bsa_verify(const bsa_verify_shape *shape, const int32_t *cu_draft, co
  * Self-test of the device wait limits (no compute).  Launches `ctas` CTAs
  * (1..8) whose first thread waits, through the bounded wait the attention
  * kernel uses, on an mbarrier that nothing completes.  CTA 0 gives up after
- * limit_ns nanoseconds (1e6 .. 1e9) and writes BSA_ERR_DEVICE_TIMEOUT into
+ * limit_ns nanoseconds (1e6 .. 1e9), lets a second warp that stands at a
+ * barrier of both go, and writes BSA_ERR_DEVICE_TIMEOUT into
  * *dev_status (int32, caller-owned, 4-byte aligned, 0 before the call); the
  * other CTAs wait with the library's own 4 s limit and stop as soon as they
  * see the status.  Returns BSA_ERR_INVALID_ARG for a null or misaligned

@@ -31,6 +31,18 @@ def test_wait_runs_out_and_reports():
     assert dt < 1.0, dt
 
 
+def test_a_partner_at_a_barrier_is_let_go():
+    """The second warp of every CTA stands at a barrier without a limit; the call returns with the first one's."""
+    import block_sparse_long_kv_gb300 as bsa
+    for ctas in (1, 8):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        bsa.selftest_wait_timeout(st, 10_000_000, ctas=ctas)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 6 and time.perf_counter() - t0 < 1.0
+
+
 def test_context_usable_after_timeout():
     import block_sparse_long_kv_gb300 as bsa
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
