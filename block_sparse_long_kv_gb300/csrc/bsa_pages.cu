@@ -79,8 +79,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
 __global__ void __launch_bounds__(kThreads) trim_kernel(const TrimArgs a) {
   const int b = blockIdx.x;
   const int n = held(a.cached, b, a.page_shift, a.stride, a.status), keep = a.keep[b];
+  const bool bad = keep < 0 || keep > n || a.cached[b] != n;  // (a length that its row cannot hold reads as 0)
   __syncthreads();  // everyone has read the length
-  if (keep < 0 || keep > n) {
+  if (bad) {
     if (threadIdx.x == 0) report(a.status, BSA_ERR_INVALID_ARG);
     return;
   }

@@ -447,3 +447,21 @@ def test_captured_on_another_stream():
             dev.refs[p] -= 1
         pool.cached, pool.table = pool.cached[1:], pool.table[1:]
     assert int(dev.status.item()) == 0
+
+
+LENGTHS_THAT_ARE_NONE = [-1, 8 * 64 + 1, -(1 << 31), (1 << 31) - 1]
+
+
+@pytest.mark.parametrize("n", LENGTHS_THAT_ARE_NONE)
+@pytest.mark.parametrize("keep", [0, 5, -1])
+def test_trim_of_a_length_that_is_none(n, keep):
+    """Nothing of that row changes, not even where nothing is to be kept; the others are trimmed."""
+    pool = shared_rows(3, [70, 90, 128])
+    dev = Gpu(pool)
+    dev.cached[1] = n
+    dev.trim([60, keep, 128])
+    pool.trim([60, 90, 128])
+    pool.cached[1] = n
+    torch.cuda.synchronize()
+    assert int(dev.status.item()) == INVALID
+    assert dev.cached.tolist() == pool.cached and dev.refs.tolist() == pool.refs and dev.table.tolist() == pool.table
