@@ -39,10 +39,15 @@ __device__ __forceinline__ int held(const int32_t *cached, int b, int page_shift
 __device__ __forceinline__ int pages_of(int tokens, int page_shift) {
   return tokens == 0 ? 0 : ((tokens - 1) >> page_shift) + 1;
 }
-// One table entry more or less names `page`.
+// `by` table entries more (or one less) name `page`, which one does: a count below 1 is not right, and stays as it is.
+// (Right counts are above 0 whenever this looks, as the entry looked at is among those counted.)
 __device__ __forceinline__ void count_page(int32_t *refs, int pages, int page, int by, int32_t *status) {
-  if (page < 0 || page >= pages) report(status, BSA_ERR_INVALID_ARG);
-  else if (atomicAdd(refs + page, by) + by < 0) report(status, BSA_ERR_INVALID_ARG);
+  if (page < 0 || page >= pages) {
+    report(status, BSA_ERR_INVALID_ARG);
+  } else if (atomicAdd(refs + page, by) < 1) {
+    atomicSub(refs + page, by);
+    report(status, BSA_ERR_INVALID_ARG);
+  }
 }
 
 // ---------------------------------------------------------------- fork, trim

@@ -685,8 +685,11 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * refs follow, and *live = L (int32).  Pages from L on are free afterwards.
  * block_table must hold every entry that refs counts.
  *
- * Entries and counts that do not fit together set BSA_ERR_INVALID_ARG and are
- * left out.  All int32 arrays 4-byte aligned, workspaces 16-byte.
+ * An entry of fork or trim that names no page of the pool, or one whose count is
+ * below 1, sets BSA_ERR_INVALID_ARG, and no count changes for it (fork looks at
+ * the rows that are not taken exactly once, and copies entries as they are).  A
+ * count that is too small but above 0 is not seen before it reaches 0, from where
+ * on its page is free, whoever still names it.  All int32 arrays 4-byte aligned, workspaces 16-byte.
  * ------------------------------------------------------------------------ */
 bsa_status bsa_cache_fork(const bsa_cache_shape *shape, int32_t batch, int32_t batch_out, int32_t table_stride,
                           const int32_t *source, const int32_t *cached, const int32_t *block_table, int32_t *refs,

@@ -465,3 +465,42 @@ def test_trim_of_a_length_that_is_none(n, keep):
     torch.cuda.synchronize()
     assert int(dev.status.item()) == INVALID
     assert dev.cached.tolist() == pool.cached and dev.refs.tolist() == pool.refs and dev.table.tolist() == pool.table
+
+
+@pytest.mark.parametrize("count", [1, 0, -5])
+def test_counts_too_small_for_what_is_given_up(count):
+    """Page 3 is named by three rows.  A count that would go below 0 stays and is reported; one that reaches 0 early is
+    that of a free page, whoever still names it."""
+    pool = shared_rows(3, [70, 90, 128])
+    for row in ([0], [0, 1], [0, 1, 2]):                        # rows given up, one after the other
+        dev = Gpu(pool)
+        dev.refs[3] = count
+        for x in row:
+            before = int(dev.refs[3].item())
+            keep = dev.cached.tolist()
+            keep[x] = 0
+            dev.status.zero_()
+            dev.trim(keep)
+            torch.cuda.synchronize()
+            assert int(dev.refs[3].item()) == (before - 1 if before > 0 else before)
+            assert int(dev.status.item()) == (0 if before > 0 else INVALID)
+        refs = list(pool.refs)
+        refs[3], refs[4] = min(count, 0), refs[4] - len(row)
+        assert dev.refs.tolist() == refs
+        assert [t[:2] for t in dev.table.tolist()] == [[-1, -1] if x in row else [3, 4] for x in range(3)]
+        assert dev.cached.tolist() == [0 if x in row else n for x, n in enumerate([70, 90, 128])]
+
+
+@pytest.mark.parametrize("count", [0, -5])
+@pytest.mark.parametrize("source", [[1, 2], [0, 0, 0, 1, 2]])
+def test_fork_of_a_page_whose_count_is_too_small(count, source):
+    """A page that row 0 alone names, given up or taken more often: its count stays as it is, the others follow."""
+    pool = shared_rows(3, [70, 90, 128])
+    pool.table[0][0] = 9
+    pool.refs[9], pool.refs[3] = 1, 2
+    dev = Gpu(pool)
+    dev.refs[9] = count
+    dev.fork(source)
+    pool.fork(source)
+    pool.refs[9] = count
+    dev.same(INVALID)
