@@ -17,6 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kSms = 152;
+constexpr int kMarks = 1 << 18;  // most bits by which growth knows last pages of two sequences (32 KB)
 constexpr int kHeld = 4;  // neighbouring pages of a planning thread, of which the first round's counts stay in registers
 
 // Threads of a planning CTA: a round takes all pages, and all sequences, up to kPlanThreads (fewer threads meet sooner).
@@ -144,6 +145,8 @@ __device__ __forceinline__ Held held_pages(const int32_t *refs, int pages, int r
   }
   return h;
 }
+// Bits for a pool's pages: as many, or kMarks, of which page p takes bit p % kMarks.
+__host__ __device__ __forceinline__ int mark_words(int pages) { return ((pages < kMarks ? pages : kMarks) + 31) / 32; }
 __device__ __forceinline__ int rounds_of(int pages) { return (pages + blockDim.x * kHeld - 1) / (blockDim.x * kHeld); }
 
 // One CTA plans: who needs how many pages (a copy of a shared last page among them, unless this is the last sequence
@@ -152,8 +155,8 @@ __device__ __forceinline__ int rounds_of(int pages) { return (pages + blockDim.x
 __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs a) {
   extern __shared__ int sm[];
   // [batch] the partial last page that gets tokens or -1; [batch] where the first new page goes, times 2, and whether
-  // that is a copy; [batch + 1] the first new page
-  int *last = sm, *goes = sm + a.batch, *first = goes + a.batch;
+  // that is a copy; [batch + 1] the first new page; a bit per page that is somebody's last and counts once
+  int *last = sm, *goes = sm + a.batch, *first = goes + a.batch, *marks = first + a.batch + 1;
   __shared__ int warps[33];
   __shared__ int carry;
   const int tid = threadIdx.x, threads = blockDim.x, shift = a.c.page_shift, mask = a.c.page - 1;
@@ -176,33 +179,44 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
     }
     if (s.g > 0 && (s.n & mask) != 0) {
       s.page = a.table[static_cast<size_t>(b) * a.stride + (s.n >> shift)];
-      if (s.page < 0 || s.page >= a.c.pages) {
+      if (s.page >= 0 && s.page < a.c.pages) s.refs = a.refs[s.page];
+      if (s.refs < 1) {  // none, or one that is free for others to get
         report(a.status, BSA_ERR_INVALID_ARG);
         s.page = -1;
         s.g = 0;
-      } else {
-        s.refs = a.refs[s.page];
       }
     }
     return s;
   };
   const Held round0 = held_pages(a.refs, a.c.pages, 0);
+  for (int i = tid; i < mark_words(a.c.pages); i += threads) marks[i] = 0;
   Seq seq0{0, 0, -1, 0};  // the first round's stays in registers
+  if (tid < a.batch) seq0 = read(tid);
+  __syncthreads();
+  bool met = false;       // a page that counts once was marked before: two sequences name it (or pages kMarks apart)
   for (int b = tid; b < a.batch; b += threads) {
-    const Seq s = read(b);
-    if (b == tid) seq0 = s;
+    const Seq s = b == tid ? seq0 : read(b);
     last[b] = s.page;
+    if (s.refs == 1) {
+      const int bit = s.page & (kMarks - 1);
+      met |= (atomicOr(marks + (bit >> 5), 1 << (bit & 31)) >> (bit & 31) & 1) != 0;
+    }
   }
   if (tid == 0) carry = 0;
-  __syncthreads();
+  met = __syncthreads_or(met) != 0;
   for (int base = 0; base < a.batch; base += threads) {
     const int b = base + tid;
     int need = 0;
     if (b < a.batch) {
-      const Seq s = base == 0 ? seq0 : read(b);
+      Seq s = base == 0 ? seq0 : read(b);
       int earlier = 0;
-      if (s.refs > 1)
+      if (s.refs > 1 || (s.refs == 1 && met))
         for (int x = 0; x < b; ++x) earlier += last[x] == s.page ? 1 : 0;
+      if (s.page >= 0 && s.refs - earlier < 1) {  // more sequences hold it than are counted: the first of them grow
+        report(a.status, BSA_ERR_INVALID_ARG);
+        s.g = 0;
+        if (base == 0) seq0.g = 0;
+      }
       const bool copy = s.refs - earlier > 1;
       need = s.g == 0 ? 0 : pages_of(s.n + s.g, shift) - pages_of(s.n, shift) + (copy ? 1 : 0);
       goes[b] = 2 * (pages_of(s.n, shift) - (copy ? 1 : 0)) + (copy ? 1 : 0);
@@ -444,11 +458,11 @@ cudaError_t launch_trim(const TrimArgs &a, cudaStream_t stream) {
 size_t grow_workspace_bytes(int batch) { return static_cast<size_t>(batch) * sizeof(GrowJob); }
 
 cudaError_t launch_grow(const GrowArgs &a, cudaStream_t stream) {
-  auto smem_of = [](int batch) { return (3 * static_cast<size_t>(batch) + 1) * sizeof(int); };
+  auto smem_of = [](int batch, int pages) { return (3 * static_cast<size_t>(batch) + 1 + mark_words(pages)) * sizeof(int); };
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = set_up(grow_plan_kernel, smem_of(kMaxDecodeRows), 0, done);
+  cudaError_t e = set_up(grow_plan_kernel, smem_of(kMaxDecodeRows, kMarks), 0, done);
   if (e != cudaSuccess) return e;
-  grow_plan_kernel<<<1, plan_threads(a.c.pages, a.batch), smem_of(a.batch), stream>>>(a);
+  grow_plan_kernel<<<1, plan_threads(a.c.pages, a.batch), smem_of(a.batch, a.c.pages), stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int want = (a.total + kThreads - 1) / kThreads, slot_blocks = want < kSms ? want : kSms;
   return launch_after(grow_rows_kernel, dim3(slot_blocks + a.batch * a.c.hkv * 2), kThreads, 0, stream, a, slot_blocks);

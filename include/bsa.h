@@ -673,7 +673,9 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * arrays.  When the pool lacks pages nothing changes: *dev_status is set to
  * BSA_ERR_WORKSPACE and every slot is -1.  A sequence whose row cannot hold the
  * tokens (or whose cu_new, grow, cached or last page is inconsistent) sets
- * BSA_ERR_INVALID_ARG and does not grow.  Slots past cu_new[batch] are left as
+ * BSA_ERR_INVALID_ARG and does not grow: a last page that gets tokens has a count of
+ * at least 1, and where more sequences grow into it than its count says, the first
+ * ones do.  Slots past cu_new[batch] are left as
  * they were.  batch <= 4096.
  *
  * bsa_cache_trim: sequence b keeps its first keep[b] tokens (int32 [batch],

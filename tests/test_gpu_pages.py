@@ -504,3 +504,57 @@ def test_fork_of_a_page_whose_count_is_too_small(count, source):
     pool.fork(source)
     pool.refs[9] = count
     dev.same(INVALID)
+
+
+@pytest.mark.parametrize("count", [3, 2, 1, 0, -5])
+@pytest.mark.parametrize("growing", [[1, 1, 1], [0, 1, 1], [1, 0, 65], [0, 0, 1]])
+def test_growth_into_a_last_page_whose_count_is_too_small(count, growing):
+    """One after the other: while the count is above 1 a row gets a copy, at 1 it keeps the page, and then no row does."""
+    pool = shared_rows(4, [70, 90, 100, 64])
+    dev = Gpu(pool)
+    dev.refs[4] = count
+    want, refs, short, free = [], count, False, [0, 1, 2, 5, 6]
+    for b, g in enumerate(growing):
+        if g and refs < 1:
+            want.append(None)
+            short = True
+            continue
+        first = 4
+        if g and refs > 1:
+            refs, first = refs - 1, free.pop(0)
+        elif g:
+            refs = 0                                          # (kept: no one else's)
+        at = [70, 90, 100][b]
+        pages = [3, first] + ([free.pop(0)] if at + g > 128 else [])
+        want.append([pages[x // 64] * 64 + x % 64 for x in range(at, at + g)])
+    want.append([free.pop(0) * 64])                           # and a row that takes no copy
+    cu = [0] + np.cumsum(growing + [1]).tolist()
+    slots = dev.grow(cu)
+    torch.cuda.synchronize()
+    assert int(dev.status.item()) == (INVALID if short else 0)
+    if count != 0:                                            # (0 says that page 4 is free)
+        assert slots == [s for w, g in zip(want, growing + [1]) for s in (w if w is not None else [-1] * g)]
+    assert dev.cached.tolist() == [n + (g if w is not None else 0) for n, w, g in zip([70, 90, 100, 64], want, growing + [1])]
+
+
+@pytest.mark.parametrize("pages, step", [(3000, 1499), ((1 << 18) + 3000, 1 << 18)])
+def test_growth_of_many_rows_two_of_them_into_one_page(pages, step):
+    """More rows than a planning CTA has threads: two name the same last page, which counts once.  And pages a power of two
+    apart, which nobody shares."""
+    pool = Pool(pages, 64, 2)
+    batch = 1500
+    pool.cached = [1] * batch
+    pool.table = [[p, -1] for p in range(batch)]
+    for b in range(0, batch, 100):
+        pool.table[b][0] = (b + step) % pages if step == 1 << 18 else b
+    for t in pool.table:
+        pool.refs[t[0]] = 1
+    pool.table[1400][0] = 7
+    dev = Gpu(pool, C.E2M1, hkv=1)
+    cu = list(range(batch + 1))
+    want = [t[0] * 64 + 1 for t in pool.table]
+    want[1400] = -1                                           # row 7 keeps it
+    assert dev.grow(cu) == want
+    torch.cuda.synchronize()
+    assert int(dev.status.item()) == INVALID
+    assert dev.cached.tolist() == [1 if b == 1400 else 2 for b in range(batch)] and dev.refs.tolist() == pool.refs
