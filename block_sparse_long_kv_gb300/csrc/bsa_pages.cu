@@ -18,6 +18,7 @@ constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kSms = 152;
 constexpr int kMarks = 1 << 18;  // most bits by which growth knows last pages of two sequences (32 KB)
+constexpr int kWide = 1 << 18;   // pages of one sequence from which on a sum of 4096 of them is taken in 64 bits
 constexpr int kHeld = 4;  // neighbouring pages of a planning thread, of which the first round's counts stay in registers
 
 // Threads of a planning CTA: a round takes all pages, and all sequences, up to kPlanThreads (fewer threads meet sooner).
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
   int *last = sm, *goes = sm + a.batch, *first = goes + a.batch, *marks = first + a.batch + 1;
   __shared__ int warps[33];
   __shared__ int carry;
+  __shared__ unsigned long long wide;  // pages of the sequences that need kWide or more
   const int tid = threadIdx.x, threads = blockDim.x, shift = a.c.page_shift, mask = a.c.page - 1;
   launch_next();
   struct Seq {
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
       met |= (atomicOr(marks + (bit >> 5), 1 << (bit & 31)) >> (bit & 31) & 1) != 0;
     }
   }
-  if (tid == 0) carry = 0;
+  if (tid == 0) carry = 0, wide = 0;
   met = __syncthreads_or(met) != 0;
   for (int base = 0; base < a.batch; base += threads) {
     const int b = base + tid;
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
       }
       const bool copy = s.refs - earlier > 1;
       need = s.g == 0 ? 0 : pages_of(s.n + s.g, shift) - pages_of(s.n, shift) + (copy ? 1 : 0);
+      if (need >= kWide) atomicAdd(&wide, static_cast<unsigned long long>(need));
       goes[b] = 2 * (pages_of(s.n, shift) - (copy ? 1 : 0)) + (copy ? 1 : 0);
       a.jobs[b] = GrowJob{s.g > 0 ? s.n : -1, copy ? s.page : -1, -1, copy ? s.n & mask : 0};
     }
@@ -260,6 +263,12 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
       ++k;
     }
   };
+  auto nobody = [&]() {  // not enough pages: nobody grows
+    if (tid == 0) report(a.status, BSA_ERR_WORKSPACE);
+    for (int b = tid; b < a.batch; b += threads) a.jobs[b] = GrowJob{-1, -1, -1, 0};
+  };
+  // offsets that descend name a token in several sequences, whose pages may add up to more than 32 bits hold
+  if (wide > static_cast<unsigned long long>(a.c.pages)) return nobody();
   if (total > 0) {
     int n;
     const int k0 = scan_block(free_of(round0), warps, &n);
@@ -270,11 +279,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_plan_kernel(const GrowArgs 
       scan_block(free_of(held_pages(a.refs, a.c.pages, r)), warps, &more);
       found += more;
     }
-    if (found < total) {  // not enough: nobody grows
-      if (tid == 0) report(a.status, BSA_ERR_WORKSPACE);
-      for (int b = tid; b < a.batch; b += threads) a.jobs[b] = GrowJob{-1, -1, -1, 0};
-      return;
-    }
+    if (found < total) return nobody();
     give(round0, 0, k0);
     for (int r = 1; n < total; ++r) {
       const Held h = held_pages(a.refs, a.c.pages, r);

@@ -558,3 +558,21 @@ def test_growth_of_many_rows_two_of_them_into_one_page(pages, step):
     torch.cuda.synchronize()
     assert int(dev.status.item()) == INVALID
     assert dev.cached.tolist() == [1 if b == 1400 else 2 for b in range(batch)] and dev.refs.tolist() == pool.refs
+
+
+def test_growth_whose_pages_do_not_add_up_in_32_bits():
+    """2048 sequences of 2^20 new pages each: offsets that descend name the same tokens again and again."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs a table of 16 GB")
+    import block_sparse_long_kv_gb300 as bsa
+    batch, stride, n = 4096, 1 << 20, 1 << 26
+    cs = bsa.make_cache_shape(8, 64, 1, 64, C.E4M3)
+    cache = bsa.alloc_cache(cs)
+    cached, refs, st = torch.zeros(batch, dtype=torch.int32, device="cuda"), i32([0] * 8), i32([0])
+    table = torch.full((batch, stride), -1, dtype=torch.int32, device="cuda")
+    slots = torch.full((n,), -9, dtype=torch.int32, device="cuda")
+    bsa.cache_grow(cs, i32([0, n] * (batch // 2) + [0]), None, None, cached, table, refs, cache, slots, None, st)
+    torch.cuda.synchronize()
+    assert st.item() == INVALID                               # (of the sequences between them, which come first)
+    assert not cached.any() and not refs.any() and bool((slots < 0).all())
+    assert all(bool((table[i:i + 64] == -1).all()) for i in range(0, batch, 64))
