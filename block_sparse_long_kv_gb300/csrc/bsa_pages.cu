@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
       if (p >= pages) break;
       if (p < live && h.refs[e] <= 0) holes[hole++] = p;
       if (p >= live && h.refs[e] > 0) moved[move++] = p;
-      if (p >= live && h.refs[e] <= 0) to[p] = -1;  // (no entry should name it)
+      if (h.refs[e] <= 0) to[p] = -1;  // (no entry should name it: below L it gets another's page)
+      else if (p < live) to[p] = p;
     }
     nh += n & 0xFFFF;
     nm += n >> 16;
@@ -402,7 +403,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   }
   if (tid == 0) {
     a.work[0] = nm;
-    a.work[1] = live;
     *a.live = live;
   }
 }
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
 // The first blocks rewrite the tables, all copy pages.
 __global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArgs a) {
   after_previous_kernel();
-  const int pages = a.c.pages, moves = a.work[0], live = a.work[1];
+  const int pages = a.c.pages;
   const int *holes = a.work + 4, *moved = holes + pages, *to = moved + pages;
   const long long entries = static_cast<long long>(a.batch) * a.stride;
   for (long long e = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; e < entries;
@@ -418,10 +418,11 @@ __global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArg
     const int b = static_cast<int>(e / a.stride), j = static_cast<int>(e % a.stride);
     if (j >= pages_of(held(a.cached, b, a.c.page_shift, a.stride, a.status), a.c.page_shift)) continue;
     const int p = a.table[e];
-    const int q = p >= 0 && p < live ? p : p >= live && p < pages ? to[p] : -1;
+    const int q = p >= 0 && p < pages ? to[p] : -1;
     if (q < 0) report(a.status, BSA_ERR_INVALID_ARG);
     else if (q != p) a.table[e] = q;
   }
+  const int moves = a.work[0];
   // a block takes pieces of a page's part of an array, codes first; four loads of a thread under way
   constexpr int kPiece = 4 * kThreads;  // times 16 bytes
   const int n16[2] = {static_cast<int>(static_cast<size_t>(a.c.hkv) * a.c.page * a.c.row / 16),

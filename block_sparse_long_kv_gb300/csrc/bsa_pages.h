@@ -46,7 +46,7 @@ struct CompactArgs {
   const int32_t *cached;
   int32_t *table, *refs, *live;
   uint8_t *planes[4];
-  int32_t *work;  // [2] moves and live pages, then [pages] holes and [pages] moved pages, and [pages] new places
+  int32_t *work;  // moves, from [4] on [pages] holes, [pages] moved pages, and [pages] new places (-1: a free page)
   int32_t *status;
   int batch, stride;
 };

@@ -685,7 +685,8 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * bsa_cache_compact: with L pages in use, the pages in use from L on move, in
  * ascending order, to the free ones below L, in ascending order; the tables and
  * refs follow, and *live = L (int32).  Pages from L on are free afterwards.
- * block_table must hold every entry that refs counts.
+ * block_table must hold every entry that refs counts; one that names no page of the
+ * pool, or one whose count is below 1, sets BSA_ERR_INVALID_ARG and stays as it is.
  *
  * An entry of fork or trim that names no page of the pool, or one whose count is
  * below 1, sets BSA_ERR_INVALID_ARG, and no count changes for it (fork looks at

@@ -576,3 +576,16 @@ def test_growth_whose_pages_do_not_add_up_in_32_bits():
     assert st.item() == INVALID                               # (of the sequences between them, which come first)
     assert not cached.any() and not refs.any() and bool((slots < 0).all())
     assert all(bool((table[i:i + 64] == -1).all()) for i in range(0, batch, 64))
+
+
+@pytest.mark.parametrize("bad", [0, 1, 2, 39])
+def test_compaction_reports_an_entry_that_names_a_free_page(bad):
+    """One below the pages in use among them, which gets another row's page."""
+    pool = shared_rows(3, [70, 90, 128])
+    dev = Gpu(pool)
+    dev.table[1, 0] = bad
+    assert dev.compact() == 2
+    torch.cuda.synchronize()
+    assert int(dev.status.item()) == INVALID
+    assert [t[:2] for t in dev.table.tolist()] == [[0, 1], [bad, 1], [0, 1]]
+    assert dev.refs.tolist()[:6] == [3, 3, 0, 0, 0, 0]
