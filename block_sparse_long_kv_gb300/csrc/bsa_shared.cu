@@ -35,10 +35,11 @@
 // Every mbarrier wait is bounded, as in the prefill kernel.
 //
 // Measured (32 / 4 heads of 128): 32 answers over 128K in bf16 78 us (295 MB, 3.8 TB/s, 0.88 PFLOP/s), 8 answers 67 (bf16),
-// 74 (e4m3), 74 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 9 pass before the first product
-// (plan, look-ups, first tile) and 9 after the last (parts through the L2, combine).  bf16: 3300 cycles a unit and pair of
-// row tiles, 2150 of them products; the thread that issues them sets the pace (P released in halves: 90 us, waits that
-// spin: 82).  Codes: a loader warp's chain (of 3700 cycles a unit 2300 converted) and instruction supply.
+// 74 (e4m3), 74 (e2m1); 16 x 16 drafts over 32K in bf16 126 us (1.05 PFLOP/s).  Of 78 us 10 pass before the first product
+// (5 of plan, then look-ups and the first tile) and 10 after the last was issued (parts through the L2, combine); of 66 with
+// four groups of e4m3 15 and 10.  bf16: 3300 cycles a unit and pair of row tiles, 2150 of them products; the thread that
+// issues them sets the pace (P released in halves: 90 us, waits that spin: 82, four barriers a lane for S: 82).  Codes: a
+// loader warp's chain (of 3700 cycles a unit 2300 converted) and instruction supply.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -12,8 +12,8 @@
 // What is left of a row stays in shared memory from refusal to refusal, so that each reads one more row of q; 8 bytes an
 // element, as far as a second CTA still fits beside this one.
 // Bound by the latency of a walk of dependent decisions, not by its bytes: 32 trees of 32 tokens over 131072 ids (34 MB,
-// 5 us of them) take 44 us, as long as the sequence with most refusals (104 with rows read anew each time); 19 chains of
-// 8 over 50021 ids 9.6; one chain of 4 over 32768 ids 7.
+// 5 us of them) take 45 us, as long as the sequence with most refusals (39 to 55 by the draws; 104 with rows read anew each
+// time), in bf16 the same; 19 chains of 8 over 50021 ids 9.7; one chain of 4 over 32768 ids 7.4.
 #include <stdint.h>
 
 #include <atomic>

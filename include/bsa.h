@@ -619,7 +619,17 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
  *
  * What is rounded: as stated at bsa_tree_fwd for more than 16 rows, but over an 8-
  * or 4-bit cache rows of a group's sequences are computed together, so the largest
- * |v| is that of the cached and drafted tokens of all of them.
+ * |v| is that of the cached and drafted tokens of all of them, and the last bits of a
+ * sequence's rows may depend on the others' magnitudes.
+ *
+ * When it pays: a shared key costs once what it costs bsa_tree_fwd for every sequence,
+ * but a key of a sequence's own pages is computed for all rows of a tile (128 or 256),
+ * and over an 8- or 4-bit cache costs 2 to 3.3 times what it costs there.  With 32 / 4
+ * heads of 128 and a token each this call was the faster one, over codes, while a
+ * sequence's own tokens were fewer than 0.3 of the shared ones (32 sequences) or 0.4 to
+ * 0.6 of them (8 sequences; 0.25 with heads of 64); over a bf16 cache with heads of 128
+ * at half as many as are shared, and about even at twice as many (slower there with 8
+ * drafts each).  Past that, bsa_tree_fwd over the same tables is the better call.
  *
  * Limits: as bsa_tree_fwd, but max_cached may be any number of pages up to
  * table_stride; groups <= 4096; total_draft * hq < 2^31.  The device checks what
@@ -630,7 +640,8 @@ bsa_status bsa_tree_fwd(const bsa_tree_shape *shape, const bsa_cache_shape *cach
  *   - for a sequence that drafts but holds fewer tokens than the group's pages:
  *     it attends to the group's pages and its drafts.
  * workspace: bsa_shared_workspace_bytes bytes, 16-byte aligned, the caller's
- * alone while the call runs (two graphs that may replay at the same time need one each).
+ * alone while the call runs (two graphs that may replay at the same time need one each,
+ * and a graph works in the one it was captured with, which has to live as long).
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t groups, batch, total_draft, max_draft, max_cached, hq, table_stride;
@@ -650,9 +661,11 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * A row of block_table (int32 [batch, table_stride]) names the pages of a
  * sequence's cached[b] tokens, ceil(cached[b] / page) of them; entries behind
  * those are -1 or left as they were.  refs (int32 [pages]) counts the entries
- * that name a page: 0 is a free page, and all zeros an empty pool.  These calls keep
- * both in step.  They run on the device alone, so a step that forks, grows and
- * trims can be captured; calls over one pool follow one another on a stream.  Free pages are given out lowest first, to sequences in ascending order.
+ * that name a page: 0 is a free page, all zeros an empty pool, and none is negative.
+ * These calls keep both in step.  They run on the device alone, so a step that forks,
+ * grows and trims can be captured (with a workspace that lives as long as the graph);
+ * calls over one pool follow one another on a stream.  Free pages are given out lowest
+ * first, to sequences in ascending order.
  *
  * bsa_cache_fork: the rows of table_out [batch_out, table_stride] and
  * cached_out [batch_out] take the place of those of block_table: row j is a
@@ -692,7 +705,8 @@ bsa_status bsa_shared_fwd(const bsa_shared_shape *shape, const bsa_cache_shape *
  * below 1, sets BSA_ERR_INVALID_ARG, and no count changes for it (fork looks at
  * the rows that are not taken exactly once, and copies entries as they are).  A
  * count that is too small but above 0 is not seen before it reaches 0, from where
- * on its page is free, whoever still names it.  All int32 arrays 4-byte aligned, workspaces 16-byte.
+ * on its page is free, whoever still names it.  All int32 arrays 4-byte aligned,
+ * workspaces 16-byte.
  * ------------------------------------------------------------------------ */
 bsa_status bsa_cache_fork(const bsa_cache_shape *shape, int32_t batch, int32_t batch_out, int32_t table_stride,
                           const int32_t *source, const int32_t *cached, const int32_t *block_table, int32_t *refs,
@@ -738,9 +752,12 @@ bsa_status bsa_cache_compact(const bsa_cache_shape *shape, int32_t batch, int32_
  * last token that has anything left).  Sums and what is left are integers in units of
  * 2^-60: what is smaller counts as nothing.  A row with nothing gives token 0.  Another root, a
  * parent that is not smaller than its token or an id outside the vocabulary (the last two set
- * BSA_ERR_INVALID_ARG in *dev_status) is not reached.  rank past cu_draft[batch] is left as it was.  Limits: max_draft <= 256
- * and <= total_draft, vocab <= 2^22, batch <= 65535, strides in elements, at least vocab and at most 2^30; p and q
- * aligned to their elements, the rest 4-byte.
+ * BSA_ERR_INVALID_ARG in *dev_status) is not reached.  A sequence of more than max_draft
+ * tokens, or whose offsets descend or leave 0 .. total_draft, sets BSA_ERR_INVALID_ARG and
+ * reads as one without drafts; its ranks, and rank past cu_draft[batch], are left as they
+ * were.  Limits: max_draft <= 256 and <= total_draft, vocab <= 2^22, batch <= 65535,
+ * strides in elements, at least vocab and at most 2^30; p and q aligned to their elements,
+ * the rest 4-byte.
  * ------------------------------------------------------------------------ */
 #define BSA_PROBS_F32 0
 #define BSA_PROBS_BF16 1
